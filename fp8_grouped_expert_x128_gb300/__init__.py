@@ -46,6 +46,9 @@ MOE_GEMM_EARLY_WEIGHTS = 0x20
 MOE_GEMM_DEBUG_STALL = 0x100
 MOE_QUANT_UE8M0 = 0x1
 MOE_COMBINE_ACCUMULATE = 0x1
+MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1
+MOE_KV_INTERLEAVED = 0x1
+MOE_KV_FULL = 0x1
 
 EXPORTED = [
     "moe_status_string", "moe_version", "moe_read_device_status", "moe_quant_fp8",
@@ -54,6 +57,7 @@ EXPORTED = [
     "moe_ffn_noalloc", "moe_ffn_noalloc_capacity", "moe_ffn_kernel_count", "moe_quant_fp8_ue8m0",
     "moe_ue8m0_scale", "moe_quant_weight_fp8_ue8m0", "moe_ue8m0_act_words", "moe_ue8m0_weight_words",
     "moe_pack_ue8m0_act", "moe_pack_ue8m0_weight", "moe_gemm_fp8_contig_ue8m0", "moe_gemm_fp8_masked_ue8m0",
+    "moe_kv_append", "moe_kv_attention", "moe_kv_attention_workspace_size",
 ]
 
 _P = ctypes.c_void_p
@@ -67,6 +71,33 @@ class moe_ffn_desc(ctypes.Structure):
         ("layout", _I32), ("max_m", _I32), ("expected_m", _I32), ("gemm_flags", _I32),
         ("x", _P), ("topk_ids", _P), ("topk_w", _P), ("w13", _P), ("w13_s", _P), ("w2", _P),
         ("w2_s", _P), ("out", _P), ("err", _P), ("stage_events", _P), ("w13_sf", _P), ("w2_sf", _P),
+    ]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("page_table", _P), ("cu_new", _P), ("kv_len", _P),
+        ("k_page_ld", _I64), ("k_head_ld", _I64), ("k_slot_ld", _I64), ("v_page_ld", _I64), ("v_head_ld", _I64),
+        ("v_slot_ld", _I64), ("table_ld", _I64), ("pages", _I64), ("batch", _I32), ("max_pages", _I32),
+        ("page_size", _I32), ("kv_heads", _I32), ("dim", _I32), ("dtype", _I32),
+    ]
+
+
+class moe_kv_append_desc(ctypes.Structure):
+    _fields_ = [
+        ("cache", moe_kv_cache), ("T", _I64), ("k", _P), ("v", _P), ("q", _P), ("q_out", _P), ("cos_sin", _P), ("err", _P),
+        ("k_token_ld", _I64), ("k_head_ld", _I64), ("v_token_ld", _I64), ("v_head_ld", _I64), ("q_token_ld", _I64),
+        ("q_head_ld", _I64), ("qo_token_ld", _I64), ("qo_head_ld", _I64), ("q_heads", _I32), ("rot_dim", _I32),
+        ("max_pos", _I32), ("flags", _I32),
+    ]
+
+
+class moe_kv_attention_desc(ctypes.Structure):
+    _fields_ = [
+        ("cache", moe_kv_cache), ("T", _I64), ("q", _P), ("out", _P), ("lse", _P), ("err", _P),
+        ("q_token_ld", _I64), ("q_head_ld", _I64), ("o_token_ld", _I64), ("o_head_ld", _I64),
+        ("sm_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("q_heads", _I32), ("max_q", _I32), ("window", _I32),
+        ("flags", _I32),
     ]
 
 
@@ -110,6 +141,9 @@ _sig("moe_ffn_kernel_count", ctypes.c_int, [ctypes.POINTER(moe_ffn_desc)])
 _sig("moe_ffn", ctypes.c_int, [ctypes.POINTER(moe_ffn_desc), _P, ctypes.c_size_t, _P])
 _sig("moe_ffn_noalloc", ctypes.c_int, [ctypes.POINTER(moe_ffn_desc), _P])
 _sig("moe_ffn_noalloc_capacity", ctypes.c_size_t, [])
+_sig("moe_kv_append", ctypes.c_int, [ctypes.POINTER(moe_kv_append_desc), _P])
+_sig("moe_kv_attention_workspace_size", ctypes.c_size_t, [ctypes.POINTER(moe_kv_attention_desc)])
+_sig("moe_kv_attention", ctypes.c_int, [ctypes.POINTER(moe_kv_attention_desc), _P, ctypes.c_size_t, _P])
 
 
 class MoeError(RuntimeError):
@@ -394,3 +428,131 @@ def alloc_workspace(desc: moe_ffn_desc, device=None) -> torch.Tensor:
     if n == 0:
         raise MoeError(MOE_ERR_INVALID_ARG, "moe_ffn_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+# ---------------------------------------------------------------- paged 8-bit key/value cache
+_KV_TYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+
+
+def _kv_rows(t, name, T, heads, dim, dtype, device):
+    """Strides (token, head) of a [T, heads, dim] tensor of the step's rows."""
+    if t.shape != (T, heads, dim) or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name}: expected {dtype} [{T}, {heads}, {dim}] on the cache's GPU, got {t.dtype} {list(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.numel():
+        raise ValueError(f"{name}: the elements of a row must be next to each other")
+    return st, sh
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype):
+    """The cache part of a descriptor, as a tuple in the order of its fields."""
+    pages, heads, page, dim = k_cache.shape
+    device = k_cache.get_device()
+    if device < 0:
+        raise ValueError("k_cache must be a CUDA tensor")
+    if v_cache.shape != k_cache.shape or k_cache.dtype not in _U8 or v_cache.dtype not in _U8:
+        raise ValueError("k_cache and v_cache: expected uint8 or float8_e4m3fn [pages, kv_heads, page_size, dim]")
+    kp, kh, ks, kd = k_cache.stride()
+    vp, vh, vs, vd = v_cache.stride()
+    if kd != 1 or vd != 1:
+        raise ValueError("k_cache, v_cache: the elements of a row must be next to each other")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.shape != (pages, heads) or t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous float32 [{pages}, {heads}]")
+    batch, max_pages = page_table.shape
+    if page_table.dtype != torch.int32 or (max_pages > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table: expected int32 [batch, max_pages], rows contiguous")
+    if (cu_new.shape != (batch + 1,) or kv_len.shape != (batch,) or cu_new.dtype != torch.int32
+            or kv_len.dtype != torch.int32 or not cu_new.is_contiguous() or not kv_len.is_contiguous()):
+        raise ValueError(f"cu_new, kv_len: expected contiguous int32 [{batch + 1}] and [{batch}]")
+    if dtype not in _KV_TYPES:
+        raise ValueError(f"token tensors: expected bfloat16 or float16, got {dtype}")
+    for t, name in ((v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"), (page_table, "page_table"),
+                    (cu_new, "cu_new"), (kv_len, "kv_len")):
+        if t.get_device() != device:
+            raise ValueError(f"{name}: not on the GPU that holds k_cache")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+            cu_new.data_ptr(), kv_len.data_ptr(), kp, kh, ks, vp, vh, vs, page_table.stride(0), pages, batch, max_pages,
+            page, heads, dim, _KV_TYPES[dtype])
+
+
+def _kv_err(err, device):
+    if err is None:
+        return None
+    if err.dtype != torch.int32 or err.get_device() != device:
+        raise ValueError("err: expected an int32 word on the cache's GPU (new_error_word)")
+    return err.data_ptr()
+
+
+def moe_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, cos_sin=None, flags=0, q=None,
+                  q_out=None, err=None, stream=None):
+    """Append the step's keys and values k, v [T, kv_heads, dim] (bf16 or f16, any
+    token and head strides) to the paged E4M3 cache k_cache, v_cache [pages,
+    kv_heads, page_size, dim] (any strides but the last) with scales k_scale,
+    v_scale fp32 [pages, kv_heads]; see moe_fp8.h for the rule.  Sequence b's new
+    tokens are rows cu_new[b] .. cu_new[b + 1] - 1, the last of its kv_len[b].
+    cos_sin fp32 [max_pos, rot_dim] rotates the keys, and q [T, q_heads, dim] into
+    q_out (which may be q); flags = MOE_KV_INTERLEAVED for adjacent pairs."""
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, k.dtype)
+    device, heads, dim, T = k_cache.get_device(), k_cache.shape[1], k_cache.shape[3], k.shape[0]
+    kl = _kv_rows(k, "k", T, heads, dim, k.dtype, device)
+    vl = _kv_rows(v, "v", T, heads, dim, k.dtype, device)
+    ql = ol = (0, 0)
+    q_heads = max_pos = rot = 0
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q_out: queries need a tensor to be written to")
+        q_heads = q.shape[1]
+        ql = _kv_rows(q, "q", T, q_heads, dim, k.dtype, device)
+        ol = _kv_rows(q_out, "q_out", T, q_heads, dim, k.dtype, device)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != device:
+            raise ValueError("cos_sin: expected contiguous float32 [max_pos, rot_dim] on the cache's GPU")
+        max_pos, rot = cos_sin.shape
+    d = moe_kv_append_desc(c, T, k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None,
+                           q_out.data_ptr() if q is not None else None, cos_sin.data_ptr() if rot else None,
+                           _kv_err(err, device), *kl, *vl, *ql, *ol, q_heads, rot, max_pos, flags)
+    _check(_lib.moe_kv_append(ctypes.byref(d), _stream(stream)), "moe_kv_append")
+
+
+def make_kv_attention_desc(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q=0, window=0,
+                           softcap=0.0, flags=0, lse=None, err=None):
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, q.dtype)
+    device, dim = k_cache.get_device(), k_cache.shape[3]
+    T, heads = q.shape[0], q.shape[1]
+    qs = _kv_rows(q, "q", T, heads, dim, q.dtype, device)
+    os_ = _kv_rows(out, "out", T, heads, dim, q.dtype, device)
+    if lse is not None and (lse.shape != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous()
+                            or lse.get_device() != device):
+        raise ValueError(f"lse: expected contiguous float32 [{T}, {heads}] on the cache's GPU")
+    return moe_kv_attention_desc(c, T, q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                                 _kv_err(err, device), *qs, *os_, sm_scale, softcap, heads, max_q, window, flags)
+
+
+def moe_kv_attention_workspace_size(desc: moe_kv_attention_desc) -> int:
+    return int(_lib.moe_kv_attention_workspace_size(ctypes.byref(desc)))
+
+
+def moe_kv_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, workspace, sm_scale, max_q=0,
+                     window=0, softcap=0.0, flags=0, lse=None, err=None, stream=None):
+    """Attention of the step's queries q [T, q_heads, dim] over the paged cache
+    (arguments as in moe_kv_append) into out; see moe_fp8.h for the definition.
+    max_q: the largest number of new tokens of a sequence (0 = not known).
+    workspace: a uint8 device tensor of at least moe_kv_attention_workspace_size
+    bytes, zeroed once before its first use.  lse: optional fp32 [T, q_heads]."""
+    d = make_kv_attention_desc(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q, window,
+                               softcap, flags, lse, err)
+    if workspace.get_device() != q.get_device():
+        raise ValueError("workspace: not on the cache's GPU")
+    _check(_lib.moe_kv_attention(ctypes.byref(d), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 _stream(stream)), "moe_kv_attention")
+    return out
+
+
+def alloc_kv_workspace(desc: moe_kv_attention_desc, device=None) -> torch.Tensor:
+    n = moe_kv_attention_workspace_size(desc)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_kv_attention_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")

@@ -172,7 +172,7 @@ extern "C" const char* moe_status_string(int status) {
   }
 }
 
-extern "C" int moe_version(void) { return 200; }
+extern "C" int moe_version(void) { return 201; }
 
 extern "C" int moe_read_device_status(int32_t* err, void* stream, int* status_out,
                                       int32_t* raw_bits_out) {

@@ -1,0 +1,324 @@
+// Appending a step's keys and values to the paged 8-bit cache, with the position
+// rotation of keys and queries on the way.
+//
+// Per page, head and K or V: s' = the power-of-two scale of the page's new
+// tokens (and of what the page held before), q = e4m3(x / s').  The maximum has
+// to be known before the first code is written, so a CTA takes one page and one
+// of K or V, keeps the page's rotated rows in registers (fp32, 16 values a
+// thread and row), takes the maximum over the CTA and then writes the codes: the
+// inputs are read once.  It walks over several heads, so that a row's cosines and
+// sines (as many bytes as the row has in 16 bits) are loaded once for all of
+// them.  Query rows need no maximum; further CTAs of the same launch rotate them.
+#include "kv_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kQHeadsPerCta = 8;   // query heads one thread rotates with the same angles
+
+struct AppendArgs {
+  moe_kv_append_desc d;
+  int32_t units;        // page units: floor(T / page_size) + 2 * batch
+  int32_t head_groups;  // CTAs per unit and kind
+  int32_t heads_per;    // kv heads per CTA
+  int32_t kv_ctas;      // units * 2 * head_groups
+  int32_t q_groups;     // CTAs per run of query rows
+};
+
+// A thread's 16 dimensions of a row: two runs of 8.  Where dimensions (i, i +
+// rot / 2) turn together the runs are rot / 2 apart, so that both ends of a pair
+// are in one thread; else they are neighbours.
+__device__ __forceinline__ void group_runs(int g, int rot, bool interleaved, int& a, int& b) {
+  const int rg = rot >> 4;
+  if (!interleaved && g < rg) {
+    a = 8 * g;
+    b = 8 * (g + rg);
+  } else {
+    a = 16 * g;
+    b = 16 * g + 8;
+  }
+}
+
+__device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
+  const float4 u = __ldg(reinterpret_cast<const float4*>(p)), v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
+  f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+}
+
+__device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (&c)[8], const float (&s)[8],
+                                     bool interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = a * c[i] - b * s[i];
+      x[2 * i + 1] = b * c[i] + a * s[i];
+      a = y[2 * i], b = y[2 * i + 1];
+      y[2 * i] = a * c[4 + i] - b * s[4 + i];
+      y[2 * i + 1] = b * c[4 + i] + a * s[4 + i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[i], b = y[i];
+      x[i] = a * c[i] - b * s[i];
+      y[i] = b * c[i] + a * s[i];
+    }
+  }
+}
+
+// |x| where x is finite, else 0: what counts toward a page's maximum.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.0f;
+}
+
+// e4m3(x / s): a product with the exact reciprocal where s is a power of two.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, bool pow2) {
+  float q[8];
+  const float r = pow2 ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = pow2 ? x[i] * r : __fdiv_rn(x[i], s);
+  return pack_e4m3x8(q);
+}
+
+template <bool F16, int D, int TT>
+__device__ void rotate_queries(const AppendArgs& a, int cta) {
+  const moe_kv_append_desc& d = a.d;
+  constexpr int kGroups = D / 16;
+  constexpr int kRows = TT / kGroups;
+  const int t = cta / a.q_groups * kRows + threadIdx.x / kGroups;
+  const int t_warp = min(t, static_cast<int>(d.T) - 1);
+  const int g = threadIdx.x % kGroups;
+  const int h0 = cta % a.q_groups * kQHeadsPerCta;
+  const int h1 = min(h0 + kQHeadsPerCta, d.q_heads);
+  // the lanes of a warp hold different rows: each searches for its own
+  int lo = 0, hi = d.cache.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(d.cache.cu_new + mid) <= t_warp) lo = mid; else hi = mid;
+  }
+  const int c0 = __ldg(d.cache.cu_new + lo), c1 = __ldg(d.cache.cu_new + lo + 1);
+  if (t >= d.T || t < c0 || t >= c1 || c1 > d.T) return;
+  const int pos = __ldg(d.cache.kv_len + lo) - (c1 - t);
+  if (pos < 0 || (d.rot_dim && pos >= d.max_pos)) {
+    set_err(d.err, MOE_DEV_BAD_INDEX);
+    return;
+  }
+  const bool inter = (d.flags & MOE_KV_INTERLEAVED) != 0;
+  const bool turned = g < (d.rot_dim >> 4);
+  int ra, rb;
+  group_runs(g, d.rot_dim, inter, ra, rb);
+  float c[8], s[8];
+  if (turned) {
+    const float* cs = d.cos_sin + static_cast<int64_t>(pos) * d.rot_dim + 8 * g;
+    load8f(cs, c);
+    load8f(cs + (d.rot_dim >> 1), s);
+  }
+  const uint16_t* q = static_cast<const uint16_t*>(d.q) + t * d.q_token_ld;
+  uint16_t* o = static_cast<uint16_t*>(d.q_out) + t * d.qo_token_ld;
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const uint4 u = *reinterpret_cast<const uint4*>(q + h * d.q_head_ld + ra);
+    const uint4 v = *reinterpret_cast<const uint4*>(q + h * d.q_head_ld + rb);
+    uint4 uo = u, vo = v;
+    if (turned) {
+      float x[8], y[8];
+      unpack8<F16>(u, x);
+      unpack8<F16>(v, y);
+      turn(x, y, c, s, inter);
+      uo = pack8<F16>(x);
+      vo = pack8<F16>(y);
+    }
+    *reinterpret_cast<uint4*>(o + h * d.qo_head_ld + ra) = uo;
+    *reinterpret_cast<uint4*>(o + h * d.qo_head_ld + rb) = vo;
+  }
+}
+
+template <bool F16, int D, int TT, int R>
+__global__ void __launch_bounds__(TT) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ uint32_t red[2][TT / 32];
+  const moe_kv_append_desc& d = a.d;
+  const moe_kv_cache& kc = d.cache;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= a.kv_ctas) {
+    rotate_queries<F16, D, TT>(a, blockIdx.x - a.kv_ctas);
+    return;
+  }
+  constexpr int kGroups = D / 16;
+  const int P = kc.page_size;
+  const int hg = blockIdx.x % a.head_groups;
+  const bool is_v = (blockIdx.x / a.head_groups) & 1;
+  const int unit = blockIdx.x / (2 * a.head_groups);
+  // Units are numbered so that sequence b's start at cu[b] / P + 2b: as many as
+  // it can need wherever its first token falls in a page, with no prefix sum.
+  const int b = warp_find(kc.batch, unit, [&](int i) { return __ldg(kc.cu_new + i) / P + 2 * i; });
+  const int c0 = __ldg(kc.cu_new + b), c1 = __ldg(kc.cu_new + b + 1), len = __ldg(kc.kv_len + b);
+  const int n = c1 - c0;
+  if (n == 0) return;
+  if (c0 < 0 || n < 0 || c1 > d.T || len < n) {
+    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
+    return;
+  }
+  const int pos0 = len - n;                                  // position of the sequence's first new token
+  const int nth = unit - (c0 / P + 2 * b);                   // of the pages the new tokens fall on
+  const int pi = pos0 / P + nth;
+  if (nth < 0 || pi > (len - 1) / P) return;
+  if (pi >= kc.max_pages) {
+    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_OVERFLOW);
+    return;
+  }
+  const int page = __ldg(kc.page_table + b * kc.table_ld + pi);
+  const int s0 = max(pos0 - pi * P, 0), s1 = min(len - pi * P, P);   // slots of the new tokens
+  if (page < 0 || page >= kc.pages || (d.rot_dim && pi * P + s1 > d.max_pos)) {
+    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
+    return;
+  }
+  const int64_t row0 = c0 + (pi * P - pos0);                 // token row of slot 0
+  const uint16_t* src = static_cast<const uint16_t*>(is_v ? d.v : d.k);
+  const int64_t src_tld = is_v ? d.v_token_ld : d.k_token_ld, src_hld = is_v ? d.v_head_ld : d.k_head_ld;
+  uint8_t* dst = (is_v ? kc.v + page * kc.v_page_ld : kc.k + page * kc.k_page_ld);
+  const int64_t dst_hld = is_v ? kc.v_head_ld : kc.k_head_ld, dst_sld = is_v ? kc.v_slot_ld : kc.k_slot_ld;
+  float* scale = (is_v ? kc.v_scale : kc.k_scale) + static_cast<int64_t>(page) * kc.kv_heads;
+  const int rot = is_v ? 0 : d.rot_dim;
+  const bool inter = (d.flags & MOE_KV_INTERLEAVED) != 0;
+  const int h0 = hg * a.heads_per, h1 = min(h0 + a.heads_per, kc.kv_heads);
+
+  for (int h = h0; h < h1; ++h) {
+    float x[R][8], y[R][8];
+    float amax = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int item = threadIdx.x + r * TT;
+      const int slot = item / kGroups, g = item % kGroups;
+      if (slot < s0 || slot >= s1) continue;
+      int ra, rb;
+      group_runs(g, rot, inter, ra, rb);
+      const uint16_t* p = src + (row0 + slot) * src_tld + h * src_hld;
+      unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(p + ra)), x[r]);
+      unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(p + rb)), y[r]);
+      if (g < (rot >> 4)) {
+        float c[8], s[8];
+        const float* cs = d.cos_sin + static_cast<int64_t>(pi * P + slot) * rot + 8 * g;
+        load8f(cs, c);
+        load8f(cs + (rot >> 1), s);
+        turn(x[r], y[r], c, s, inter);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_abs(x[r][i]), finite_abs(y[r][i])));
+    }
+    const float before = scale[h];
+    // floats that are not negative order as their bit patterns do
+    const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+    uint32_t* slot_red = red[h & 1];
+    if ((threadIdx.x & 31) == 0) slot_red[threadIdx.x >> 5] = wmax;
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (int w = 0; w < TT / 32; ++w) all = max(all, slot_red[w]);
+    uint8_t byte;
+    float s = block_scale_ue8m0(__uint_as_float(all), &byte);
+    const bool grown = s0 > 0 && s > before;
+    if (s0 > 0 && !grown) s = before;
+    const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+    uint8_t* out = dst + h * dst_hld;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int item = threadIdx.x + r * TT;
+      const int slot = item / kGroups, g = item % kGroups;
+      if (slot < s0 || slot >= s1) continue;
+      int ra, rb;
+      group_runs(g, rot, inter, ra, rb);
+      uint8_t* o = out + slot * dst_sld;
+      *reinterpret_cast<uint2*>(o + ra) = codes8(x[r], s, pow2);
+      *reinterpret_cast<uint2*>(o + rb) = codes8(y[r], s, pow2);
+    }
+    if (grown) {
+      // the slots that were there take the page's new scale
+      for (int item = threadIdx.x; item < s0 * kGroups; item += TT) {
+        uint4* o = reinterpret_cast<uint4*>(out + item / kGroups * dst_sld + 16 * (item % kGroups));
+        const uint4 u = *o;
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint2 q[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t p = e4m3x2_to_f16x2(static_cast<uint16_t>(w[2 * half + (i >> 1)] >> (16 * (i & 1))));
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p));
+            f[2 * i] = v.x * before;
+            f[2 * i + 1] = v.y * before;
+          }
+          q[half] = codes8(f, s, pow2);
+        }
+        *o = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+      }
+    }
+    // every thread read the old scale before the barrier above
+    if (threadIdx.x == 0) scale[h] = s;
+  }
+}
+
+template <bool F16, int D, int TT, int R>
+int launch_append(AppendArgs& a, cudaStream_t st) {
+  const moe_kv_append_desc& d = a.d;
+  a.units = static_cast<int32_t>(d.T / d.cache.page_size) + 2 * d.cache.batch;
+  a.heads_per = 1;
+  a.head_groups = d.cache.kv_heads;
+  const int64_t kv = static_cast<int64_t>(a.units) * 2 * a.head_groups;
+  a.q_groups = (d.q_heads + kQHeadsPerCta - 1) / kQHeadsPerCta;
+  constexpr int kRows = TT / (D / 16);
+  const int64_t qc = d.q ? (d.T + kRows - 1) / kRows * a.q_groups : 0;
+  if (kv + qc > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  a.kv_ctas = static_cast<int32_t>(kv);
+  return launch_pdl(kv_append_kernel<F16, D, TT, R>, dim3(static_cast<unsigned>(kv + qc)), dim3(TT), 0, st, a);
+}
+
+// One thread holds 16 values of a row, so a page takes page_size * dim / 16
+// threads; above 256 a thread holds 2 or 4 rows.
+template <bool F16>
+int pick_append(AppendArgs& a, cudaStream_t st) {
+  const int P = a.d.cache.page_size;
+  if (a.d.cache.dim == 64) {
+    if (P == 16) return launch_append<F16, 64, 64, 1>(a, st);
+    if (P == 32) return launch_append<F16, 64, 128, 1>(a, st);
+    if (P == 64) return launch_append<F16, 64, 256, 1>(a, st);
+    return launch_append<F16, 64, 256, 2>(a, st);
+  }
+  if (P == 16) return launch_append<F16, 128, 128, 1>(a, st);
+  if (P == 32) return launch_append<F16, 128, 256, 1>(a, st);
+  if (P == 64) return launch_append<F16, 128, 256, 2>(a, st);
+  return launch_append<F16, 128, 256, 4>(a, st);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_kv_append(const moe_kv_append_desc* d, void* stream) {
+  MOE_CHECK_ARG(d != nullptr);
+  if (int rc = check_kv_cache(d->cache, d->T)) return rc;
+  MOE_CHECK_ARG((d->flags & ~MOE_KV_INTERLEAVED) == 0);
+  MOE_CHECK_ARG(d->rot_dim >= 0 && d->rot_dim <= d->cache.dim && d->rot_dim % 16 == 0 && d->max_pos >= 0);
+  MOE_CHECK_ARG(kv_strides_ok(d->k_token_ld, d->k_head_ld, d->v_token_ld, 8) &&
+                kv_strides_ok(d->v_head_ld, d->q_token_ld, d->q_head_ld, 8) &&
+                kv_strides_ok(d->qo_token_ld, d->qo_head_ld, 0, 8));
+  if (d->T == 0 || d->cache.batch == 0) return MOE_OK;
+  MOE_CHECK_ARG(d->k && d->v && aligned16(d->k) && aligned16(d->v));
+  MOE_CHECK_ARG(d->rot_dim == 0 || (d->cos_sin && aligned16(d->cos_sin)));
+  if (d->q != nullptr) {
+    MOE_CHECK_ARG(d->q_out && aligned16(d->q) && aligned16(d->q_out));
+    MOE_CHECK_ARG(d->q_heads >= 1);
+    if (d->q_heads > 65536) return MOE_ERR_UNSUPPORTED;
+  } else {
+    MOE_CHECK_ARG(d->q_heads == 0 && d->q_out == nullptr);
+  }
+  if (int rc = check_device()) return rc;
+  AppendArgs a{};
+  a.d = *d;
+  return d->cache.dtype == MOE_DTYPE_F16 ? pick_append<true>(a, as_stream(stream))
+                                         : pick_append<false>(a, as_stream(stream));
+}

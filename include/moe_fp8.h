@@ -452,6 +452,137 @@ int moe_ffn(const moe_ffn_desc *desc, void *workspace, size_t workspace_bytes, v
 size_t moe_ffn_noalloc_capacity(void);
 int moe_ffn_noalloc(const moe_ffn_desc *desc, void *stream);
 
+/*
+ * The attention half of a decoder layer in serving: a paged key/value cache in
+ * 8 bits, the call that appends to it, and the attention that reads it.
+ *
+ * The cache.  K and V are E4M3 codes in pages of page_size tokens.  Element
+ * (page, head, slot, d) of K sits at k[page * k_page_ld + head * k_head_ld +
+ * slot * k_slot_ld + d] (V likewise), so head-major and token-major pages, and
+ * slices of a larger allocation, are all the same call.  One fp32 scale for
+ * each page and head: the value of a code q is scale * e4m3(q).  Sequence b
+ * owns the pages page_table[b * table_ld + i], i = 0 .. ceil(kv_len[b] /
+ * page_size) - 1; entries past those are never read.  Its new tokens (the rows
+ * of this step) are rows cu_new[b] .. cu_new[b + 1] - 1 of the token tensors;
+ * they are the last n = cu_new[b + 1] - cu_new[b] of its kv_len[b] tokens, so
+ * new token i has position kv_len[b] - n + i.  n may be 0.
+ *
+ * Limits: dim 64 or 128; page_size 16, 32, 64 or 128; strides in bytes,
+ * multiples of 16, not negative; q_heads a multiple of kv_heads; page, row and
+ * head offsets are 64-bit.  Device-side faults of the descriptors set bits in
+ * `err` and skip what they touch: a sequence that does not lie in the token
+ * rows (cu_new decreasing, negative or past T), that is shorter than its new
+ * tokens, or that has a page id outside [0, pages) -- MOE_DEV_BAD_INDEX; more
+ * pages than max_pages -- MOE_DEV_OVERFLOW.
+ */
+#define MOE_DTYPE_BF16 0              /* element types of q, k, v and out */
+#define MOE_DTYPE_F16 1
+
+typedef struct moe_kv_cache {
+  uint8_t *k;                 /* device, codes                              */
+  uint8_t *v;
+  float *k_scale;             /* device fp32 [pages, kv_heads]              */
+  float *v_scale;
+  const int32_t *page_table;  /* device int32 [batch, max_pages]            */
+  const int32_t *cu_new;      /* device int32 [batch + 1]                   */
+  const int32_t *kv_len;      /* device int32 [batch], new tokens included  */
+  int64_t k_page_ld, k_head_ld, k_slot_ld;   /* bytes */
+  int64_t v_page_ld, v_head_ld, v_slot_ld;   /* bytes */
+  int64_t table_ld;           /* elements between rows of page_table        */
+  int64_t pages;              /* pages of the cache                         */
+  int32_t batch, max_pages, page_size, kv_heads, dim;
+  int32_t dtype;              /* MOE_DTYPE_* of the token tensors           */
+} moe_kv_cache;
+
+/*
+ * moe_kv_append -- write the step's keys and values into the cache, the keys
+ * (and, with q given, the queries) rotated by position on the way.
+ * Rotation of a row x at position p (rot_dim > 0): the first rot_dim dimensions
+ * are pairs (a, b) -- dimensions (i, i + rot_dim / 2), or (2i, 2i + 1) with
+ * MOE_KV_INTERLEAVED -- turned in fp32 to (a cos - b sin, b cos + a sin) with
+ * cos = cos_sin[p * rot_dim + i], sin = cos_sin[p * rot_dim + rot_dim / 2 + i],
+ * i < rot_dim / 2; the other dimensions stay.
+ * Per page that new tokens fall on, head, and K or V, with amax the largest
+ * finite |x| over those tokens (after the rotation):
+ *   need = the power-of-two scale of moe_quant_fp8_ue8m0 for amax
+ *   s'   = need               if the page's first slot is among the new tokens
+ *        = max(s, need)       else; s' replaces the page's scale s
+ *   new tokens:   q  = e4m3_rne_satfinite(x / s')  (+-inf -> +-448, NaN -> 0x7F)
+ *   slots before: q' = e4m3_rne_satfinite(s * e4m3(q) / s')  where s' > s
+ * Scales that are powers of two (as this call writes them) make both divisions
+ * exact, so a token loses only what falls under a larger scale's subnormals.
+ * Slots past the new tokens are not touched.  A page that several sequences
+ * share must not be appended to.
+ * k, v, q, q_out: device rows of dim elements (dtype of the cache descriptor);
+ * row (t, head) at t * *_token_ld + head * *_head_ld elements, both multiples
+ * of 8.  q may be NULL (then q_heads = 0); q_out may be q itself.
+ * cos_sin: device fp32 [max_pos, rot_dim]; rot_dim a multiple of 16, 0 .. dim
+ * (0: no rotation, cos_sin may be NULL).  A page with a position at or past
+ * max_pos is skipped whole, and such a q row too, with MOE_DEV_BAD_INDEX.
+ * T may be 0 (nothing is launched).
+ */
+#define MOE_KV_INTERLEAVED 0x1
+
+typedef struct moe_kv_append_desc {
+  moe_kv_cache cache;
+  int64_t T;                  /* rows of k, v and q                         */
+  const void *k;
+  const void *v;
+  const void *q;              /* or NULL                                    */
+  void *q_out;
+  const float *cos_sin;
+  int32_t *err;
+  int64_t k_token_ld, k_head_ld, v_token_ld, v_head_ld;          /* elements */
+  int64_t q_token_ld, q_head_ld, qo_token_ld, qo_head_ld;
+  int32_t q_heads, rot_dim, max_pos, flags;
+} moe_kv_append_desc;
+
+int moe_kv_append(const moe_kv_append_desc *desc, void *stream);
+
+/*
+ * moe_kv_attention -- the step's queries attend over the cache.
+ * For new token i of sequence b at position p, query head hq, kv head
+ * h = hq / (q_heads / kv_heads):
+ *   score_j = sm_scale * sum_d q[d] * K[j, h, d]
+ *   score_j = softcap * tanh(score_j / softcap)                if softcap > 0
+ *   visible: 0 <= j < kv_len[b]; j <= p unless MOE_KV_FULL; j > p - window if
+ *            window > 0 (not together with MOE_KV_FULL)
+ *   out = sum_j softmax_j(score) V[j, h, :],  lse = log sum_j exp(score_j)
+ * over the visible j; a row that sees nothing gives out = 0 and lse = -inf.
+ * Codes that are not visible to a row, whatever they hold (NaN too), do not
+ * reach it; a visible NaN does.
+ * Arithmetic: the products run on the tensor cores on f16 operands with fp32
+ * sums.  E4M3 codes are exact in f16; a q row is first scaled by a power of two
+ * that takes its largest element into [1, 2), so bf16 rows fit (elements below
+ * 2^-14 of the largest lose bits below 2^-24 of it).  Scores, softmax statistics
+ * and outputs are held in fp32; the softmax weights are rounded to f16 for the
+ * second product, and out once to its type.  Scales must be positive, finite.
+ * q, out: device rows as in moe_kv_append; lse: device fp32 [T, q_heads] or NULL.
+ * max_q: no sequence has more new tokens than this (0 = T): a hint that picks
+ * the kernels; a sequence with more is skipped with MOE_DEV_OVERFLOW.
+ * workspace: device, moe_kv_attention_workspace_size(desc) bytes (0 for a bad
+ * descriptor), 256-byte aligned.  It has to be zero before its first use and
+ * may then be used for any number of calls one after another, of any sizes that
+ * it has room for; calls that overlap on the GPU need one each.
+ * T may be 0 (nothing is launched).
+ */
+#define MOE_KV_FULL 0x1
+
+typedef struct moe_kv_attention_desc {
+  moe_kv_cache cache;
+  int64_t T;                  /* rows of q and out                          */
+  const void *q;
+  void *out;
+  float *lse;                 /* or NULL                                    */
+  int32_t *err;
+  int64_t q_token_ld, q_head_ld, o_token_ld, o_head_ld;          /* elements */
+  float sm_scale, softcap;
+  int32_t q_heads, max_q, window, flags;
+} moe_kv_attention_desc;
+
+size_t moe_kv_attention_workspace_size(const moe_kv_attention_desc *desc);
+int moe_kv_attention(const moe_kv_attention_desc *desc, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
