@@ -169,6 +169,11 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _stream_of(device: int, stream=None) -> int:
+    """The handle of `stream`, or of the current stream of GPU `device`."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
 def _check(rc: int, where: str):
     if rc != MOE_OK:
         raise MoeError(rc, where)
@@ -514,7 +519,7 @@ def moe_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, 
     d = moe_kv_append_desc(c, T, k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None,
                            q_out.data_ptr() if q is not None else None, cos_sin.data_ptr() if rot else None,
                            _kv_err(err, device), *kl, *vl, *ql, *ol, q_heads, rot, max_pos, flags)
-    _check(_lib.moe_kv_append(ctypes.byref(d), _stream(stream)), "moe_kv_append")
+    _check(_lib.moe_kv_append(ctypes.byref(d), _stream_of(device, stream)), "moe_kv_append")
 
 
 def make_kv_attention_desc(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q=0, window=0,
@@ -544,10 +549,11 @@ def moe_kv_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, 
     bytes, zeroed once before its first use.  lse: optional fp32 [T, q_heads]."""
     d = make_kv_attention_desc(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q, window,
                                softcap, flags, lse, err)
-    if workspace.get_device() != q.get_device():
+    device = q.get_device()
+    if workspace.get_device() != device:
         raise ValueError("workspace: not on the cache's GPU")
     _check(_lib.moe_kv_attention(ctypes.byref(d), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 _stream(stream)), "moe_kv_attention")
+                                 _stream_of(device, stream)), "moe_kv_attention")
     return out
 
 

@@ -2,14 +2,10 @@
 //
 // One warp per (token, query head): the lanes split the head's dimensions, a
 // score is a warp sum, and the softmax runs online (running maximum and sum).
-#include <float.h>
-
-#include "kv_common.cuh"
+#include "kv_attention.cuh"
 
 namespace moe {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 // cap * tanh(x / cap) in fp32: tanh(y) = 1 - 2 / (exp(2y) + 1).
 __device__ __forceinline__ float capped(float x, float cap) {
@@ -30,6 +26,7 @@ __global__ void __launch_bounds__(128) kv_attention_kernel(const __grid_constant
   const int b = warp_find(kc.batch, t, [&](int i) { return __ldg(kc.cu_new + i); });
   const int c0 = __ldg(kc.cu_new + b), c1 = __ldg(kc.cu_new + b + 1), len = __ldg(kc.kv_len + b);
   if (t < c0 || t >= c1) return;
+  if ((c1 - c0) * (d.q_heads / kc.kv_heads) <= kDecodeRows) return;
   const int P = kc.page_size, h = hq / (d.q_heads / kc.kv_heads);
   if (c0 < 0 || c1 > d.T || len < c1 - c0) {
     if (lane == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
@@ -111,7 +108,7 @@ int check_attention(const moe_kv_attention_desc* d) {
 using namespace moe;
 
 extern "C" size_t moe_kv_attention_workspace_size(const moe_kv_attention_desc* d) {
-  return check_attention(d) == MOE_OK ? 256 : 0;
+  return check_attention(d) == MOE_OK ? kv_decode_workspace() : 0;
 }
 
 extern "C" int moe_kv_attention(const moe_kv_attention_desc* d, void* workspace, size_t workspace_bytes, void* stream) {
@@ -121,6 +118,14 @@ extern "C" int moe_kv_attention(const moe_kv_attention_desc* d, void* workspace,
   MOE_CHECK_ARG(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255) == 0);
   MOE_CHECK_ARG(workspace_bytes >= moe_kv_attention_workspace_size(d));
   if (int rc = check_device()) return rc;
+  AttnArgs a{};
+  a.d = *d;
+  a.G = d->q_heads / d->cache.kv_heads;
+  a.counters = static_cast<int32_t*>(workspace);
+  a.parts = reinterpret_cast<float*>(a.counters + kDecodeCounters);
+  const int64_t max_rows = (d->max_q ? static_cast<int64_t>(d->max_q) : d->T) * a.G;
+  if (int rc = kv_decode_launch(a, max_rows, as_stream(stream))) return rc;
+  if (max_rows <= kDecodeRows) return MOE_OK;
   const dim3 grid(static_cast<unsigned>((d->T * d->q_heads + 3) / 4));
   cudaStream_t st = as_stream(stream);
   const bool f16 = d->cache.dtype == MOE_DTYPE_F16;

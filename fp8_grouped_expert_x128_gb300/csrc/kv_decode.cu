@@ -1,0 +1,642 @@
+// Attention over the paged 8-bit cache for few rows per kv head (decode steps
+// and draft tokens): memory bound, 2 * dim bytes for each key token and kv head.
+//
+// The keys of every (sequence, kv head) are cut into 64-token tiles; the tiles of
+// all of them, in order, are split evenly over the CTAs of one resident wave, so
+// lengths that differ and few sequences both keep all SMs loading.  A (sequence,
+// kv head) that several CTAs share is joined by the last of them to finish, from
+// the running maximum, sum and unnormalised output that each has left in the
+// workspace; parts are added in the order of their keys, so results repeat bit
+// for bit whichever CTA comes last.  More than 16 parts are joined in two levels.
+//
+// A warp takes 16 keys of a tile through a cp.async ring of its own (no barrier
+// inside a CTA's loop).  Both products run transposed on mma.m16n8k16 f16, S^T =
+// K Q^T and O^T = V^T P^T, with the rows as the n side: 8 rows cost no padding to
+// 16, and K fragments are read straight from shared memory, the head's dimensions
+// taken in the order in which a lane's bytes lie (Q is put in the same order).
+// E4M3 widens exactly to f16 in one instruction per pair.  The V scale rides in
+// the weight: w = exp2(s + log2 s_V - m), the sum takes w / s_V.
+#include "kv_attention.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStep = 16;                 // keys a warp takes at a time
+constexpr int kTile = kStep * kWarps;
+constexpr int kCtasPerSm = 2;
+constexpr int kGroup = 16;                // parts joined at a time
+constexpr int kMaxParts = 1024;           // CTAs of a launch at most
+static_assert(3 * kMaxParts == kDecodeCounters, "counters of the three levels");
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kStages = D == 128 ? (NT == 4 ? 5 : 6) : 8;
+  static constexpr int kStageBytes = 2 * kStep * D;       // K, then V
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kLd = D + 4;                       // merge buffer row, padded against bank conflicts
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kScales = kRing;                   // [warp][stage][2] floats
+  static constexpr int kBuf = kScales + kWarps * kStages * 8;
+  static constexpr int kSmem = kBuf + kRows * kLd * 4;
+};
+constexpr int kPartFloats = kDecodeRows * (128 + 2);      // one part: m[32], l[32], O[32][dim]
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk ch of key row r in a stage: chunks are swapped
+// around within 128 bytes so that both the fragment loads of K (a lane's own
+// bytes of 8 rows) and the transposing loads of V (one chunk of 8 rows) touch
+// every bank once.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
+  if constexpr (D == 128) {
+    return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4));
+  } else {
+    return static_cast<uint32_t>((r >> 1) * 128 + (((((r & 1) << 2) | ch) ^ ((r >> 1) & 7)) << 4));
+  }
+}
+
+// Tiles of a sequence's keys: from the one with the first key its first row sees.
+struct Tiles {
+  int first, count;
+};
+__device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, const Seq& s, int rows_max) {
+  Tiles t{0, 0};
+  if (s.n == 0 || s.n * a.G > rows_max) return t;
+  t.first = first_key(a.d, s, 0) / kTile;
+  t.count = (s.len + kTile - 1) / kTile - t.first;
+  return t;
+}
+
+// First unit of CTA c when W units are split over C CTAs.
+__device__ __forceinline__ int64_t range_start(int64_t W, int c, int C) { return W * c / C; }
+// The CTA that owns unit u: the largest c with range_start(c) <= u.
+__device__ __forceinline__ int owner(int64_t u, int64_t W, int C) {
+  return static_cast<int>(((u + 1) * C + W - 1) / W) - 1;
+}
+
+template <bool F16, int D, int NT>
+__global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_constant__ AttnArgs a) {
+  using C = Cfg<D, NT>;
+  constexpr int KS = D / 16;              // 16-deep steps of S, and 16-dimension blocks of O
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scan[kWarps];
+  __shared__ int64_t s_u;                 // units before the sequence that holds this CTA's first one
+  __shared__ int s_b, s_last;
+  __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows], s_inv[C::kRows];
+
+  const moe_kv_attention_desc& d = a.d;
+  const moe_kv_cache& kc = d.cache;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  const int H = kc.kv_heads, P = kc.page_size;
+  const int page_shift = 31 - __clz(P);
+  int ctas = gridDim.x;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // ---- this CTA's range of units: a scan over the sequences, a run of them per thread
+  int64_t total, u0, u1;
+  {
+    const int per = (kc.batch + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, kc.batch), b1 = min(b0 + per, kc.batch);
+    int32_t bad = 0;
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(tiles_of(a, load_seq(d, b, &bad), C::kRows).count) * H;
+    if (bad && blockIdx.x == 0) set_err(d.err, bad);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) incl += scan[w];
+      total += scan[w];
+    }
+    // at least one unit each: the CTAs that share a row are then a run without gaps
+    ctas = static_cast<int>(min(static_cast<int64_t>(ctas), total));
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    u0 = range_start(total, blockIdx.x, ctas);
+    u1 = range_start(total, blockIdx.x + 1, ctas);
+    if (u0 >= incl - mine && u0 < incl) {
+      int64_t u = incl - mine;
+      for (int b = b0; b < b1; ++b) {
+        const int64_t t = static_cast<int64_t>(tiles_of(a, load_seq(d, b, &bad), C::kRows).count) * H;
+        if (u0 < u + t) {
+          s_b = b;
+          s_u = u;
+          break;
+        }
+        u += t;
+      }
+    }
+    __syncthreads();
+  }
+  const int first_b = s_b;
+  const int64_t first_u = s_u;
+
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+  float* ring_scales = reinterpret_cast<float*>(smem + C::kScales) + warp * C::kStages * 2;
+  float* buf = reinterpret_cast<float*>(smem + C::kBuf);
+
+  // ---- producer: walks the CTA's units, kStages - 1 ahead of the consumer
+  int64_t p_left = u1 - u0;
+  int p_b = first_b, p_h, p_tile, p_end, p_base, p_stage = 0, p_pid = 0;
+  int32_t ignored = 0;                     // the scan has told
+  Seq p_s = load_seq(d, p_b, &ignored);
+  Tiles p_t = tiles_of(a, p_s, C::kRows);
+  const auto p_pages = [&] {               // the page of this warp's keys in 32 tiles from p_tile, one per lane
+    p_base = p_tile;
+    const int key = (p_tile + lane) * kTile + warp * kStep;
+    p_pid = key < p_s.len ? __ldg(kc.page_table + p_b * kc.table_ld + (key >> page_shift)) : 0;
+  };
+  p_h = static_cast<int>((u0 - first_u) / p_t.count);
+  p_tile = p_t.first + static_cast<int>((u0 - first_u) % p_t.count);
+  p_end = p_t.first + p_t.count;
+  const int first_h = p_h, first_tile = p_tile;
+  p_pages();
+  const auto issue = [&] {
+    if (p_left > 0) {
+      if (p_tile == p_end) {
+        if (++p_h == H) {
+          p_h = 0;
+          do {
+            p_s = load_seq(d, ++p_b, &ignored);
+            p_t = tiles_of(a, p_s, C::kRows);
+          } while (p_t.count == 0 && p_b + 1 < kc.batch);
+        }
+        p_tile = p_t.first;
+        p_end = p_t.first + p_t.count;
+        p_pages();
+      } else if (p_tile - p_base == 32) {
+        p_pages();
+      }
+      const int key0 = p_tile * kTile + warp * kStep;
+      int page = __shfl_sync(0xffffffffu, p_pid, p_tile - p_base);
+      bool on = key0 < p_s.len;
+      if (on && (page < 0 || page >= kc.pages)) {
+        if (lane == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
+        on = false;
+      }
+      if (!on) page = 0;
+      const int slot0 = key0 & (P - 1);
+      const uint8_t* kp = kc.k + page * kc.k_page_ld + p_h * kc.k_head_ld + slot0 * kc.k_slot_ld;
+      const uint8_t* vp = kc.v + page * kc.v_page_ld + p_h * kc.v_head_ld + slot0 * kc.v_slot_ld;
+      const uint32_t st = ring + p_stage * C::kStageBytes;
+      constexpr int kChunks = D / 16, kRowsPer = 32 / kChunks;
+#pragma unroll
+      for (int i = 0; i < kStep / kRowsPer; ++i) {
+        const int r = lane / kChunks + i * kRowsPer, ch = lane % kChunks;
+        const bool in = on && key0 + r < p_s.len;      // past the end: zeros, nothing is read
+        cp16(st + chunk_at<D>(r, ch), in ? kp + r * kc.k_slot_ld + ch * 16 : kc.k, in);
+        cp16(st + kStep * D + chunk_at<D>(r, ch), in ? vp + r * kc.v_slot_ld + ch * 16 : kc.v, in);
+      }
+      if (lane < 2) {
+        const float* sp = (lane ? kc.v_scale : kc.k_scale) + static_cast<int64_t>(page) * H + p_h;
+        cp_async_4(smem_u32(ring_scales + p_stage * 2 + lane), sp, on ? 4 : 0);
+      }
+      ++p_tile;
+      --p_left;
+      if (++p_stage == C::kStages) p_stage = 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::kStages - 1; ++i) issue();
+
+  // ---- consumer: one (sequence, kv head) after the other
+  int stage = 0, b = first_b, h = first_h, tile = first_tile;
+  int64_t u = u0;
+  Seq s = load_seq(d, b, &ignored);
+  Tiles t = tiles_of(a, s, C::kRows);
+  while (true) {
+    const int rows = s.n * a.G;
+    const int tile_begin = tile;
+    const int tile_stop = static_cast<int>(min(static_cast<int64_t>(t.first + t.count), tile + (u1 - u)));
+    const int lo_first = first_key(d, s, 0), lo_last = first_key(d, s, s.n - 1);
+    const int hi_first = end_key(d, s, 0);
+
+    // Q as the second operand: lane (g, c) holds row g's dimensions c * D/4 ..., scaled into f16
+    uint32_t q[NT][KS][2];
+    float qs[NT][2], m[NT][2], mu[NT][2], l[NT][2], o[NT][KS][4];
+    int lo[NT][2], hi[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      float amax = 0.0f;
+      uint4 w[D / 32];
+      if (r < rows) {
+        const int i = r / a.G;
+        const uint16_t* qp = static_cast<const uint16_t*>(d.q) + (s.c0 + i) * d.q_token_ld +
+                             (h * a.G + r - i * a.G) * d.q_head_ld + c * (D / 4);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) w[k] = __ldg(reinterpret_cast<const uint4*>(qp) + k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) w[k] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        float f[8];
+        unpack8<F16>(w[k], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = f[e] != f[e] ? INFINITY : fmaxf(amax, fabsf(f[e]));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      float mul, inv;
+      row_scale(amax, mul, inv);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        float f[8];
+        unpack8<F16>(w[k], f);
+        q[nt][2 * k][0] = f16x2(f[0] * mul, f[1] * mul);
+        q[nt][2 * k][1] = f16x2(f[2] * mul, f[3] * mul);
+        q[nt][2 * k + 1][0] = f16x2(f[4] * mul, f[5] * mul);
+        q[nt][2 * k + 1][1] = f16x2(f[6] * mul, f[7] * mul);
+      }
+      inv *= d.softcap > 0.0f ? d.sm_scale / d.softcap : d.sm_scale * kLog2e;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {       // of the columns of S^T that this lane holds
+        qs[nt][e] = __shfl_sync(0xffffffffu, inv, (2 * c + e) * 4);
+        const int i = min((nt * 8 + 2 * c + e) / a.G, s.n - 1);
+        lo[nt][e] = first_key(d, s, i);
+        hi[nt][e] = end_key(d, s, i);
+        m[nt][e] = -INFINITY;
+        mu[nt][e] = 0.0f;
+        l[nt][e] = 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][k][e] = 0.0f;
+    }
+
+    uint32_t nan_seen = 0;
+#pragma unroll 1
+    for (; tile < tile_stop; ++tile) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+      __syncwarp();
+      const int key0 = tile * kTile + warp * kStep;
+      if (key0 < s.len && key0 + kStep > lo_first) {
+        const uint32_t ks = ring + stage * C::kStageBytes, vs = ks + kStep * D;
+        const float k_scale = ring_scales[stage * 2], v_scale = fmaxf(ring_scales[stage * 2 + 1], kMinScale);
+        const float v_log = __log2f(v_scale), v_inv = __fdividef(1.0f, v_scale);
+        const bool edge = key0 < lo_last || key0 + kStep > hi_first;
+        float sc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
+#pragma unroll
+        for (int k4 = 0; k4 < KS / 4; ++k4) {
+          const int ch = c * (D / 64) + k4;
+          const uint4 x = lds16(ks + chunk_at<D>(g, ch)), y = lds16(ks + chunk_at<D>(g + 8, ch));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t f[4] = {e4m3x2_to_f16x2(xw[k] & 0xFFFF), e4m3x2_to_f16x2(yw[k] & 0xFFFF),
+                                   e4m3x2_to_f16x2(xw[k] >> 16), e4m3x2_to_f16x2(yw[k] >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              if (nt * 8 < rows) mma(sc[nt], f, q[nt][k4 * 4 + k][0], q[nt][k4 * 4 + k][1]);
+          }
+        }
+        // scores in powers of two, with the V scale's logarithm
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = sc[nt][e] * (qs[nt][e & 1] * k_scale);
+            if (d.softcap > 0.0f) x = capped_log2(x, d.softcap * kLog2e);
+            x += v_log;
+            if (edge) {
+              const int key = key0 + g + (e >> 1) * 8;
+              if (key < lo[nt][e & 1] || key >= hi[nt][e & 1]) x = -INFINITY;
+            }
+            sc[nt][e] = x;
+          }
+          over |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + kLazy || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + kLazy;
+        }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(sc[nt][e], sc[nt][e + 2]);
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              x = fmaxf(x, m[nt][e]);
+              const float keep = x == -INFINITY ? 1.0f : ex2(m[nt][e] - x);
+              m[nt][e] = x;
+              mu[nt][e] = x == -INFINITY ? 0.0f : x;
+              l[nt][e] *= keep;
+#pragma unroll
+              for (int k = 0; k < KS; ++k) {
+                o[nt][k][e] *= keep;
+                o[nt][k][e + 2] *= keep;
+              }
+            }
+        }
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = ex2(sc[nt][e] - mu[nt][e & 1]);
+          l[nt][0] = fmaf(w[0] + w[2], v_inv, l[nt][0]);
+          l[nt][1] = fmaf(w[1] + w[3], v_inv, l[nt][1]);
+          p[nt][0] = transposed(f16x2(w[0], w[1]));
+          p[nt][1] = transposed(f16x2(w[2], w[3]));
+        }
+#pragma unroll
+        for (int k2 = 0; k2 < KS / 2; ++k2) {
+          uint32_t v[4];
+          ldsm4_t(vs + chunk_at<D>((lane & 7) + (lane & 8), 2 * k2 + (lane >> 4)), v);
+          if (edge) {
+            // a NaN that some row does not see must not meet its zero weight: it is
+            // put back for the rows that do see it once the keys are done
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t bad = nan_codes(v[i]);
+              nan_seen |= bad;
+              v[i] &= ~((bad >> 7) * 0xFFu);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t x = __byte_perm(v[2 * i], 0, 0x3120), y = __byte_perm(v[2 * i + 1], 0, 0x3120);
+            const uint32_t f[4] = {e4m3x2_to_f16x2(x & 0xFFFF), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y & 0xFFFF),
+                                   e4m3x2_to_f16x2(y >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              if (nt * 8 < rows) mma(o[nt][2 * k2 + i], f, p[nt][0], p[nt][1]);
+          }
+        }
+      }
+      __syncwarp();                        // every lane has read the stage that is filled next
+      issue();
+      if (++stage == C::kStages) stage = 0;
+    }
+
+    // ---- the four warps' results together, in buf: m, l and the unnormalised output
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+        if (g == 0) {
+          s_m[warp][nt * 8 + 2 * c + e] = m[nt][e];
+          s_l[warp][nt * 8 + 2 * c + e] = l[nt][e];
+        }
+      }
+    const bool fix_nan = __syncthreads_or(nan_seen != 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * c + e;
+        float top = s_m[0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        // a warp without weights (m = -inf) may still hold a NaN
+        const float keep = m[nt][e] == -INFINITY ? 1.0f : ex2(m[nt][e] - top);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          o[nt][k][e] *= keep;
+          o[nt][k][e + 2] *= keep;
+        }
+      }
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float2* at = reinterpret_cast<float2*>(buf + (nt * 8 + 2 * c + e) * C::kLd + 16 * k + 2 * g);
+              float2 x = w ? *at : make_float2(0.0f, 0.0f);
+              x.x += o[nt][k][e];
+              x.y += o[nt][k][e + 2];
+              *at = x;
+            }
+      }
+      __syncthreads();
+    }
+    float top = -INFINITY, sum = 0.0f;     // of row tid
+    if (tid < C::kRows) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][tid]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        sum += s_l[w][tid] * (s_m[w][tid] == -INFINITY ? 1.0f : ex2(s_m[w][tid] - top));
+    }
+    if (fix_nan) {
+      for (int x = tid; x < rows * D; x += kThreads) {
+        const int r = x / D, dim = x % D, i = r / a.G;
+        const int from = max(first_key(d, s, i), tile_begin * kTile), to = min(end_key(d, s, i), tile_stop * kTile);
+        for (int j = from; j < to; ++j) {
+          const int k0 = j & ~(kStep - 1);
+          if (!(k0 < lo_last || k0 + kStep > hi_first)) {   // not a step whose NaNs were taken out
+            j = max(j, (hi_first & ~(kStep - 1)) - 1);      // on to the next one
+            continue;
+          }
+          const int page = __ldg(kc.page_table + b * kc.table_ld + (j >> page_shift));
+          if (page < 0 || page >= kc.pages) continue;
+          const uint8_t code = kc.v[page * kc.v_page_ld + h * kc.v_head_ld + (j & (P - 1)) * kc.v_slot_ld + dim];
+          if ((code & 0x7F) == 0x7F) buf[r * C::kLd + dim] = __uint_as_float(0x7FC00000u);
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- write the rows, or leave a part and let the last CTA join them
+    const int64_t seg0 = u - (tile_begin - t.first), seg1 = seg0 + t.count;   // units of this (sequence, kv head)
+    const bool whole = seg0 >= u0 && seg1 <= u1;
+    const auto write_rows = [&] {
+      if (tid < C::kRows) {
+        s_inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;       // NaN stays
+        if (d.lse != nullptr && tid < rows) {
+          const int i = tid / a.G;
+          d.lse[static_cast<int64_t>(s.c0 + i) * d.q_heads + h * a.G + tid - i * a.G] =
+              sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+        }
+      }
+      __syncthreads();
+      for (int x = tid; x < rows * (D / 8); x += kThreads) {
+        const int r = x / (D / 8), e = x % (D / 8) * 8, i = r / a.G;
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = buf[r * C::kLd + e + k] * s_inv[r];
+        uint16_t* op = static_cast<uint16_t*>(d.out) + (s.c0 + i) * d.o_token_ld + (h * a.G + r - i * a.G) * d.o_head_ld + e;
+        *reinterpret_cast<uint4*>(op) = pack8<F16>(f);
+      }
+    };
+    if (whole) {
+      write_rows();
+    } else {
+      const int ca = owner(seg0, total, ctas), cz = owner(seg1 - 1, total, ctas);
+      // a CTA leaves at most two parts: of a row that began before it, and of one that goes on after it
+      const auto part_of = [&](int cta) { return a.parts + (2ll * cta + (cta == ca ? 1 : 0)) * kPartFloats; };
+      const auto leave = [&](float* part) {
+        if (tid < rows) {
+          __stcg(part + tid, top);
+          __stcg(part + kDecodeRows + tid, sum);
+        }
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+          const int r = x / (D / 4), e = x % (D / 4) * 4;
+          __stcg(reinterpret_cast<float4*>(part + 2 * kDecodeRows + r * D + e),
+                 *reinterpret_cast<const float4*>(buf + r * C::kLd + e));
+        }
+      };
+      const auto arrive_last = [&](int32_t* counter, int count) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          const int before = atomicAdd(counter, 1);
+          s_last = before == count - 1;
+          if (s_last) *counter = 0;                          // as the next call wants it
+        }
+        __syncthreads();
+        __threadfence();
+        return s_last != 0;
+      };
+      // parts of CTAs first, first + stride, ... into buf, top and sum
+      const auto join = [&](int first, int stride, int count) {
+        if (tid < C::kRows) {
+          top = -INFINITY;
+          sum = 0.0f;
+          if (tid < rows) {
+            for (int k = 0; k < count; ++k) top = fmaxf(top, __ldcg(part_of(first + k * stride) + tid));
+            for (int k = 0; k < count; ++k) {
+              const float* part = part_of(first + k * stride);
+              const float pm = __ldcg(part + tid);
+              sum += __ldcg(part + kDecodeRows + tid) * (pm == -INFINITY ? 1.0f : ex2(pm - top));
+            }
+          }
+          s_m[0][tid] = top;
+        }
+        __syncthreads();
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+          const int r = x / (D / 4), e = x % (D / 4) * 4;
+          float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+          for (int k = 0; k < count; ++k) {
+            const float* part = part_of(first + k * stride);
+            const float pm = __ldcg(part + r);
+            const float keep = pm == -INFINITY ? 1.0f : ex2(pm - s_m[0][r]);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + 2 * kDecodeRows + r * D + e));
+            acc.x = fmaf(v.x, keep, acc.x);
+            acc.y = fmaf(v.y, keep, acc.y);
+            acc.z = fmaf(v.z, keep, acc.z);
+            acc.w = fmaf(v.w, keep, acc.w);
+          }
+          *reinterpret_cast<float4*>(buf + r * C::kLd + e) = acc;
+        }
+        __syncthreads();
+      };
+      // Counters: a CTA may be the first of the row it begins and of a later group
+      // of the row it goes on with, so these count apart.
+      const int parts = cz - ca + 1;
+      leave(part_of(blockIdx.x));
+      const int group = ca + (static_cast<int>(blockIdx.x) - ca) / kGroup * kGroup;
+      const int in_group = min(kGroup, cz - group + 1);
+      if (arrive_last(a.counters + (group == ca ? 0 : kMaxParts) + group, in_group)) {
+        join(group, 1, in_group);
+        if (parts <= kGroup) {
+          write_rows();
+        } else {
+          // the group's first part takes the group's sum
+          leave(part_of(group));
+          const int groups = (parts + kGroup - 1) / kGroup;
+          if (arrive_last(a.counters + 2 * kMaxParts + ca, groups)) {
+            join(ca, kGroup, groups);
+            write_rows();
+          }
+        }
+      }
+    }
+    u += tile_stop - tile_begin;
+    if (u >= u1) break;
+    // the next (sequence, kv head)
+    if (++h == H) {
+      h = 0;
+      do {
+        s = load_seq(d, ++b, &ignored);
+        t = tiles_of(a, s, C::kRows);
+      } while (t.count == 0 && b + 1 < kc.batch);
+    }
+    tile = t.first;
+    __syncthreads();                       // buf and the statistics are free
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <bool F16, int D, int NT>
+int launch(const AttnArgs& a, cudaStream_t st) {
+  static int prepared[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  constexpr int smem = Cfg<D, NT>::kSmem;
+  if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kv_decode_kernel<F16, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
+  }
+  const int ctas = min(kMaxParts, num_sms() * kCtasPerSm);
+  return launch_pdl(kv_decode_kernel<F16, D, NT>, dim3(ctas), dim3(kThreads), smem, st, a);
+}
+
+template <bool F16, int D>
+int pick_rows(const AttnArgs& a, int64_t rows, cudaStream_t st) {
+  if (rows <= 8) return launch<F16, D, 1>(a, st);
+  if (rows <= 16) return launch<F16, D, 2>(a, st);
+  return launch<F16, D, 4>(a, st);
+}
+
+}  // namespace
+
+size_t kv_decode_workspace() {
+  const size_t ctas = static_cast<size_t>(min(kMaxParts, num_sms() * kCtasPerSm));
+  return kDecodeCounters * sizeof(int32_t) + ctas * 2 * kPartFloats * sizeof(float);
+}
+
+int kv_decode_launch(const AttnArgs& a, int64_t max_rows, cudaStream_t st) {
+  const bool f16 = a.d.cache.dtype == MOE_DTYPE_F16;
+  if (a.d.cache.dim == 64) return f16 ? pick_rows<true, 64>(a, max_rows, st) : pick_rows<false, 64>(a, max_rows, st);
+  return f16 ? pick_rows<true, 128>(a, max_rows, st) : pick_rows<false, 128>(a, max_rows, st);
+}
+
+}  // namespace moe
