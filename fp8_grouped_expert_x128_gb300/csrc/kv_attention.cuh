@@ -22,6 +22,7 @@ struct AttnArgs {
 
 int kv_decode_launch(const AttnArgs& a, int64_t max_rows, cudaStream_t st);
 size_t kv_decode_workspace();
+int kv_prefill_launch(const AttnArgs& a, cudaStream_t st);
 
 namespace {
 

@@ -1,0 +1,548 @@
+// Attention over the paged 8-bit cache for many rows per kv head (prompts and
+// chunks of prompts): bound by the tensor cores, 4 * dim operations for each row
+// and visible key.
+//
+// A CTA takes 256 rows (new tokens x the query heads of one kv head, so that
+// grouped heads fill tiles too) as two 128-row tiles, and walks over their keys,
+// 128 at a time.  Per tile and key block: S = Q K^T (tcgen05, f16, both operands
+// in shared memory) into TMEM; a warpgroup, one row per thread, turns S into
+// softmax weights and writes them back over S as f16; O += P V with P read from
+// TMEM.  The two tiles take turns: while one is in its softmax the tensor cores
+// work on the other.  E4M3 K and V are widened to f16 (exact) by a third
+// warpgroup on the way into shared memory, straight from global memory through
+// registers, so pages and strides cost nothing extra; a warp of the fourth issues
+// the MMAs.  Page scales stay out of the operands: K's multiply the scores, V's
+// ride in the weights as in the decode kernel.
+#include "kv_attention.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTileRows = 128;
+constexpr int kKeys = 128;               // keys per block
+constexpr int kStages = 2;               // of K and of V
+constexpr int kScaleSlots = 4;
+constexpr uint32_t kTmemCols = 512;
+// 512 * 128 registers at launch, split over the four warpgroups
+constexpr int kRegsSoftmax = 184, kRegsWiden = 96, kRegsIssue = 48;
+static_assert(256 * kRegsSoftmax + 128 * kRegsWiden + 128 * kRegsIssue <= kThreads * 128, "register split");
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;               // 64 dimensions = 128 bytes of a row each
+  static constexpr int kTileBytes = kPanels * 128 * 128;
+  static constexpr int kQ = 0;
+  static constexpr int kV = 2 * kTileBytes;
+  static constexpr int kK = kV + kStages * kTileBytes;
+  static constexpr int kScale = kK + kStages * kTileBytes;          // [slot][8 groups of 16 keys] float4
+  static constexpr int kBars = kScale + kScaleSlots * 8 * 16;
+  static constexpr int kSmem = 1024 + kBars + 256;
+  static constexpr uint32_t kTmemO = 256;              // S0, S1 (and P over them) at 0, 128; O0, O1 here
+};
+
+// mbarriers, in order
+enum { kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
+       kPFull = kSFull + 2, kOFull = kPFull + 2, kBarCount = kOFull + 2 };
+
+// Instruction descriptor, kind::f16: D fp32, A and B f16, A K-major; B K-major or
+// (mn) with its N dimension contiguous.
+constexpr uint32_t idesc_f16(int N, bool mn) {
+  return (1u << 4) | (mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+// V as the B operand: [keys][64 dimensions] panels, the dimension (N) contiguous,
+// 128-byte swizzle: 64-dimension blocks a panel apart, groups of 8 keys 1024 bytes.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t panel_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(panel_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ float4 lds16f(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+// Key blocks [first, end) that the rows [r0, r1) of a sequence see.
+struct Blocks {
+  int first, end;
+};
+__device__ __forceinline__ Blocks blocks_of(const AttnArgs& a, const Seq& s, int r0, int r1) {
+  return {first_key(a.d, s, r0 / a.G) / kKeys, (end_key(a.d, s, (r1 - 1) / a.G) + kKeys - 1) / kKeys};
+}
+
+template <bool F16, int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_constant__ AttnArgs a, uint64_t wait_ns) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_nan;
+  const moe_kv_attention_desc& d = a.d;
+  const moe_kv_cache& kc = d.cache;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
+  const int H = kc.kv_heads, P = kc.page_size, page_shift = 31 - __clz(P);
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // ---- the unit's rows.  Units of sequence b start at cu[b] * G / 256 + b: enough
+  // for its rows whatever cu is, and nothing has to be summed.
+  const int h = blockIdx.x % H, unit = blockIdx.x / H;
+  const auto unit0 = [&](int b) {
+    return static_cast<int>(static_cast<int64_t>(__ldg(kc.cu_new + b)) * a.G / (2 * kTileRows)) + b;
+  };
+  const int b = warp_find(kc.batch, unit, unit0);
+  int32_t bad = 0;
+  const Seq s = load_seq(d, b, &bad);    // faults are told by the decode kernel
+  const int rows = s.n * a.G;
+  if (rows <= kDecodeRows) return;
+  const int tiles2 = (rows + 2 * kTileRows - 1) / (2 * kTileRows);
+  const int nth = tiles2 - 1 - (unit - unit0(b));           // the last rows, with the most keys, first
+  if (nth < 0 || nth >= tiles2) return;
+  const int row0 = nth * 2 * kTileRows, row_end = min(rows, row0 + 2 * kTileRows);
+  const int tiles = row_end - row0 > kTileRows ? 2 : 1;
+  const Blocks all = blocks_of(a, s, row0, row_end);
+  const Blocks mine0 = blocks_of(a, s, row0, min(row0 + kTileRows, row_end));
+  const Blocks mine1 = tiles == 2 ? blocks_of(a, s, row0 + kTileRows, row_end) : Blocks{all.end, all.end};
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + C::kBars;
+  const auto bar = [&](int i) { return bars + 8 * i; };
+  volatile int* abort = &s_abort;
+  if (tid == 0) {
+    for (int i = 0; i < kBarCount; ++i) {
+      const bool widen = i == kKFull || i == kKFull + 1 || i == kVFull || i == kVFull + 1;
+      const bool soft = i == kPFull || i == kPFull + 1;
+      mbar_init(bar(i), i == kQFull ? 128 * tiles : widen || soft ? 128 : 1);
+    }
+    s_abort = 0;
+    s_nan = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const auto wait = [&](int i, int phase) { return mbar_wait_bounded(bar(i), phase & 1, abort, d.err, wait_ns); };
+
+  if (wg == 3) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 12 && lane == 0) {
+      // ------------------------------------------------------------ MMA issue
+      // Order per key block: for each tile, P V of the block before, then S of this
+      // one over the space that P took (MMAs of one thread run in order).
+      const uint32_t id_s = idesc_f16(kKeys, false), id_o = idesc_f16(D, true);
+      bool ok = wait(kQFull, 0);
+      int done[2] = {0, 0};              // blocks of each tile whose S has been issued
+      for (int j = all.first; ok && j <= all.end; ++j) {
+        const int kst = (j - all.first) & 1, kph = (j - all.first) >> 1;
+        const int vst = kst ^ 1, vph = (j - 1 - all.first) >> 1;
+        bool have_k = false, have_v = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Blocks m = i ? mine1 : mine0;
+          if (ok && j > m.first && j <= m.end) {
+            if (!have_v) ok = wait(kVFull + vst, vph);
+            have_v = true;
+            ok = ok && wait(kPFull + i, done[i] - 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = sdesc_mn_sw128(sbase + C::kV + vst * C::kTileBytes, 16384);
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + 8 * k, vd + 128 * k, id_o, k > 0 || done[i] > 1);
+            umma_commit(bar(kOFull + i));
+          }
+          if (ok && j < all.end && j >= m.first && j < m.end) {
+            if (!have_k) ok = wait(kKFull + kst, kph);
+            have_k = true;
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t qd = sdesc_kmajor_sw128(sbase + C::kQ + i * C::kTileBytes);
+            const uint64_t kd = sdesc_kmajor_sw128(sbase + C::kK + kst * C::kTileBytes);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = (k >> 2) * 1024 + (k & 3) * 2;
+              mma_ss(tmem + i * 128, qd + at, kd + at, id_s, k > 0);
+            }
+            umma_commit(bar(kSFull + i));
+            ++done[i];
+          }
+        }
+        if (!ok) break;
+        if (j > all.first) umma_commit(bar(kVEmpty + vst));
+        if (j < all.end) umma_commit(bar(kKEmpty + kst));
+      }
+      if (!ok && done[0] + done[1] > 0) {
+        // the MMAs in flight end before TMEM is freed: the commit below follows them
+        int dummy = 0;
+        umma_commit(bar(kQFull));        // completes phase 1 of a barrier that nobody else waits on any more
+        for (int k = 1; k < 128 * tiles; ++k) mbar_arrive(bar(kQFull));
+        mbar_wait_bounded(bar(kQFull), 1, &dummy, nullptr, wait_ns / 10);
+      }
+    }
+  } else if (wg == 2) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    // ------------------------------------------------------------ widening of K and V
+    constexpr int kChunks = D / 16;                    // 16-code chunks of a row
+    constexpr int kRowsPer = 128 / kChunks;            // rows the warpgroup takes at a time
+    constexpr int kIter = kKeys / kRowsPer;
+    const int t = tid & 127, ch = t % kChunks, r0 = t / kChunks;
+    const int hi_all = end_key(d, s, row0 / a.G), lo_all = first_key(d, s, (row_end - 1) / a.G);
+    uint4 kreg[kIter], vreg[kIter];
+    int pages = 0, pages_from = -1;                    // page of 16-key group pages_from + lane
+    bool bad_page = false;
+    const auto page_at = [&](int key) {
+      const int group = key >> 4;
+      if (pages_from < 0 || group - pages_from >= 32) {
+        pages_from = group & ~7;
+        const int k0 = (pages_from + lane) << 4;
+        pages = k0 < s.len ? __ldg(kc.page_table + b * kc.table_ld + (k0 >> page_shift)) : 0;
+        if (pages < 0 || pages >= kc.pages) {
+          bad_page = true;
+          pages = -1;
+        }
+      }
+      return __shfl_sync(0xffffffffu, pages, group - pages_from);
+    };
+    const auto load = [&](uint4 (&reg)[kIter], int j, const uint8_t* base, int64_t page_ld, int64_t head_ld, int64_t slot_ld) {
+      // a group's first key decides whether its page is looked up again: all of a
+      // block's groups are within one look-up (32 groups from a multiple of 8)
+      page_at(j * kKeys);
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const int key = j * kKeys + i * kRowsPer + r0;
+        const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
+        reg[i] = make_uint4(0, 0, 0, 0);               // past the end, or a page that is none: zeros
+        if (key < s.len && page >= 0)
+          reg[i] = __ldg(reinterpret_cast<const uint4*>(base + page * page_ld + h * head_ld + (key & (P - 1)) * slot_ld + ch * 16));
+      }
+    };
+    const auto widen = [&](const uint4 (&reg)[kIter], uint32_t tile, bool edge) {
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        uint32_t w[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
+        if (edge) {
+          // as in the decode kernel: a NaN must not meet the zero weight of a row
+          // that does not see it; the rows that do get it in the end
+          uint32_t any = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bad = nan_codes(w[k]);
+            any |= bad;
+            w[k] &= ~((bad >> 7) * 0xFFu);
+          }
+          if (any) s_nan = 1;
+        }
+        uint4 lo, hi;
+        lo.x = e4m3x2_to_f16x2(w[0] & 0xFFFF); lo.y = e4m3x2_to_f16x2(w[0] >> 16);
+        lo.z = e4m3x2_to_f16x2(w[1] & 0xFFFF); lo.w = e4m3x2_to_f16x2(w[1] >> 16);
+        hi.x = e4m3x2_to_f16x2(w[2] & 0xFFFF); hi.y = e4m3x2_to_f16x2(w[2] >> 16);
+        hi.z = e4m3x2_to_f16x2(w[3] & 0xFFFF); hi.w = e4m3x2_to_f16x2(w[3] >> 16);
+        const int r = i * kRowsPer + r0, c = 2 * (ch & 3);
+        const uint32_t row = tile + (ch >> 2) * 16384 + r * 128;
+        // chunks 4 apart share their place in the other panel's row: they go the other way round
+        const bool swap = (ch >> 2) != 0;
+        sts16(row + (((c + swap) ^ (r & 7)) << 4), swap ? hi : lo);
+        sts16(row + (((c + !swap) ^ (r & 7)) << 4), swap ? lo : hi);
+      }
+      fence_proxy_async_shared();
+    };
+    // scales of a block's 16-key groups, by the first warp's first lanes: (K, V)
+    float2 scales;
+    const auto load_scales = [&](int j) {
+      const int key = j * kKeys + (lane & 7) * 16;
+      const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
+      scales = make_float2(0.0f, 0.0f);
+      if (t < 8 && key < s.len && page >= 0) {
+        const int64_t at = static_cast<int64_t>(page) * H + h;
+        scales = make_float2(__ldg(kc.k_scale + at), __ldg(kc.v_scale + at));
+      }
+    };
+    load(kreg, all.first, kc.k, kc.k_page_ld, kc.k_head_ld, kc.k_slot_ld);
+    load_scales(all.first);
+    load(vreg, all.first, kc.v, kc.v_page_ld, kc.v_head_ld, kc.v_slot_ld);
+    for (int j = all.first; j < all.end; ++j) {
+      const int n = j - all.first, st = n & 1, use = n >> 1;
+      if (use > 0 && !wait(kKEmpty + st, use - 1)) break;
+      if (t < 8) {
+        const float v = fmaxf(scales.y, kMinScale);    // its logarithm and inverse are what the weights take
+        *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + t) * 16) =
+            make_float4(scales.x, __log2f(v), __fdividef(1.0f, v), 0.0f);
+      }
+      widen(kreg, sbase + C::kK + st * C::kTileBytes, false);
+      mbar_arrive(bar(kKFull + st));
+      if (j + 1 < all.end) {
+        load(kreg, j + 1, kc.k, kc.k_page_ld, kc.k_head_ld, kc.k_slot_ld);
+        load_scales(j + 1);
+      }
+      if (use > 0 && !wait(kVEmpty + st, use - 1)) break;
+      widen(vreg, sbase + C::kV + st * C::kTileBytes, j * kKeys < lo_all || (j + 1) * kKeys > hi_all);
+      mbar_arrive(bar(kVFull + st));
+      if (j + 1 < all.end) load(vreg, j + 1, kc.v, kc.v_page_ld, kc.v_head_ld, kc.v_slot_ld);
+    }
+    if (bad_page) set_err(d.err, MOE_DEV_BAD_INDEX);
+  } else if (wg < tiles) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ------------------------------------------------------------ softmax and output of tile wg
+    const int t = tid & 127;
+    const int r = row0 + wg * kTileRows + t;
+    const bool live = r < rows;
+    const int i = min(r, rows - 1) / a.G, head = h * a.G + min(r, rows - 1) - i * a.G;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // this warp's TMEM lanes (bits 16 and up)
+    const uint32_t ts = tmem + lanes + wg * 128, to = tmem + lanes + C::kTmemO + wg * D;
+    float qs;
+    {
+      const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d.q) + (s.c0 + i) * d.q_token_ld +
+                                                       head * d.q_head_ld);
+      const uint32_t tile = sbase + C::kQ + wg * C::kTileBytes + t * 128;
+      uint4 w[D / 8];
+      float amax = 0.0f;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        w[k] = live ? __ldg(qp + k) : make_uint4(0, 0, 0, 0);
+        float f[8];
+        unpack8<F16>(w[k], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = f[e] != f[e] ? INFINITY : fmaxf(amax, fabsf(f[e]));
+      }
+      float mul, inv;
+      row_scale(amax, mul, inv);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        float f[8];
+        unpack8<F16>(w[k], f);
+        sts16(tile + (k >> 3) * 16384 + (((k & 7) ^ (t & 7)) << 4),
+              make_uint4(f16x2(f[0] * mul, f[1] * mul), f16x2(f[2] * mul, f[3] * mul), f16x2(f[4] * mul, f[5] * mul),
+                         f16x2(f[6] * mul, f[7] * mul)));
+      }
+      qs = inv * (CAP ? d.sm_scale / d.softcap : d.sm_scale * kLog2e);
+      fence_proxy_async_shared();
+      mbar_arrive(bar(kQFull));
+    }
+    const int lo = first_key(d, s, i), hi = end_key(d, s, i);
+    const int tile_r1 = min(rows, row0 + (wg + 1) * kTileRows) - 1;
+    const int lo_last = first_key(d, s, tile_r1 / a.G), hi_first = end_key(d, s, (row0 + wg * kTileRows) / a.G);
+    const Blocks m = wg ? mine1 : mine0;
+    float top = -INFINITY, ref = 0.0f, sum = 0.0f;       // running reference (ref: the same, 0 while -inf) and sum
+    bool ok = true;
+    for (int j = m.first; j < m.end; ++j) {
+      const int n = j - m.first;
+      ok = wait(kSFull + wg, n);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[4][32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(ts + 32 * k, x[k]);
+      const uint32_t scale = sbase + C::kScale + ((j - all.first) & (kScaleSlots - 1)) * 128;
+      tmem_ld_wait();
+      const bool edge = j * kKeys < lo_last || (j + 1) * kKeys > hi_first;
+      float best = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float4 sc = lds16f(scale + (2 * k + half) * 16);
+          const float f = qs * sc.x;
+          const uint64_t f2 = f2_pack(f, f), v2 = f2_pack(sc.y, sc.y);
+#pragma unroll
+          for (int e = 16 * half; e < 16 * half + 16; e += 2) {
+            float y0, y1;
+            if constexpr (CAP) {
+              y0 = capped_log2(__uint_as_float(x[k][e]) * f, d.softcap * kLog2e) + sc.y;
+              y1 = capped_log2(__uint_as_float(x[k][e + 1]) * f, d.softcap * kLog2e) + sc.y;
+            } else {
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])), f2, v2), y0, y1);
+            }
+            if (edge) {
+              const int key = j * kKeys + 32 * k + e;
+              if (key < lo || key >= hi) y0 = -INFINITY;
+              if (key + 1 < lo || key + 1 >= hi) y1 = -INFINITY;
+            }
+            best = fmaxf(best, fmaxf(y0, y1));
+            x[k][e] = __float_as_uint(y0);
+            x[k][e + 1] = __float_as_uint(y1);
+          }
+        }
+      if (__any_sync(0xffffffffu, best > top + kLazy)) {
+        const float next = best > top + kLazy ? best : top;
+        const float keep = next == -INFINITY ? 1.0f : ex2(top - next);
+        top = next;
+        ref = next == -INFINITY ? 0.0f : next;
+        sum *= keep;
+        if (n > 0) {
+          ok = wait(kOFull + wg, n - 1);                 // P V of the block before is in
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 32 * k, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+            tmem_st_x32(to + 32 * k, o);
+          }
+        }
+      }
+      const uint64_t nref = f2_pack(-ref, -ref);
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        uint32_t p[32];
+#pragma unroll
+        for (int k = 2 * k2; k < 2 * k2 + 2; ++k)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint64_t acc = 0;
+#pragma unroll
+            for (int e = 16 * half; e < 16 * half + 16; e += 2) {
+              float y0, y1;
+              f2_unpack(f2_add(f2_pack(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])), nref), y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              acc = f2_add(acc, f2_pack(y0, y1));
+              p[(k - 2 * k2) * 16 + e / 2] = f16x2(y0, y1);
+            }
+            const float4 sc = lds16f(scale + (2 * k + half) * 16);
+            float a0, a1;
+            f2_unpack(acc, a0, a1);
+            sum = fmaf(a0 + a1, sc.z, sum);
+          }
+        tmem_st_x32(ts + 32 * k2, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bar(kPFull + wg));
+    }
+    if (ok) ok = wait(kOFull + wg, m.end - m.first - 1);
+    if (ok) {
+      tc_fence_after();
+      uint32_t nans[D / 32];
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) nans[k] = 0;
+      if (*static_cast<volatile int*>(&s_nan)) {
+        // NaN codes that were taken out of blocks with rows that do not see them all
+        const int hi_all = end_key(d, s, row0 / a.G), lo_all = first_key(d, s, (row_end - 1) / a.G);
+        for (int key = lo; key < hi; ++key) {
+          const int k0 = key & ~(kKeys - 1);
+          if (!(k0 < lo_all || k0 + kKeys > hi_all)) {
+            key = max(key, (hi_all & ~(kKeys - 1)) - 1);
+            continue;
+          }
+          const int page = __ldg(kc.page_table + b * kc.table_ld + (key >> page_shift));
+          if (page < 0 || page >= kc.pages) continue;
+          const uint8_t* vp = kc.v + page * kc.v_page_ld + h * kc.v_head_ld + (key & (P - 1)) * kc.v_slot_ld;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            for (int e = 0; e < 32; ++e)
+              if ((vp[32 * k + e] & 0x7F) == 0x7F) nans[k] |= 1u << e;
+        }
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(d.out) + (s.c0 + i) * d.o_token_ld + head * d.o_head_ld);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(to + 32 * k, o);
+        tmem_ld_wait();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float f[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              f[y] = (nans[k] >> (e + y)) & 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(o[e + y]) * inv;
+            op[4 * k + e / 8] = pack8<F16>(f);
+          }
+        }
+      }
+      if (live && d.lse != nullptr)
+        d.lse[static_cast<int64_t>(s.c0 + i) * d.q_heads + head] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <bool F16, int D, bool CAP>
+int launch(const AttnArgs& a, cudaStream_t st) {
+  static int prepared[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  const auto kernel = kv_prefill_kernel<F16, D, CAP>;
+  if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
+    // the register split counts on exactly the launch allocation
+    cudaFuncAttributes attr;
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&attr, kernel));
+    if (attr.numRegs * kThreads != 65536) return MOE_ERR_UNSUPPORTED;
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem));
+    __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
+  }
+  const int64_t units = (a.d.T * a.G / (2 * kTileRows) + a.d.cache.batch) * a.d.cache.kv_heads;
+  if (units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(units)), dim3(kThreads), Cfg<D>::kSmem, st, a, kWaitLimitNs);
+}
+
+template <bool F16, int D>
+int pick_cap(const AttnArgs& a, cudaStream_t st) {
+  return a.d.softcap > 0.0f ? launch<F16, D, true>(a, st) : launch<F16, D, false>(a, st);
+}
+
+}  // namespace
+
+int kv_prefill_launch(const AttnArgs& a, cudaStream_t st) {
+  const bool f16 = a.d.cache.dtype == MOE_DTYPE_F16;
+  if (a.d.cache.dim == 64) return f16 ? pick_cap<true, 64>(a, st) : pick_cap<false, 64>(a, st);
+  return f16 ? pick_cap<true, 128>(a, st) : pick_cap<false, 128>(a, st);
+}
+
+}  // namespace moe
