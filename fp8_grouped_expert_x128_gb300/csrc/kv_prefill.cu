@@ -25,7 +25,7 @@ constexpr int kStages = 2;               // of K and of V
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmemCols = 512;
 // 512 * 128 registers at launch, split over the four warpgroups
-constexpr int kRegsSoftmax = 184, kRegsWiden = 96, kRegsIssue = 48;
+constexpr int kRegsSoftmax = 176, kRegsWiden = 96, kRegsIssue = 64;
 static_assert(256 * kRegsSoftmax + 128 * kRegsWiden + 128 * kRegsIssue <= kThreads * 128, "register split");
 
 template <int D>
@@ -50,29 +50,26 @@ enum { kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVF
 constexpr uint32_t idesc_f16(int N, bool mn) {
   return (1u << 4) | (mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
-// V as the B operand: [keys][64 dimensions] panels, the dimension (N) contiguous,
-// 128-byte swizzle: 64-dimension blocks a panel apart, groups of 8 keys 1024 bytes.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t panel_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(panel_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// Shared-memory matrix descriptors, 128-byte swizzle, as their low words (the high
+// one is the same for all): Q and K have the contracted dimension contiguous; V, as
+// the B operand of P V, its N dimension: 64-dimension blocks a panel apart (the
+// leading offset), groups of 8 keys 1024 bytes (the stride offset, in both).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t leading) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(static_cast<uint32_t>(acc))
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc)), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(static_cast<uint32_t>(acc))
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc)), "r"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_x32(uint32_t addr, const uint32_t (&r)[32]) {
@@ -86,11 +83,38 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t addr, const uint32_t (&r)[3
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Waits for this thread's TMEM loads, x's among them: no use of x moves ahead of it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]),
+                 "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]),
+                 "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]),
+                 "+r"(x[30]), "+r"(x[31])::"memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+// 16 bytes read once by this CTA (no place in L1, what shared memory leaves of
+// it), or zeros without a read; no branch either way.
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p, bool on) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"(static_cast<uint32_t>(on)));
+  return v;
 }
 __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -189,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
             ok = ok && wait(kPFull + i, done[i] - 1);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t vd = sdesc_mn_sw128(sbase + C::kV + vst * C::kTileBytes, 16384);
+            uint32_t vd = desc_lo(sbase + C::kV + vst * C::kTileBytes, 16384);
+            asm volatile("" : "+r"(vd));             // kept from being spread over registers ahead of the loop
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
               mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + 8 * k, vd + 128 * k, id_o, k > 0 || done[i] > 1);
@@ -200,8 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
             have_k = true;
             if (!ok) break;
             tc_fence_after();
-            const uint64_t qd = sdesc_kmajor_sw128(sbase + C::kQ + i * C::kTileBytes);
-            const uint64_t kd = sdesc_kmajor_sw128(sbase + C::kK + kst * C::kTileBytes);
+            uint32_t qd = desc_lo(sbase + C::kQ + i * C::kTileBytes, 16);
+            uint32_t kd = desc_lo(sbase + C::kK + kst * C::kTileBytes, 16);
+            asm volatile("" : "+r"(qd), "+r"(kd));
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t at = (k >> 2) * 1024 + (k & 3) * 2;
@@ -247,7 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       }
       return __shfl_sync(0xffffffffu, pages, group - pages_from);
     };
-    const auto load = [&](uint4 (&reg)[kIter], int j, const uint8_t* base, int64_t page_ld, int64_t head_ld, int64_t slot_ld) {
+    const uint8_t* k_base = kc.k + h * kc.k_head_ld + ch * 16;
+    const uint8_t* v_base = kc.v + h * kc.v_head_ld + ch * 16;
+    const auto load = [&](uint4 (&reg)[kIter], int j, const uint8_t* base, int64_t page_ld, int64_t slot_ld) {
       // a group's first key decides whether its page is looked up again: all of a
       // block's groups are within one look-up (32 groups from a multiple of 8)
       page_at(j * kKeys);
@@ -255,27 +283,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       for (int i = 0; i < kIter; ++i) {
         const int key = j * kKeys + i * kRowsPer + r0;
         const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
-        reg[i] = make_uint4(0, 0, 0, 0);               // past the end, or a page that is none: zeros
-        if (key < s.len && page >= 0)
-          reg[i] = __ldg(reinterpret_cast<const uint4*>(base + page * page_ld + h * head_ld + (key & (P - 1)) * slot_ld + ch * 16));
+        // past the end, or a page that is none: zeros
+        reg[i] = ldg_stream(base + page * page_ld + (key & (P - 1)) * slot_ld, key < s.len && page >= 0);
       }
     };
-    const auto widen = [&](const uint4 (&reg)[kIter], uint32_t tile, bool edge) {
+    // A NaN must not meet the zero weight of a row that does not see it (as in the
+    // decode kernel): blocks with such rows lose theirs here, and the rows that do
+    // see them get them in the end.
+    const auto take_nans = [&](uint4 (&reg)[kIter]) {
+      uint32_t any = 0;
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
-        uint32_t w[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
-        if (edge) {
-          // as in the decode kernel: a NaN must not meet the zero weight of a row
-          // that does not see it; the rows that do get it in the end
-          uint32_t any = 0;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&reg[i]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t bad = nan_codes(w[k]);
-            any |= bad;
-            w[k] &= ~((bad >> 7) * 0xFFu);
-          }
-          if (any) s_nan = 1;
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t bad = nan_codes(w[k]);
+          any |= bad;
+          w[k] &= ~((bad >> 7) * 0xFFu);
         }
+      }
+      if (any) s_nan = 1;
+    };
+    const auto widen = [&](const uint4 (&reg)[kIter], uint32_t tile) {
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const uint32_t w[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
         uint4 lo, hi;
         lo.x = e4m3x2_to_f16x2(w[0] & 0xFFFF); lo.y = e4m3x2_to_f16x2(w[0] >> 16);
         lo.z = e4m3x2_to_f16x2(w[1] & 0xFFFF); lo.w = e4m3x2_to_f16x2(w[1] >> 16);
@@ -301,9 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         scales = make_float2(__ldg(kc.k_scale + at), __ldg(kc.v_scale + at));
       }
     };
-    load(kreg, all.first, kc.k, kc.k_page_ld, kc.k_head_ld, kc.k_slot_ld);
+    load(kreg, all.first, k_base, kc.k_page_ld, kc.k_slot_ld);
     load_scales(all.first);
-    load(vreg, all.first, kc.v, kc.v_page_ld, kc.v_head_ld, kc.v_slot_ld);
+    load(vreg, all.first, v_base, kc.v_page_ld, kc.v_slot_ld);
     for (int j = all.first; j < all.end; ++j) {
       const int n = j - all.first, st = n & 1, use = n >> 1;
       if (use > 0 && !wait(kKEmpty + st, use - 1)) break;
@@ -312,16 +344,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + t) * 16) =
             make_float4(scales.x, __log2f(v), __fdividef(1.0f, v), 0.0f);
       }
-      widen(kreg, sbase + C::kK + st * C::kTileBytes, false);
+      widen(kreg, sbase + C::kK + st * C::kTileBytes);
       mbar_arrive(bar(kKFull + st));
       if (j + 1 < all.end) {
-        load(kreg, j + 1, kc.k, kc.k_page_ld, kc.k_head_ld, kc.k_slot_ld);
+        load(kreg, j + 1, k_base, kc.k_page_ld, kc.k_slot_ld);
         load_scales(j + 1);
       }
       if (use > 0 && !wait(kVEmpty + st, use - 1)) break;
-      widen(vreg, sbase + C::kV + st * C::kTileBytes, j * kKeys < lo_all || (j + 1) * kKeys > hi_all);
+      if (j * kKeys < lo_all || (j + 1) * kKeys > hi_all) take_nans(vreg);
+      widen(vreg, sbase + C::kV + st * C::kTileBytes);
       mbar_arrive(bar(kVFull + st));
-      if (j + 1 < all.end) load(vreg, j + 1, kc.v, kc.v_page_ld, kc.v_head_ld, kc.v_slot_ld);
+      if (j + 1 < all.end) load(vreg, j + 1, v_base, kc.v_page_ld, kc.v_slot_ld);
     }
     if (bad_page) set_err(d.err, MOE_DEV_BAD_INDEX);
   } else if (wg < tiles) {
@@ -350,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       }
       float mul, inv;
       row_scale(amax, mul, inv);
+      mul = copysignf(mul, d.sm_scale);
 #pragma unroll
       for (int k = 0; k < D / 8; ++k) {
         float f[8];
@@ -358,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
               make_uint4(f16x2(f[0] * mul, f[1] * mul), f16x2(f[2] * mul, f[3] * mul), f16x2(f[4] * mul, f[5] * mul),
                          f16x2(f[6] * mul, f[7] * mul)));
       }
-      qs = inv * (CAP ? d.sm_scale / d.softcap : d.sm_scale * kLog2e);
+      qs = inv * fabsf(CAP ? d.sm_scale / d.softcap : d.sm_scale * kLog2e);
       fence_proxy_async_shared();
       mbar_arrive(bar(kQFull));
     }
@@ -373,39 +407,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       ok = wait(kSFull + wg, n);
       if (!ok) break;
       tc_fence_after();
-      uint32_t x[4][32];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(ts + 32 * k, x[k]);
       const uint32_t scale = sbase + C::kScale + ((j - all.first) & (kScaleSlots - 1)) * 128;
-      tmem_ld_wait();
       const bool edge = j * kKeys < lo_last || (j + 1) * kKeys > hi_first;
+      const int from = lo - j * kKeys, to_key = hi - j * kKeys;
+      const auto mask = [&](uint32_t (&x)[32], int k) {  // one branch, not one for each element
+        if (edge) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * k + e < from || 32 * k + e >= to_key) x[e] = 0xFF800000u;
+        }
+      };
+      // S is read twice, for the maximum and for the weights, 32 columns at a time and
+      // the next ones under this one's arithmetic: TMEM has the bandwidth, and a thread
+      // never holds its whole row.  A score is a function of S that does not fall within
+      // a group of one scale (q has taken sm_scale's sign), so the maximum needs it once
+      // for each group.
+      uint32_t xs[2][32];
+      tmem_ld_32x32b_x32(ts, xs[0]);
       float best = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 4; ++k) {
+        uint32_t (&x)[32] = xs[k & 1];
+        tmem_ld_wait_for(x);
+        tmem_ld_32x32b_x32(ts + 32 * ((k + 1) & 3), xs[(k + 1) & 1]);
+        mask(x, k);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const float4 sc = lds16f(scale + (2 * k + half) * 16);
-          const float f = qs * sc.x;
-          const uint64_t f2 = f2_pack(f, f), v2 = f2_pack(sc.y, sc.y);
+          const uint32_t* y = &x[half * 16];
+          float top16 = __uint_as_float(y[0]);
 #pragma unroll
-          for (int e = 16 * half; e < 16 * half + 16; e += 2) {
-            float y0, y1;
-            if constexpr (CAP) {
-              y0 = capped_log2(__uint_as_float(x[k][e]) * f, d.softcap * kLog2e) + sc.y;
-              y1 = capped_log2(__uint_as_float(x[k][e + 1]) * f, d.softcap * kLog2e) + sc.y;
-            } else {
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])), f2, v2), y0, y1);
-            }
-            if (edge) {
-              const int key = j * kKeys + 32 * k + e;
-              if (key < lo || key >= hi) y0 = -INFINITY;
-              if (key + 1 < lo || key + 1 >= hi) y1 = -INFINITY;
-            }
-            best = fmaxf(best, fmaxf(y0, y1));
-            x[k][e] = __float_as_uint(y0);
-            x[k][e + 1] = __float_as_uint(y1);
-          }
+          for (int e = 1; e < 15; e += 2)
+            top16 = fmaxf(fmaxf(top16, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
+          top16 = fmaxf(top16, __uint_as_float(y[15]));
+          const float4 sc = lds16f(scale + (2 * k + half) * 16);
+          best = fmaxf(best, CAP ? capped_log2(top16 * (qs * sc.x), d.softcap * kLog2e) + sc.y : fmaf(top16, qs * sc.x, sc.y));
         }
+      }
       if (__any_sync(0xffffffffu, best > top + kLazy)) {
         const float next = best > top + kLazy ? best : top;
         const float keep = next == -INFINITY ? 1.0f : ex2(top - next);
@@ -420,37 +457,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           for (int k = 0; k < D / 32; ++k) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(to + 32 * k, o);
-            tmem_ld_wait();
+            tmem_ld_wait_for(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
             tmem_st_x32(to + 32 * k, o);
           }
         }
       }
-      const uint64_t nref = f2_pack(-ref, -ref);
 #pragma unroll
-      for (int k2 = 0; k2 < 2; ++k2) {
-        uint32_t p[32];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t (&x)[32] = xs[k & 1];
+        uint32_t p[16];
+        tmem_ld_wait_for(x);
+        if (k < 3) tmem_ld_32x32b_x32(ts + 32 * (k + 1), xs[(k + 1) & 1]);
+        float inv_scale[2];
 #pragma unroll
-        for (int k = 2 * k2; k < 2 * k2 + 2; ++k)
+        for (int half = 0; half < 2; ++half) {
+          const float4 sc = lds16f(scale + (2 * k + half) * 16);
+          const float f = qs * sc.x, v = sc.y - ref;
+          const uint64_t f2 = f2_pack(f, f), v2 = f2_pack(v, v);
+          inv_scale[half] = sc.z;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint64_t acc = 0;
-#pragma unroll
-            for (int e = 16 * half; e < 16 * half + 16; e += 2) {
-              float y0, y1;
-              f2_unpack(f2_add(f2_pack(__uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1])), nref), y0, y1);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              acc = f2_add(acc, f2_pack(y0, y1));
-              p[(k - 2 * k2) * 16 + e / 2] = f16x2(y0, y1);
+          for (int e = 16 * half; e < 16 * half + 16; e += 2) {
+            float y0 = __uint_as_float(x[e]), y1 = __uint_as_float(x[e + 1]);
+            if constexpr (CAP) {
+              y0 = capped_log2(y0 * f, d.softcap * kLog2e) + v;
+              y1 = capped_log2(y1 * f, d.softcap * kLog2e) + v;
+            } else {
+              f2_unpack(f2_fma(f2_pack(y0, y1), f2, v2), y0, y1);
             }
-            const float4 sc = lds16f(scale + (2 * k + half) * 16);
-            float a0, a1;
-            f2_unpack(acc, a0, a1);
-            sum = fmaf(a0 + a1, sc.z, sum);
+            x[e] = __float_as_uint(y0);
+            x[e + 1] = __float_as_uint(y1);
           }
-        tmem_st_x32(ts + 32 * k2, p);
+        }
+        mask(x, k);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint64_t acc[2] = {0, 0};
+#pragma unroll
+          for (int e = 16 * half; e < 16 * half + 16; e += 2) {
+            const float y0 = ex2(__uint_as_float(x[e])), y1 = ex2(__uint_as_float(x[e + 1]));
+            acc[(e >> 1) & 1] = f2_add(acc[(e >> 1) & 1], f2_pack(y0, y1));
+            p[e / 2] = f16x2(y0, y1);
+          }
+          float a0, a1;
+          f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+          sum = fmaf(a0 + a1, inv_scale[half], sum);
+        }
+        tmem_st_x16(ts + 16 * k, p);                     // over columns that have been read
       }
       tmem_st_wait();
       tc_fence_before();
@@ -486,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       for (int k = 0; k < D / 32; ++k) {
         uint32_t o[32];
         tmem_ld_32x32b_x32(to + 32 * k, o);
-        tmem_ld_wait();
+        tmem_ld_wait_for(o);
         if (live) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
