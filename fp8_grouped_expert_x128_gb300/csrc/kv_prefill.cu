@@ -24,6 +24,7 @@ constexpr int kKeys = 128;               // keys per block
 constexpr int kStages = 2;               // of K and of V
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmemCols = 512;
+constexpr float kMinQScale = 8.6736174e-19f, kMinKScale = 8.6736174e-19f;   // 2^-60 each
 // 512 * 128 registers at launch, split over the four warpgroups
 constexpr int kRegsSoftmax = 176, kRegsWiden = 96, kRegsIssue = 64;
 static_assert(256 * kRegsSoftmax + 128 * kRegsWiden + 128 * kRegsIssue <= kThreads * 128, "register split");
@@ -58,19 +59,34 @@ constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t leading) {
   return ((saddr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+// By the lane with `lead`: the whole warp runs the issuing loop, so its control flow
+// and addresses are uniform.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
-      "r"(static_cast<uint32_t>(acc)), "r"(kDescHi)
+      "{\n\t.reg .pred p, l;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %6, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+      "r"(kDescHi), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
-      "r"(static_cast<uint32_t>(acc)), "r"(kDescHi)
+      "{\n\t.reg .pred p, l;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %6, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+      "r"(kDescHi), "r"(lead)
       : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+      "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
 }
 __device__ __forceinline__ void tmem_st_x32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -193,13 +209,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
 
   if (wg == 3) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
       // ------------------------------------------------------------ MMA issue
       // Order per key block: for each tile, P V of the block before, then S of this
       // one over the space that P took (MMAs of one thread run in order).
       const uint32_t id_s = idesc_f16(kKeys, false), id_o = idesc_f16(D, true);
-      bool ok = wait(kQFull, 0);
+      const uint32_t lead = elect_one();
+      bool ok = __all_sync(0xffffffffu, wait(kQFull, 0));
       int done[2] = {0, 0};              // blocks of each tile whose S has been issued
+#pragma unroll 1
       for (int j = all.first; ok && j <= all.end; ++j) {
         const int kst = (j - all.first) & 1, kph = (j - all.first) >> 1;
         const int vst = kst ^ 1, vph = (j - 1 - all.first) >> 1;
@@ -210,44 +228,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           if (ok && j > m.first && j <= m.end) {
             if (!have_v) ok = wait(kVFull + vst, vph);
             have_v = true;
-            ok = ok && wait(kPFull + i, done[i] - 1);
+            ok = __all_sync(0xffffffffu, ok && wait(kPFull + i, done[i] - 1));
             if (!ok) break;
             tc_fence_after();
-            uint32_t vd = desc_lo(sbase + C::kV + vst * C::kTileBytes, 16384);
-            asm volatile("" : "+r"(vd));             // kept from being spread over registers ahead of the loop
+            const uint32_t vd = desc_lo(sbase + C::kV + vst * C::kTileBytes, 16384);
+            const uint32_t acc = done[i] > 1;
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + 8 * k, vd + 128 * k, id_o, k > 0 || done[i] > 1);
-            umma_commit(bar(kOFull + i));
+              mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + 8 * k, vd + 128 * k, id_o, k > 0 ? 1u : acc, lead);
+            commit(bar(kOFull + i), lead);
           }
           if (ok && j < all.end && j >= m.first && j < m.end) {
-            if (!have_k) ok = wait(kKFull + kst, kph);
+            if (!have_k) ok = __all_sync(0xffffffffu, wait(kKFull + kst, kph));
             have_k = true;
             if (!ok) break;
             tc_fence_after();
-            uint32_t qd = desc_lo(sbase + C::kQ + i * C::kTileBytes, 16);
-            uint32_t kd = desc_lo(sbase + C::kK + kst * C::kTileBytes, 16);
-            asm volatile("" : "+r"(qd), "+r"(kd));
+            const uint32_t qd = desc_lo(sbase + C::kQ + i * C::kTileBytes, 16);
+            const uint32_t kd = desc_lo(sbase + C::kK + kst * C::kTileBytes, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t at = (k >> 2) * 1024 + (k & 3) * 2;
-              mma_ss(tmem + i * 128, qd + at, kd + at, id_s, k > 0);
+              mma_ss(tmem + i * 128, qd + at, kd + at, id_s, k > 0 ? 1u : 0u, lead);
             }
-            umma_commit(bar(kSFull + i));
+            commit(bar(kSFull + i), lead);
             ++done[i];
           }
         }
         if (!ok) break;
-        if (j > all.first) umma_commit(bar(kVEmpty + vst));
-        if (j < all.end) umma_commit(bar(kKEmpty + kst));
+        if (j > all.first) commit(bar(kVEmpty + vst), lead);
+        if (j < all.end) commit(bar(kKEmpty + kst), lead);
       }
-      if (!ok && done[0] + done[1] > 0) {
+      if (!ok && done[0] + done[1] > 0 && lead) {
         // the MMAs in flight end before TMEM is freed: the commit below follows them
         int dummy = 0;
         umma_commit(bar(kQFull));        // completes phase 1 of a barrier that nobody else waits on any more
         for (int k = 1; k < 128 * tiles; ++k) mbar_arrive(bar(kQFull));
         mbar_wait_bounded(bar(kQFull), 1, &dummy, nullptr, wait_ns / 10);
       }
+      __syncwarp();
     }
   } else if (wg == 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
@@ -255,73 +273,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     constexpr int kChunks = D / 16;                    // 16-code chunks of a row
     constexpr int kRowsPer = 128 / kChunks;            // rows the warpgroup takes at a time
     constexpr int kIter = kKeys / kRowsPer;
-    const int t = tid & 127, ch = t % kChunks, r0 = t / kChunks;
+    // four lanes take half a 128-byte row of codes, the next four that of the next row:
+    // their stores then fall on all banks, whatever the swizzle
+    const int t = tid & 127, panel = (t >> 5) & (C::kPanels - 1);
+    const int r0 = ((t >> 2) & 7) | (t >> (C::kPanels == 2 ? 6 : 5)) << 3, ch = panel * 4 + (t & 3);
     const int hi_all = end_key(d, s, row0 / a.G), lo_all = first_key(d, s, (row_end - 1) / a.G);
-    uint4 kreg[kIter], vreg[kIter];
+    uint4 reg[kIter];
     int pages = 0, pages_from = -1;                    // page of 16-key group pages_from + lane
     bool bad_page = false;
-    const auto page_at = [&](int key) {
-      const int group = key >> 4;
-      if (pages_from < 0 || group - pages_from >= 32) {
-        pages_from = group & ~7;
-        const int k0 = (pages_from + lane) << 4;
-        pages = k0 < s.len ? __ldg(kc.page_table + b * kc.table_ld + (k0 >> page_shift)) : 0;
-        if (pages < 0 || pages >= kc.pages) {
-          bad_page = true;
-          pages = -1;
-        }
+    const auto look_up = [&](int j) {                  // 32 groups from a multiple of 8: whole blocks
+      if (pages_from >= 0 && j * 8 - pages_from < 32) return;
+      pages_from = j * 8;
+      const int key = (pages_from + lane) << 4;
+      pages = key < s.len ? __ldg(kc.page_table + b * kc.table_ld + (key >> page_shift)) : 0;
+      if (pages < 0 || pages >= kc.pages) {
+        bad_page = true;
+        pages = -1;
       }
-      return __shfl_sync(0xffffffffu, pages, group - pages_from);
+    };
+    const auto load = [&](int i, int j, const uint8_t* base, int64_t page_ld, int64_t slot_ld) {
+      const int key = j * kKeys + i * kRowsPer + r0;
+      const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
+      // past the end, or a page that is none: zeros
+      reg[i] = ldg_stream(base + page * page_ld + (key & (P - 1)) * slot_ld, key < s.len && page >= 0);
     };
     const uint8_t* k_base = kc.k + h * kc.k_head_ld + ch * 16;
     const uint8_t* v_base = kc.v + h * kc.v_head_ld + ch * 16;
-    const auto load = [&](uint4 (&reg)[kIter], int j, const uint8_t* base, int64_t page_ld, int64_t slot_ld) {
-      // a group's first key decides whether its page is looked up again: all of a
-      // block's groups are within one look-up (32 groups from a multiple of 8)
-      page_at(j * kKeys);
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int key = j * kKeys + i * kRowsPer + r0;
-        const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
-        // past the end, or a page that is none: zeros
-        reg[i] = ldg_stream(base + page * page_ld + (key & (P - 1)) * slot_ld, key < s.len && page >= 0);
-      }
-    };
-    // A NaN must not meet the zero weight of a row that does not see it (as in the
-    // decode kernel): blocks with such rows lose theirs here, and the rows that do
-    // see them get them in the end.
-    const auto take_nans = [&](uint4 (&reg)[kIter]) {
-      uint32_t any = 0;
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&reg[i]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t bad = nan_codes(w[k]);
-          any |= bad;
-          w[k] &= ~((bad >> 7) * 0xFFu);
-        }
-      }
-      if (any) s_nan = 1;
-    };
-    const auto widen = [&](const uint4 (&reg)[kIter], uint32_t tile) {
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const uint32_t w[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
-        uint4 lo, hi;
-        lo.x = e4m3x2_to_f16x2(w[0] & 0xFFFF); lo.y = e4m3x2_to_f16x2(w[0] >> 16);
-        lo.z = e4m3x2_to_f16x2(w[1] & 0xFFFF); lo.w = e4m3x2_to_f16x2(w[1] >> 16);
-        hi.x = e4m3x2_to_f16x2(w[2] & 0xFFFF); hi.y = e4m3x2_to_f16x2(w[2] >> 16);
-        hi.z = e4m3x2_to_f16x2(w[3] & 0xFFFF); hi.w = e4m3x2_to_f16x2(w[3] >> 16);
-        const int r = i * kRowsPer + r0, c = 2 * (ch & 3);
-        const uint32_t row = tile + (ch >> 2) * 16384 + r * 128;
-        // chunks 4 apart share their place in the other panel's row: they go the other way round
-        const bool swap = (ch >> 2) != 0;
-        sts16(row + (((c + swap) ^ (r & 7)) << 4), swap ? hi : lo);
-        sts16(row + (((c + !swap) ^ (r & 7)) << 4), swap ? lo : hi);
-      }
-      fence_proxy_async_shared();
-    };
     // scales of a block's 16-key groups, by the first warp's first lanes: (K, V)
     float2 scales;
     const auto load_scales = [&](int j) {
@@ -333,28 +310,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         scales = make_float2(__ldg(kc.k_scale + at), __ldg(kc.v_scale + at));
       }
     };
-    load(kreg, all.first, k_base, kc.k_page_ld, kc.k_slot_ld);
+    // K and V blocks in turn; as a register is widened, the next unit's load goes
+    // into it, so half a block's time hides the loads.
+    look_up(all.first);
     load_scales(all.first);
-    load(vreg, all.first, v_base, kc.v_page_ld, kc.v_slot_ld);
-    for (int j = all.first; j < all.end; ++j) {
-      const int n = j - all.first, st = n & 1, use = n >> 1;
-      if (use > 0 && !wait(kKEmpty + st, use - 1)) break;
-      if (t < 8) {
-        const float v = fmaxf(scales.y, kMinScale);    // its logarithm and inverse are what the weights take
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) load(i, all.first, k_base, kc.k_page_ld, kc.k_slot_ld);
+#pragma unroll 1
+    for (int unit = 2 * all.first; unit < 2 * all.end; ++unit) {
+      const int j = unit >> 1, n = j - all.first, st = n & 1, use = n >> 1;
+      const bool is_v = unit & 1;
+      if (use > 0 && !wait((is_v ? kVEmpty : kKEmpty) + st, use - 1)) break;
+      if (!is_v && t < 8) {
+        // the V scale as its logarithm and inverse, which is what the weights take
+        const float k = fmaxf(scales.x, kMinKScale), v = fmaxf(scales.y, kMinScale);
         *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + t) * 16) =
-            make_float4(scales.x, __log2f(v), __fdividef(1.0f, v), 0.0f);
+            make_float4(k, __log2f(v), __fdividef(1.0f, v), 0.0f);
       }
-      widen(kreg, sbase + C::kK + st * C::kTileBytes);
-      mbar_arrive(bar(kKFull + st));
-      if (j + 1 < all.end) {
-        load(kreg, j + 1, k_base, kc.k_page_ld, kc.k_slot_ld);
-        load_scales(j + 1);
+      if (is_v && (j * kKeys < lo_all || (j + 1) * kKeys > hi_all)) {
+        // A NaN must not meet the zero weight of a row that does not see it (as in the
+        // decode kernel): blocks with such rows lose theirs here, and the rows that do
+        // see them get them in the end.
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&reg[i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bad = nan_codes(w[k]);
+            any |= bad;
+            w[k] &= ~((bad >> 7) * 0xFFu);
+          }
+        }
+        if (any) s_nan = 1;
       }
-      if (use > 0 && !wait(kVEmpty + st, use - 1)) break;
-      if (j * kKeys < lo_all || (j + 1) * kKeys > hi_all) take_nans(vreg);
-      widen(vreg, sbase + C::kV + st * C::kTileBytes);
-      mbar_arrive(bar(kVFull + st));
-      if (j + 1 < all.end) load(vreg, j + 1, v_base, kc.v_page_ld, kc.v_slot_ld);
+      const int next = (unit + 1) >> 1;
+      const bool more = unit + 1 < 2 * all.end;
+      if (is_v && more) {
+        look_up(next);
+        load_scales(next);
+      }
+      const uint8_t* base = is_v ? k_base : v_base;
+      const int64_t page_ld = is_v ? kc.k_page_ld : kc.v_page_ld, slot_ld = is_v ? kc.k_slot_ld : kc.v_slot_ld;
+      const uint32_t row = sbase + (is_v ? C::kV : C::kK) + st * C::kTileBytes + panel * 16384 + r0 * 128;
+      const uint32_t at_lo = row + (((2 * (t & 3)) ^ (r0 & 7)) << 4), at_hi = row + (((2 * (t & 3) + 1) ^ (r0 & 7)) << 4);
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const uint32_t w[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
+        if (more) load(i, next, base, page_ld, slot_ld);
+        uint4 lo, hi;
+        lo.x = e4m3x2_to_f16x2(w[0] & 0xFFFF); lo.y = e4m3x2_to_f16x2(w[0] >> 16);
+        lo.z = e4m3x2_to_f16x2(w[1] & 0xFFFF); lo.w = e4m3x2_to_f16x2(w[1] >> 16);
+        hi.x = e4m3x2_to_f16x2(w[2] & 0xFFFF); hi.y = e4m3x2_to_f16x2(w[2] >> 16);
+        hi.z = e4m3x2_to_f16x2(w[3] & 0xFFFF); hi.w = e4m3x2_to_f16x2(w[3] >> 16);
+        sts16(at_lo + i * kRowsPer * 128, lo);
+        sts16(at_hi + i * kRowsPer * 128, hi);
+      }
+      fence_proxy_async_shared();
+      mbar_arrive(bar((is_v ? kVFull : kKFull) + st));
     }
     if (bad_page) set_err(d.err, MOE_DEV_BAD_INDEX);
   } else if (wg < tiles) {
@@ -396,6 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       fence_proxy_async_shared();
       mbar_arrive(bar(kQFull));
     }
+    // with the caps, f is never so small that -inf (a key that is not seen) times f
+    // would be no number; scores that small are all 0 to fp32 anyway
+    if (qs < kMinQScale) qs = kMinQScale;
+    const auto score = [&](float x, float f, float add) {
+      if constexpr (CAP) return x == -INFINITY ? x : capped_log2(x * f, d.softcap * kLog2e) + add;
+      return fmaf(x, f, add);
+    };
     const int lo = first_key(d, s, i), hi = end_key(d, s, i);
     const int tile_r1 = min(rows, row0 + (wg + 1) * kTileRows) - 1;
     const int lo_last = first_key(d, s, tile_r1 / a.G), hi_first = end_key(d, s, (row0 + wg * kTileRows) / a.G);
@@ -410,13 +430,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       const uint32_t scale = sbase + C::kScale + ((j - all.first) & (kScaleSlots - 1)) * 128;
       const bool edge = j * kKeys < lo_last || (j + 1) * kKeys > hi_first;
       const int from = lo - j * kKeys, to_key = hi - j * kKeys;
-      const auto mask = [&](uint32_t (&x)[32], int k) {  // one branch, not one for each element
-        if (edge) {
+      if (edge) {
+        // -inf into S where a row does not see a key, once, so that the passes below
+        // stay small (their code is what the instruction caches hold)
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t x[32];
+          tmem_ld_32x32b_x32(ts + 32 * k, x);
+          tmem_ld_wait_for(x);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (32 * k + e < from || 32 * k + e >= to_key) x[e] = 0xFF800000u;
+          tmem_st_x32(ts + 32 * k, x);
         }
-      };
+        tmem_st_wait();
+      }
       // S is read twice, for the maximum and for the weights, 32 columns at a time and
       // the next ones under this one's arithmetic: TMEM has the bandwidth, and a thread
       // never holds its whole row.  A score is a function of S that does not fall within
@@ -425,22 +453,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       uint32_t xs[2][32];
       tmem_ld_32x32b_x32(ts, xs[0]);
       float best = -INFINITY;
+#pragma unroll 1
+      for (int k2 = 0; k2 < 4; k2 += 2) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t (&x)[32] = xs[k & 1];
-        tmem_ld_wait_for(x);
-        tmem_ld_32x32b_x32(ts + 32 * ((k + 1) & 3), xs[(k + 1) & 1]);
-        mask(x, k);
+        for (int k1 = 0; k1 < 2; ++k1) {
+          uint32_t (&x)[32] = xs[k1];
+          tmem_ld_wait_for(x);
+          tmem_ld_32x32b_x32(ts + 32 * ((k2 + k1 + 1) & 3), xs[k1 ^ 1]);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t* y = &x[half * 16];
-          float top16 = __uint_as_float(y[0]);
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t* y = &x[half * 16];
+            float top16 = __uint_as_float(y[0]);
 #pragma unroll
-          for (int e = 1; e < 15; e += 2)
-            top16 = fmaxf(fmaxf(top16, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
-          top16 = fmaxf(top16, __uint_as_float(y[15]));
-          const float4 sc = lds16f(scale + (2 * k + half) * 16);
-          best = fmaxf(best, CAP ? capped_log2(top16 * (qs * sc.x), d.softcap * kLog2e) + sc.y : fmaf(top16, qs * sc.x, sc.y));
+            for (int e = 1; e < 15; e += 2)
+              top16 = fmaxf(fmaxf(top16, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
+            top16 = fmaxf(top16, __uint_as_float(y[15]));
+            const float4 sc = lds16f(scale + (2 * (k2 + k1) + half) * 16);
+            best = fmaxf(best, score(top16, qs * sc.x, sc.y));
+          }
         }
       }
       if (__any_sync(0xffffffffu, best > top + kLazy)) {
@@ -464,47 +494,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           }
         }
       }
+#pragma unroll 1
+      for (int k2 = 0; k2 < 4; k2 += 2) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t (&x)[32] = xs[k & 1];
-        uint32_t p[16];
-        tmem_ld_wait_for(x);
-        if (k < 3) tmem_ld_32x32b_x32(ts + 32 * (k + 1), xs[(k + 1) & 1]);
-        float inv_scale[2];
+        for (int k1 = 0; k1 < 2; ++k1) {
+          uint32_t (&x)[32] = xs[k1];
+          uint32_t p[16];
+          tmem_ld_wait_for(x);
+          if (k2 + k1 < 3) tmem_ld_32x32b_x32(ts + 32 * (k2 + k1 + 1), xs[k1 ^ 1]);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float4 sc = lds16f(scale + (2 * k + half) * 16);
-          const float f = qs * sc.x, v = sc.y - ref;
-          const uint64_t f2 = f2_pack(f, f), v2 = f2_pack(v, v);
-          inv_scale[half] = sc.z;
+          for (int half = 0; half < 2; ++half) {
+            const float4 sc = lds16f(scale + (2 * (k2 + k1) + half) * 16);
+            const float f = qs * sc.x, v = sc.y - ref;
+            const uint64_t f2 = f2_pack(f, f), v2 = f2_pack(v, v);
+            uint64_t acc[2] = {0, 0};
 #pragma unroll
-          for (int e = 16 * half; e < 16 * half + 16; e += 2) {
-            float y0 = __uint_as_float(x[e]), y1 = __uint_as_float(x[e + 1]);
-            if constexpr (CAP) {
-              y0 = capped_log2(y0 * f, d.softcap * kLog2e) + v;
-              y1 = capped_log2(y1 * f, d.softcap * kLog2e) + v;
-            } else {
-              f2_unpack(f2_fma(f2_pack(y0, y1), f2, v2), y0, y1);
+            for (int e = 16 * half; e < 16 * half + 16; e += 2) {
+              float y0 = __uint_as_float(x[e]), y1 = __uint_as_float(x[e + 1]);
+              if constexpr (CAP) {
+                y0 = score(y0, f, v);
+                y1 = score(y1, f, v);
+              } else {
+                f2_unpack(f2_fma(f2_pack(y0, y1), f2, v2), y0, y1);
+              }
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              acc[(e >> 1) & 1] = f2_add(acc[(e >> 1) & 1], f2_pack(y0, y1));
+              p[e / 2] = f16x2(y0, y1);
             }
-            x[e] = __float_as_uint(y0);
-            x[e + 1] = __float_as_uint(y1);
+            float a0, a1;
+            f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+            sum = fmaf(a0 + a1, sc.z, sum);
           }
+          tmem_st_x16(ts + 16 * (k2 + k1), p);           // over columns that have been read
         }
-        mask(x, k);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint64_t acc[2] = {0, 0};
-#pragma unroll
-          for (int e = 16 * half; e < 16 * half + 16; e += 2) {
-            const float y0 = ex2(__uint_as_float(x[e])), y1 = ex2(__uint_as_float(x[e + 1]));
-            acc[(e >> 1) & 1] = f2_add(acc[(e >> 1) & 1], f2_pack(y0, y1));
-            p[e / 2] = f16x2(y0, y1);
-          }
-          float a0, a1;
-          f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
-          sum = fmaf(a0 + a1, inv_scale[half], sum);
-        }
-        tmem_st_x16(ts + 16 * k, p);                     // over columns that have been read
       }
       tmem_st_wait();
       tc_fence_before();
