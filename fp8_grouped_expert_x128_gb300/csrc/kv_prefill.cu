@@ -18,16 +18,17 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;             // two warpgroups of softmax, two that widen, one that issues
+constexpr int kWidenThreads = 256, kIssueWarp = 16;
+constexpr int kLaunchRegs = 96;           // registers a thread at launch, split over the warpgroups
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;               // keys per block
 constexpr int kStages = 2;               // of K and of V
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kMinQScale = 8.6736174e-19f, kMinKScale = 8.6736174e-19f;   // 2^-60 each
-// 512 * 128 registers at launch, split over the four warpgroups
-constexpr int kRegsSoftmax = 176, kRegsWiden = 96, kRegsIssue = 64;
-static_assert(256 * kRegsSoftmax + 128 * kRegsWiden + 128 * kRegsIssue <= kThreads * 128, "register split");
+constexpr int kRegsSoftmax = 144, kRegsWiden = 72, kRegsIssue = 48;
+static_assert(256 * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreads * kLaunchRegs, "register split");
 
 template <int D>
 struct Cfg {
@@ -191,13 +192,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     for (int i = 0; i < kBarCount; ++i) {
       const bool widen = i == kKFull || i == kKFull + 1 || i == kVFull || i == kVFull + 1;
       const bool soft = i == kPFull || i == kPFull + 1;
-      mbar_init(bar(i), i == kQFull ? 128 * tiles : widen || soft ? 128 : 1);
+      mbar_init(bar(i), i == kQFull ? 128 * tiles : widen ? kWidenThreads : soft ? 128 : 1);
     }
     s_abort = 0;
     s_nan = 0;
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     tmem_alloc(smem_u32(&s_tmem), kTmemCols);
     tmem_relinquish();
   }
@@ -207,9 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   const uint32_t tmem = s_tmem;
   const auto wait = [&](int i, int phase) { return mbar_wait_bounded(bar(i), phase & 1, abort, d.err, wait_ns); };
 
-  if (wg == 3) {
+  if (wg == 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 12) {
+    if (warp == kIssueWarp) {
       // ------------------------------------------------------------ MMA issue
       // Order per key block: for each tile, P V of the block before, then S of this
       // one over the space that P took (MMAs of one thread run in order).
@@ -267,38 +268,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       }
       __syncwarp();
     }
-  } else if (wg == 2) {
+  } else if (wg >= 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
     // ------------------------------------------------------------ widening of K and V
-    constexpr int kChunks = D / 16;                    // 16-code chunks of a row
-    constexpr int kRowsPer = 128 / kChunks;            // rows the warpgroup takes at a time
+    constexpr int kRowsPer = kWidenThreads / (D / 16);  // rows the two warpgroups take at a time
     constexpr int kIter = kKeys / kRowsPer;
     // four lanes take half a 128-byte row of codes, the next four that of the next row:
     // their stores then fall on all banks, whatever the swizzle
-    const int t = tid & 127, panel = (t >> 5) & (C::kPanels - 1);
+    const int t = tid - 256, panel = (t >> 5) & (C::kPanels - 1);
     const int r0 = ((t >> 2) & 7) | (t >> (C::kPanels == 2 ? 6 : 5)) << 3, ch = panel * 4 + (t & 3);
     const int hi_all = end_key(d, s, row0 / a.G), lo_all = first_key(d, s, (row_end - 1) / a.G);
-    uint4 reg[kIter];
-    int pages = 0, pages_from = -1;                    // page of 16-key group pages_from + lane
+    // page of 16-key group pages_from + lane (whole blocks: 32 groups from a multiple
+    // of 8), and of the 32 groups after those
+    int pages_from = all.first * 8, pages, pages_next;
     bool bad_page = false;
-    const auto look_up = [&](int j) {                  // 32 groups from a multiple of 8: whole blocks
-      if (pages_from >= 0 && j * 8 - pages_from < 32) return;
-      pages_from = j * 8;
-      const int key = (pages_from + lane) << 4;
-      pages = key < s.len ? __ldg(kc.page_table + b * kc.table_ld + (key >> page_shift)) : 0;
-      if (pages < 0 || pages >= kc.pages) {
+    const auto look_up = [&](int from) {
+      const int key = (from + lane) << 4;
+      int page = key < s.len ? __ldg(kc.page_table + b * kc.table_ld + (key >> page_shift)) : 0;
+      if (page < 0 || page >= kc.pages) {
         bad_page = true;
-        pages = -1;
+        page = -1;
       }
+      return page;
     };
-    const auto load = [&](int i, int j, const uint8_t* base, int64_t page_ld, int64_t slot_ld) {
+    pages = look_up(pages_from);
+    pages_next = look_up(pages_from + 32);
+    uint4 reg[2][kIter];                               // K's and V's codes, loaded a block ahead
+    const auto load = [&](uint4& r, int i, int j, const uint8_t* base, int64_t page_ld, int64_t slot_ld) {
       const int key = j * kKeys + i * kRowsPer + r0;
       const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
       // past the end, or a page that is none: zeros
-      reg[i] = ldg_stream(base + page * page_ld + (key & (P - 1)) * slot_ld, key < s.len && page >= 0);
+      r = ldg_stream(base + page * page_ld + (key & (P - 1)) * slot_ld, key < s.len && page >= 0);
     };
-    const uint8_t* k_base = kc.k + h * kc.k_head_ld + ch * 16;
-    const uint8_t* v_base = kc.v + h * kc.v_head_ld + ch * 16;
+    const uint8_t* base[2] = {kc.k + h * kc.k_head_ld + ch * 16, kc.v + h * kc.v_head_ld + ch * 16};
     // scales of a block's 16-key groups, by the first warp's first lanes: (K, V)
     float2 scales;
     const auto load_scales = [&](int j) {
@@ -310,64 +312,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         scales = make_float2(__ldg(kc.k_scale + at), __ldg(kc.v_scale + at));
       }
     };
-    // K and V blocks in turn; as a register is widened, the next unit's load goes
-    // into it, so half a block's time hides the loads.
-    look_up(all.first);
     load_scales(all.first);
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) load(i, all.first, k_base, kc.k_page_ld, kc.k_slot_ld);
+    for (int i = 0; i < kIter; ++i) load(reg[0][i], i, all.first, base[0], kc.k_page_ld, kc.k_slot_ld);
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) load(reg[1][i], i, all.first, base[1], kc.v_page_ld, kc.v_slot_ld);
+    bool ok = true;
 #pragma unroll 1
-    for (int unit = 2 * all.first; unit < 2 * all.end; ++unit) {
-      const int j = unit >> 1, n = j - all.first, st = n & 1, use = n >> 1;
-      const bool is_v = unit & 1;
-      if (use > 0 && !wait((is_v ? kVEmpty : kKEmpty) + st, use - 1)) break;
-      if (!is_v && t < 8) {
-        // the V scale as its logarithm and inverse, which is what the weights take
-        const float k = fmaxf(scales.x, kMinKScale), v = fmaxf(scales.y, kMinScale);
-        *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + t) * 16) =
-            make_float4(k, __log2f(v), __fdividef(1.0f, v), 0.0f);
+    for (int j = all.first; ok && j < all.end; ++j) {
+      const int n = j - all.first, st = n & 1, use = n >> 1;
+      const bool more = j + 1 < all.end;
+      float2 now = scales;
+      if (more) {
+        if ((j + 1) * 8 - pages_from == 32) {
+          pages_from += 32;
+          pages = pages_next;
+          pages_next = look_up(pages_from + 32);
+        }
+        load_scales(j + 1);
       }
-      if (is_v && (j * kKeys < lo_all || (j + 1) * kKeys > hi_all)) {
-        // A NaN must not meet the zero weight of a row that does not see it (as in the
-        // decode kernel): blocks with such rows lose theirs here, and the rows that do
-        // see them get them in the end.
-        uint32_t any = 0;
+#pragma unroll
+      for (int is_v = 0; is_v < 2; ++is_v) {
+        if (use > 0) ok = ok && wait((is_v ? kVEmpty : kKEmpty) + st, use - 1);
+        if (!ok) break;
+        if (!is_v && t < 8) {
+          // the V scale as its logarithm and inverse, which is what the weights take
+          const float k = fmaxf(now.x, kMinKScale), v = fmaxf(now.y, kMinScale);
+          *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + t) * 16) =
+              make_float4(k, __log2f(v), __fdividef(1.0f, v), 0.0f);
+        }
+        if (is_v && (j * kKeys < lo_all || (j + 1) * kKeys > hi_all)) {
+          // A NaN must not meet the zero weight of a row that does not see it (as in the
+          // decode kernel): blocks with such rows lose theirs here, and the rows that do
+          // see them get them in the end.
+          uint32_t any = 0;
+#pragma unroll
+          for (int i = 0; i < kIter; ++i) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&reg[is_v][i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t bad = nan_codes(w[k]);
+              any |= bad;
+              w[k] &= ~((bad >> 7) * 0xFFu);
+            }
+          }
+          if (any) s_nan = 1;
+        }
+        const uint32_t row = sbase + (is_v ? C::kV : C::kK) + st * C::kTileBytes + panel * 16384 + r0 * 128;
+        const uint32_t at_lo = row + (((2 * (t & 3)) ^ (r0 & 7)) << 4), at_hi = row + (((2 * (t & 3) + 1) ^ (r0 & 7)) << 4);
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&reg[i]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t bad = nan_codes(w[k]);
-            any |= bad;
-            w[k] &= ~((bad >> 7) * 0xFFu);
-          }
+          const uint4 w = reg[is_v][i];
+          if (more)
+            load(reg[is_v][i], i, j + 1, base[is_v], is_v ? kc.v_page_ld : kc.k_page_ld, is_v ? kc.v_slot_ld : kc.k_slot_ld);
+          sts16(at_lo + i * kRowsPer * 128,
+                make_uint4(e4m3x2_to_f16x2(w.x & 0xFFFF), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y & 0xFFFF),
+                           e4m3x2_to_f16x2(w.y >> 16)));
+          sts16(at_hi + i * kRowsPer * 128,
+                make_uint4(e4m3x2_to_f16x2(w.z & 0xFFFF), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w & 0xFFFF),
+                           e4m3x2_to_f16x2(w.w >> 16)));
         }
-        if (any) s_nan = 1;
+        fence_proxy_async_shared();
+        mbar_arrive(bar((is_v ? kVFull : kKFull) + st));
       }
-      const int next = (unit + 1) >> 1;
-      const bool more = unit + 1 < 2 * all.end;
-      if (is_v && more) {
-        look_up(next);
-        load_scales(next);
-      }
-      const uint8_t* base = is_v ? k_base : v_base;
-      const int64_t page_ld = is_v ? kc.k_page_ld : kc.v_page_ld, slot_ld = is_v ? kc.k_slot_ld : kc.v_slot_ld;
-      const uint32_t row = sbase + (is_v ? C::kV : C::kK) + st * C::kTileBytes + panel * 16384 + r0 * 128;
-      const uint32_t at_lo = row + (((2 * (t & 3)) ^ (r0 & 7)) << 4), at_hi = row + (((2 * (t & 3) + 1) ^ (r0 & 7)) << 4);
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const uint32_t w[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
-        if (more) load(i, next, base, page_ld, slot_ld);
-        uint4 lo, hi;
-        lo.x = e4m3x2_to_f16x2(w[0] & 0xFFFF); lo.y = e4m3x2_to_f16x2(w[0] >> 16);
-        lo.z = e4m3x2_to_f16x2(w[1] & 0xFFFF); lo.w = e4m3x2_to_f16x2(w[1] >> 16);
-        hi.x = e4m3x2_to_f16x2(w[2] & 0xFFFF); hi.y = e4m3x2_to_f16x2(w[2] >> 16);
-        hi.z = e4m3x2_to_f16x2(w[3] & 0xFFFF); hi.w = e4m3x2_to_f16x2(w[3] >> 16);
-        sts16(at_lo + i * kRowsPer * 128, lo);
-        sts16(at_hi + i * kRowsPer * 128, hi);
-      }
-      fence_proxy_async_shared();
-      mbar_arrive(bar((is_v ? kVFull : kKFull) + st));
     }
     if (bad_page) set_err(d.err, MOE_DEV_BAD_INDEX);
   } else if (wg < tiles) {
@@ -584,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -600,7 +607,7 @@ int launch(const AttnArgs& a, cudaStream_t st) {
     // the register split counts on exactly the launch allocation
     cudaFuncAttributes attr;
     MOE_CUDA_TRY(cudaFuncGetAttributes(&attr, kernel));
-    if (attr.numRegs * kThreads != 65536) return MOE_ERR_UNSUPPORTED;
+    if (attr.numRegs != kLaunchRegs) return MOE_ERR_UNSUPPORTED;
     MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem));
     __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
   }
