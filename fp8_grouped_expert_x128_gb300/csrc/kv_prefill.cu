@@ -27,7 +27,7 @@ constexpr int kStages = 2;               // of K and of V
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kMinQScale = 8.6736174e-19f, kMinKScale = 8.6736174e-19f;   // 2^-60 each
-constexpr int kRegsSoftmax = 144, kRegsWiden = 72, kRegsIssue = 48;
+constexpr int kRegsSoftmax = 152, kRegsWiden = 72, kRegsIssue = 32;
 static_assert(256 * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreads * kLaunchRegs, "register split");
 
 template <int D>
@@ -45,7 +45,7 @@ struct Cfg {
 
 // mbarriers, in order
 enum { kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
-       kPFull = kSFull + 2, kOFull = kPFull + 2, kBarCount = kOFull + 2 };
+       kPFull = kSFull + 2, kOFull = kPFull + 4, kBarCount = kOFull + 2 };
 
 // Instruction descriptor, kind::f16: D fp32, A and B f16, A K-major; B K-major or
 // (mn) with its N dimension contiguous.
@@ -123,6 +123,12 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// y, but -inf where x is (a select, not a branch).
+__device__ __forceinline__ float keep_hidden(float x, float y) {
+  float r;
+  asm("{\n\t.reg .pred p;\n\tsetp.eq.f32 p, %1, 0fFF800000;\n\tselp.f32 %0, %1, %2, p;\n\t}" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
 // 16 bytes read once by this CTA (no place in L1, what shared memory leaves of
 // it), or zeros without a read; no branch either way.
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p, bool on) {
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
       const bool widen = i == kKFull || i == kKFull + 1 || i == kVFull || i == kVFull + 1;
-      const bool soft = i == kPFull || i == kPFull + 1;
+      const bool soft = i >= kPFull && i < kPFull + 4;
       mbar_init(bar(i), i == kQFull ? 128 * tiles : widen ? kWidenThreads : soft ? 128 : 1);
     }
     s_abort = 0;
@@ -229,14 +235,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           if (ok && j > m.first && j <= m.end) {
             if (!have_v) ok = wait(kVFull + vst, vph);
             have_v = true;
-            ok = __all_sync(0xffffffffu, ok && wait(kPFull + i, done[i] - 1));
-            if (!ok) break;
-            tc_fence_after();
             const uint32_t vd = desc_lo(sbase + C::kV + vst * C::kTileBytes, 16384);
             const uint32_t acc = done[i] > 1;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + 8 * k, vd + 128 * k, id_o, k > 0 ? 1u : acc, lead);
+            for (int part = 0; part < 2; ++part) {       // the first 64 keys' weights while the others are made
+              ok = __all_sync(0xffffffffu, ok && wait(kPFull + 2 * i + part, done[i] - 1));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = part * 4; k < part * 4 + 4; ++k)
+                mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + 8 * k, vd + 128 * k, id_o, k > 0 ? 1u : acc, lead);
+            }
+            if (!ok) break;
             commit(bar(kOFull + i), lead);
           }
           if (ok && j < all.end && j >= m.first && j < m.end) {
@@ -386,33 +396,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     const int i = min(r, rows - 1) / a.G, head = h * a.G + min(r, rows - 1) - i * a.G;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // this warp's TMEM lanes (bits 16 and up)
     const uint32_t ts = tmem + lanes + wg * 128, to = tmem + lanes + C::kTmemO + wg * D;
-    float qs;
+    float qs = 0.0f;
     {
-      const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d.q) + (s.c0 + i) * d.q_token_ld +
-                                                       head * d.q_head_ld);
-      const uint32_t tile = sbase + C::kQ + wg * C::kTileBytes + t * 128;
-      uint4 w[D / 8];
-      float amax = 0.0f;
+      // Each warp brings its 32 rows in, kLanes lanes to a row, all loads in flight at once.
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+      uint4 w[kLanes];
+      const int sub = lane / kLanes, c16 = lane % kLanes;              // row of a group, 16-byte chunk of the row
+      const int first = row0 + wg * kTileRows + (warp & 3) * 32;
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        w[k] = live ? __ldg(qp + k) : make_uint4(0, 0, 0, 0);
-        float f[8];
+      for (int k = 0; k < kLanes; ++k) {
+        const int rr = min(first + k * kAtOnce + sub, rows - 1), ii = rr / a.G;
+        w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d.q) + (s.c0 + ii) * d.q_token_ld +
+                                                    (h * a.G + rr - ii * a.G) * d.q_head_ld) + c16);
+      }
+      const uint32_t tile = sbase + C::kQ + wg * C::kTileBytes + (c16 >> 3) * 16384;
+#pragma unroll
+      for (int k = 0; k < kLanes; ++k) {
+        float f[8], amax = 0.0f;
         unpack8<F16>(w[k], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = f[e] != f[e] ? INFINITY : fmaxf(amax, fabsf(f[e]));
-      }
-      float mul, inv;
-      row_scale(amax, mul, inv);
-      mul = copysignf(mul, d.sm_scale);
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        float f[8];
-        unpack8<F16>(w[k], f);
-        sts16(tile + (k >> 3) * 16384 + (((k & 7) ^ (t & 7)) << 4),
+        for (int x = 1; x < kLanes; x <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
+        float mul, inv;
+        row_scale(amax, mul, inv);
+        // row lane belongs to group lane / kAtOnce, there to the lanes from lane % kAtOnce * kLanes on
+        const float got = __shfl_sync(0xffffffffu, inv, lane % kAtOnce * kLanes);
+        if (lane / kAtOnce == k) qs = got;
+        mul = copysignf(mul, d.sm_scale);
+        const int row = (warp & 3) * 32 + k * kAtOnce + sub;           // of the tile
+        sts16(tile + row * 128 + (((c16 & 7) ^ (row & 7)) << 4),
               make_uint4(f16x2(f[0] * mul, f[1] * mul), f16x2(f[2] * mul, f[3] * mul), f16x2(f[4] * mul, f[5] * mul),
                          f16x2(f[6] * mul, f[7] * mul)));
       }
-      qs = inv * fabsf(CAP ? d.sm_scale / d.softcap : d.sm_scale * kLog2e);
+      qs *= fabsf(CAP ? d.sm_scale / d.softcap : d.sm_scale * kLog2e);
       fence_proxy_async_shared();
       mbar_arrive(bar(kQFull));
     }
@@ -420,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     // would be no number; scores that small are all 0 to fp32 anyway
     if (qs < kMinQScale) qs = kMinQScale;
     const auto score = [&](float x, float f, float add) {
-      if constexpr (CAP) return x == -INFINITY ? x : capped_log2(x * f, d.softcap * kLog2e) + add;
+      if constexpr (CAP) return keep_hidden(x, capped_log2(x * f, d.softcap * kLog2e) + add);
       return fmaf(x, f, add);
     };
     const int lo = first_key(d, s, i), hi = end_key(d, s, i);
@@ -535,10 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           }
           tmem_st_x16(ts + 16 * (k2 + k1), p);           // over columns that have been read
         }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull + 2 * wg + (k2 >> 1)));
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(bar(kPFull + wg));
     }
     if (ok) ok = wait(kOFull + wg, m.end - m.first - 1);
     if (ok) {
