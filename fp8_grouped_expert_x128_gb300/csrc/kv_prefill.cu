@@ -22,8 +22,9 @@ constexpr int kThreads = 640;             // two warpgroups of softmax, two that
 constexpr int kWidenThreads = 256, kIssueWarp = 16;
 constexpr int kLaunchRegs = 96;           // registers a thread at launch, split over the warpgroups
 constexpr int kTileRows = 128;
-constexpr int kKeys = 128;               // keys per block
-constexpr int kStages = 2;               // of K and of V
+constexpr int kKeys = 64;                // keys per step of a tile
+constexpr int kBlock = 128;              // keys widened at a time
+constexpr int kStages = 2;               // of K and of V blocks
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kMinQScale = 8.6736174e-19f, kMinKScale = 8.6736174e-19f;   // 2^-60 each
@@ -43,9 +44,10 @@ struct Cfg {
   static constexpr uint32_t kTmemO = 256;              // S0, S1 (and P over them) at 0, 128; O0, O1 here
 };
 
-// mbarriers, in order
+// mbarriers, in order.  S, P and O have one for each buffer of a tile: two steps can be
+// under way, and a barrier must not get two phases ahead of who waits for it.
 enum { kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
-       kPFull = kSFull + 2, kOFull = kPFull + 4, kBarCount = kOFull + 2 };
+       kPFull = kSFull + 4, kOFull = kPFull + 4, kBarCount = kOFull + 4 };
 
 // Instruction descriptor, kind::f16: D fp32, A and B f16, A K-major; B K-major or
 // (mn) with its N dimension contiguous.
@@ -89,16 +91,10 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e;
 }
-__device__ __forceinline__ void tmem_st_x32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+__device__ __forceinline__ void tmem_st_x8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -116,6 +112,11 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&x)[32]) {
                  "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]),
                  "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]),
                  "+r"(x[30]), "+r"(x[31])::"memory");
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&x)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])::"memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
@@ -148,11 +149,11 @@ __device__ __forceinline__ float4 lds16f(uint32_t a) {
   return v;
 }
 
-// Key blocks [first, end) that the rows [r0, r1) of a sequence see.
-struct Blocks {
+// Steps [first, end) of kKeys keys that the rows [r0, r1) of a sequence see.
+struct Steps {
   int first, end;
 };
-__device__ __forceinline__ Blocks blocks_of(const AttnArgs& a, const Seq& s, int r0, int r1) {
+__device__ __forceinline__ Steps steps_of(const AttnArgs& a, const Seq& s, int r0, int r1) {
   return {first_key(a.d, s, r0 / a.G) / kKeys, (end_key(a.d, s, (r1 - 1) / a.G) + kKeys - 1) / kKeys};
 }
 
@@ -185,9 +186,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   if (nth < 0 || nth >= tiles2) return;
   const int row0 = nth * 2 * kTileRows, row_end = min(rows, row0 + 2 * kTileRows);
   const int tiles = row_end - row0 > kTileRows ? 2 : 1;
-  const Blocks all = blocks_of(a, s, row0, row_end);
-  const Blocks mine0 = blocks_of(a, s, row0, min(row0 + kTileRows, row_end));
-  const Blocks mine1 = tiles == 2 ? blocks_of(a, s, row0 + kTileRows, row_end) : Blocks{all.end, all.end};
+  const Steps all = steps_of(a, s, row0, row_end);
+  const Steps mine0 = steps_of(a, s, row0, min(row0 + kTileRows, row_end));
+  const Steps mine1 = tiles == 2 ? steps_of(a, s, row0 + kTileRows, row_end) : Steps{all.end, all.end};
+  const int block0 = all.first >> 1, block1 = (all.end + 1) >> 1;   // blocks to widen
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -218,58 +220,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == kIssueWarp) {
       // ------------------------------------------------------------ MMA issue
-      // Order per key block: for each tile, P V of the block before, then S of this
-      // one over the space that P took (MMAs of one thread run in order).
+      // S has two buffers a tile: step g + 2 goes where step g was.  Per step and tile:
+      // P V of step g, then S of step g + 2 over the space that its P took (MMAs of one
+      // thread run in order), so that S of step g + 1 is there when its softmax begins.
       const uint32_t id_s = idesc_f16(kKeys, false), id_o = idesc_f16(D, true);
       const uint32_t lead = elect_one();
-      bool ok = __all_sync(0xffffffffu, wait(kQFull, 0));
-      int done[2] = {0, 0};              // blocks of each tile whose S has been issued
+      bool ok = __all_sync(0xffffffffu, wait(kQFull, 0)), any = false;
+      int k_at = block0 - 1, v_at = block0 - 1;            // last blocks that were waited for
 #pragma unroll 1
-      for (int j = all.first; ok && j <= all.end; ++j) {
-        const int kst = (j - all.first) & 1, kph = (j - all.first) >> 1;
-        const int vst = kst ^ 1, vph = (j - 1 - all.first) >> 1;
-        bool have_k = false, have_v = false;
+      for (int g = all.first - 2; ok && g < all.end; ++g) {
+        const int buf = g & 1, x = g + 2;
+        const int vst = ((g >> 1) - block0) & 1, kst = ((x >> 1) - block0) & 1;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const Blocks m = i ? mine1 : mine0;
-          if (ok && j > m.first && j <= m.end) {
-            if (!have_v) ok = wait(kVFull + vst, vph);
-            have_v = true;
-            const uint32_t vd = desc_lo(sbase + C::kV + vst * C::kTileBytes, 16384);
-            const uint32_t acc = done[i] > 1;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {       // the first 64 keys' weights while the others are made
-              ok = __all_sync(0xffffffffu, ok && wait(kPFull + 2 * i + part, done[i] - 1));
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = part * 4; k < part * 4 + 4; ++k)
-                mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + 8 * k, vd + 128 * k, id_o, k > 0 ? 1u : acc, lead);
+          const Steps m = i ? mine1 : mine0;
+          if (ok && g >= m.first && g < m.end) {
+            if (v_at < (g >> 1)) {
+              v_at = g >> 1;
+              ok = wait(kVFull + vst, (v_at - block0) >> 1);
             }
-            if (!ok) break;
-            commit(bar(kOFull + i), lead);
-          }
-          if (ok && j < all.end && j >= m.first && j < m.end) {
-            if (!have_k) ok = __all_sync(0xffffffffu, wait(kKFull + kst, kph));
-            have_k = true;
+            ok = __all_sync(0xffffffffu, ok && wait(kPFull + 2 * i + buf, (g - m.first) >> 1));
             if (!ok) break;
             tc_fence_after();
+            const uint32_t vd = desc_lo(sbase + C::kV + vst * C::kTileBytes + buf * kKeys * 128, 16384);
+            const uint32_t acc = g > m.first;
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + buf * kKeys + 8 * k, vd + 128 * k, id_o, k > 0 ? 1u : acc, lead);
+            commit(bar(kOFull + 2 * i + buf), lead);
+          }
+          if (ok && x >= m.first && x < m.end) {
+            if (k_at < (x >> 1)) {
+              k_at = x >> 1;
+              ok = __all_sync(0xffffffffu, wait(kKFull + kst, (k_at - block0) >> 1));
+              if (!ok) break;
+              tc_fence_after();
+            }
             const uint32_t qd = desc_lo(sbase + C::kQ + i * C::kTileBytes, 16);
-            const uint32_t kd = desc_lo(sbase + C::kK + kst * C::kTileBytes, 16);
+            const uint32_t kd = desc_lo(sbase + C::kK + kst * C::kTileBytes + buf * kKeys * 128, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t at = (k >> 2) * 1024 + (k & 3) * 2;
-              mma_ss(tmem + i * 128, qd + at, kd + at, id_s, k > 0 ? 1u : 0u, lead);
+              mma_ss(tmem + i * 128 + buf * kKeys, qd + at, kd + at, id_s, k > 0 ? 1u : 0u, lead);
             }
-            commit(bar(kSFull + i), lead);
-            ++done[i];
+            commit(bar(kSFull + 2 * i + buf), lead);
+            any = true;
           }
         }
         if (!ok) break;
-        if (j > all.first) commit(bar(kVEmpty + vst), lead);
-        if (j < all.end) commit(bar(kKEmpty + kst), lead);
+        if (g >= all.first && (buf || g == all.end - 1)) commit(bar(kVEmpty + vst), lead);
+        if (x < all.end && (buf || x == all.end - 1)) commit(bar(kKEmpty + kst), lead);
       }
-      if (!ok && done[0] + done[1] > 0 && lead) {
+      if (!ok && any && lead) {
         // the MMAs in flight end before TMEM is freed: the commit below follows them
         int dummy = 0;
         umma_commit(bar(kQFull));        // completes phase 1 of a barrier that nobody else waits on any more
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
     // ------------------------------------------------------------ widening of K and V
     constexpr int kRowsPer = kWidenThreads / (D / 16);  // rows the two warpgroups take at a time
-    constexpr int kIter = kKeys / kRowsPer;
+    constexpr int kIter = kBlock / kRowsPer;
     // four lanes take half a 128-byte row of codes, the next four that of the next row:
     // their stores then fall on all banks, whatever the swizzle
     const int t = tid - 256, panel = (t >> 5) & (C::kPanels - 1);
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     const int hi_all = end_key(d, s, row0 / a.G), lo_all = first_key(d, s, (row_end - 1) / a.G);
     // page of 16-key group pages_from + lane (whole blocks: 32 groups from a multiple
     // of 8), and of the 32 groups after those
-    int pages_from = all.first * 8, pages, pages_next;
+    int pages_from = block0 * 8, pages, pages_next;
     bool bad_page = false;
     const auto look_up = [&](int from) {
       const int key = (from + lane) << 4;
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     pages_next = look_up(pages_from + 32);
     uint4 reg[2][kIter];                               // K's and V's codes, loaded a block ahead
     const auto load = [&](uint4& r, int i, int j, const uint8_t* base, int64_t page_ld, int64_t slot_ld) {
-      const int key = j * kKeys + i * kRowsPer + r0;
+      const int key = j * kBlock + i * kRowsPer + r0;
       const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
       // past the end, or a page that is none: zeros
       r = ldg_stream(base + page * page_ld + (key & (P - 1)) * slot_ld, key < s.len && page >= 0);
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     // scales of a block's 16-key groups, by the first warp's first lanes: (K, V)
     float2 scales;
     const auto load_scales = [&](int j) {
-      const int key = j * kKeys + (lane & 7) * 16;
+      const int key = j * kBlock + (lane & 7) * 16;
       const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
       scales = make_float2(0.0f, 0.0f);
       if (t < 8 && key < s.len && page >= 0) {
@@ -322,16 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         scales = make_float2(__ldg(kc.k_scale + at), __ldg(kc.v_scale + at));
       }
     };
-    load_scales(all.first);
+    load_scales(block0);
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) load(reg[0][i], i, all.first, base[0], kc.k_page_ld, kc.k_slot_ld);
+    for (int i = 0; i < kIter; ++i) load(reg[0][i], i, block0, base[0], kc.k_page_ld, kc.k_slot_ld);
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) load(reg[1][i], i, all.first, base[1], kc.v_page_ld, kc.v_slot_ld);
+    for (int i = 0; i < kIter; ++i) load(reg[1][i], i, block0, base[1], kc.v_page_ld, kc.v_slot_ld);
     bool ok = true;
 #pragma unroll 1
-    for (int j = all.first; ok && j < all.end; ++j) {
-      const int n = j - all.first, st = n & 1, use = n >> 1;
-      const bool more = j + 1 < all.end;
+    for (int j = block0; ok && j < block1; ++j) {
+      const int n = j - block0, st = n & 1, use = n >> 1;
+      const bool more = j + 1 < block1;
       float2 now = scales;
       if (more) {
         if ((j + 1) * 8 - pages_from == 32) {
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + t) * 16) =
               make_float4(k, __log2f(v), __fdividef(1.0f, v), 0.0f);
         }
-        if (is_v && (j * kKeys < lo_all || (j + 1) * kKeys > hi_all)) {
+        if (is_v && (j * kBlock < lo_all || (j + 1) * kBlock > hi_all)) {
           // A NaN must not meet the zero weight of a row that does not see it (as in the
           // decode kernel): blocks with such rows lose theirs here, and the rows that do
           // see them get them in the end.
@@ -403,11 +405,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       uint4 w[kLanes];
       const int sub = lane / kLanes, c16 = lane % kLanes;              // row of a group, 16-byte chunk of the row
       const int first = row0 + wg * kTileRows + (warp & 3) * 32;
+      // (token, head) of each row: one division, and then small ones by a reciprocal
+      // ((x + 1/2) / G in fp32 has the right whole part for x < G + 32 < 2^17)
+      const int i0 = min(first, rows - 1) / a.G, g0 = min(first, rows - 1) - i0 * a.G;
+      const float inv_g = 1.0f / static_cast<float>(a.G);
 #pragma unroll
       for (int k = 0; k < kLanes; ++k) {
-        const int rr = min(first + k * kAtOnce + sub, rows - 1), ii = rr / a.G;
-        w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d.q) + (s.c0 + ii) * d.q_token_ld +
-                                                    (h * a.G + rr - ii * a.G) * d.q_head_ld) + c16);
+        const int x = min(g0 + k * kAtOnce + sub, g0 + max(rows - 1 - first, 0));
+        const int up = static_cast<int>((static_cast<float>(x) + 0.5f) * inv_g);
+        w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d.q) + (s.c0 + i0 + up) * d.q_token_ld +
+                                                    (h * a.G + x - up * a.G) * d.q_head_ld) + c16);
       }
       const uint32_t tile = sbase + C::kQ + wg * C::kTileBytes + (c16 >> 3) * 16384;
 #pragma unroll
@@ -443,59 +450,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     const int lo = first_key(d, s, i), hi = end_key(d, s, i);
     const int tile_r1 = min(rows, row0 + (wg + 1) * kTileRows) - 1;
     const int lo_last = first_key(d, s, tile_r1 / a.G), hi_first = end_key(d, s, (row0 + wg * kTileRows) / a.G);
-    const Blocks m = wg ? mine1 : mine0;
+    const Steps m = wg ? mine1 : mine0;
     float top = -INFINITY, ref = 0.0f, sum = 0.0f;       // running reference (ref: the same, 0 while -inf) and sum
     bool ok = true;
-    for (int j = m.first; j < m.end; ++j) {
-      const int n = j - m.first;
-      ok = wait(kSFull + wg, n);
+#pragma unroll 1
+    for (int g = m.first; g < m.end; ++g) {
+      const int n = g - m.first, buf = g & 1;
+      ok = wait(kSFull + 2 * wg + buf, n >> 1);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t scale = sbase + C::kScale + ((j - all.first) & (kScaleSlots - 1)) * 128;
-      const bool edge = j * kKeys < lo_last || (j + 1) * kKeys > hi_first;
-      const int from = lo - j * kKeys, to_key = hi - j * kKeys;
-      if (edge) {
-        // -inf into S where a row does not see a key, once, so that the passes below
-        // stay small (their code is what the instruction caches hold)
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t x[32];
-          tmem_ld_32x32b_x32(ts + 32 * k, x);
-          tmem_ld_wait_for(x);
+      uint32_t x[2][32];
+      const uint32_t at = ts + buf * kKeys;
+      tmem_ld_32x32b_x32(at, x[0]);
+      tmem_ld_32x32b_x32(at + 32, x[1]);
+      const uint32_t scale = sbase + C::kScale + (((g >> 1) - block0) & (kScaleSlots - 1)) * 128 + buf * 64;
+      const bool edge = g * kKeys < lo_last || (g + 1) * kKeys > hi_first;
+      tmem_ld_wait_for(x[0]);
+      tmem_ld_wait_for(x[1]);
+      if (edge) {                          // one branch, not one for each element
+        const uint32_t from = lo - g * kKeys, seen = hi - lo;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * k + e < from || 32 * k + e >= to_key) x[e] = 0xFF800000u;
-          tmem_st_x32(ts + 32 * k, x);
-        }
-        tmem_st_wait();
+        for (uint32_t e = 0; e < kKeys; ++e)
+          if (e - from >= seen) x[e >> 5][e & 31] = 0xFF800000u;
       }
-      // S is read twice, for the maximum and for the weights, 32 columns at a time and
-      // the next ones under this one's arithmetic: TMEM has the bandwidth, and a thread
-      // never holds its whole row.  A score is a function of S that does not fall within
-      // a group of one scale (q has taken sm_scale's sign), so the maximum needs it once
-      // for each group.
-      uint32_t xs[2][32];
-      tmem_ld_32x32b_x32(ts, xs[0]);
+      // A score is a function of S that does not fall within a group of one scale (q has
+      // taken sm_scale's sign), so the maximum needs it once for each group.
       float best = -INFINITY;
-#pragma unroll 1
-      for (int k2 = 0; k2 < 4; k2 += 2) {
 #pragma unroll
-        for (int k1 = 0; k1 < 2; ++k1) {
-          uint32_t (&x)[32] = xs[k1];
-          tmem_ld_wait_for(x);
-          tmem_ld_32x32b_x32(ts + 32 * ((k2 + k1 + 1) & 3), xs[k1 ^ 1]);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t* y = &x[k >> 1][(k & 1) * 16];
+        float top16 = __uint_as_float(y[0]);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t* y = &x[half * 16];
-            float top16 = __uint_as_float(y[0]);
-#pragma unroll
-            for (int e = 1; e < 15; e += 2)
-              top16 = fmaxf(fmaxf(top16, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
-            top16 = fmaxf(top16, __uint_as_float(y[15]));
-            const float4 sc = lds16f(scale + (2 * (k2 + k1) + half) * 16);
-            best = fmaxf(best, score(top16, qs * sc.x, sc.y));
-          }
-        }
+        for (int e = 1; e < 15; e += 2)
+          top16 = fmaxf(fmaxf(top16, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
+        top16 = fmaxf(top16, __uint_as_float(y[15]));
+        const float4 sc = lds16f(scale + k * 16);
+        best = fmaxf(best, score(top16, qs * sc.x, sc.y));
       }
       if (__any_sync(0xffffffffu, best > top + kLazy)) {
         const float next = best > top + kLazy ? best : top;
@@ -504,60 +494,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         ref = next == -INFINITY ? 0.0f : next;
         sum *= keep;
         if (n > 0) {
-          ok = wait(kOFull + wg, n - 1);                 // P V of the block before is in
+          ok = wait(kOFull + 2 * wg + (buf ^ 1), (n - 1) >> 1);          // P V of the step before is in
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(to + 32 * k, o);
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(to + 16 * k, o);
             tmem_ld_wait_for(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-            tmem_st_x32(to + 32 * k, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+            tmem_st_x16(to + 16 * k, o);
           }
         }
       }
-#pragma unroll 1
-      for (int k2 = 0; k2 < 4; k2 += 2) {
 #pragma unroll
-        for (int k1 = 0; k1 < 2; ++k1) {
-          uint32_t (&x)[32] = xs[k1];
-          uint32_t p[16];
-          tmem_ld_wait_for(x);
-          if (k2 + k1 < 3) tmem_ld_32x32b_x32(ts + 32 * (k2 + k1 + 1), xs[k1 ^ 1]);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t p[8];
+        const float4 sc = lds16f(scale + k * 16);
+        const float f = qs * sc.x, v = sc.y - ref;
+        const uint64_t f2 = f2_pack(f, f), v2 = f2_pack(v, v);
+        uint64_t acc[2] = {0, 0};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float4 sc = lds16f(scale + (2 * (k2 + k1) + half) * 16);
-            const float f = qs * sc.x, v = sc.y - ref;
-            const uint64_t f2 = f2_pack(f, f), v2 = f2_pack(v, v);
-            uint64_t acc[2] = {0, 0};
-#pragma unroll
-            for (int e = 16 * half; e < 16 * half + 16; e += 2) {
-              float y0 = __uint_as_float(x[e]), y1 = __uint_as_float(x[e + 1]);
-              if constexpr (CAP) {
-                y0 = score(y0, f, v);
-                y1 = score(y1, f, v);
-              } else {
-                f2_unpack(f2_fma(f2_pack(y0, y1), f2, v2), y0, y1);
-              }
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              acc[(e >> 1) & 1] = f2_add(acc[(e >> 1) & 1], f2_pack(y0, y1));
-              p[e / 2] = f16x2(y0, y1);
-            }
-            float a0, a1;
-            f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
-            sum = fmaf(a0 + a1, sc.z, sum);
+        for (int e = 0; e < 16; e += 2) {
+          float y0 = __uint_as_float(x[k >> 1][(k & 1) * 16 + e]), y1 = __uint_as_float(x[k >> 1][(k & 1) * 16 + e + 1]);
+          if constexpr (CAP) {
+            y0 = score(y0, f, v);
+            y1 = score(y1, f, v);
+          } else {
+            f2_unpack(f2_fma(f2_pack(y0, y1), f2, v2), y0, y1);
           }
-          tmem_st_x16(ts + 16 * (k2 + k1), p);           // over columns that have been read
+          y0 = ex2(y0);
+          y1 = ex2(y1);
+          acc[(e >> 1) & 1] = f2_add(acc[(e >> 1) & 1], f2_pack(y0, y1));
+          p[e / 2] = f16x2(y0, y1);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar(kPFull + 2 * wg + (k2 >> 1)));
+        float a0, a1;
+        f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+        sum = fmaf(a0 + a1, sc.z, sum);
+        tmem_st_x8(at + 8 * k, p);                       // over S, which is in registers
       }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bar(kPFull + 2 * wg + buf));
     }
-    if (ok) ok = wait(kOFull + wg, m.end - m.first - 1);
+    if (ok) ok = wait(kOFull + 2 * wg + ((m.end - 1) & 1), (m.end - m.first - 1) >> 1);
     if (ok) {
       tc_fence_after();
       uint32_t nans[D / 32];
@@ -567,9 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         // NaN codes that were taken out of blocks with rows that do not see them all
         const int hi_all = end_key(d, s, row0 / a.G), lo_all = first_key(d, s, (row_end - 1) / a.G);
         for (int key = lo; key < hi; ++key) {
-          const int k0 = key & ~(kKeys - 1);
-          if (!(k0 < lo_all || k0 + kKeys > hi_all)) {
-            key = max(key, (hi_all & ~(kKeys - 1)) - 1);
+          const int k0 = key & ~(kBlock - 1);
+          if (!(k0 < lo_all || k0 + kBlock > hi_all)) {
+            key = max(key, (hi_all & ~(kBlock - 1)) - 1);
             continue;
           }
           const int page = __ldg(kc.page_table + b * kc.table_ld + (key >> page_shift));
