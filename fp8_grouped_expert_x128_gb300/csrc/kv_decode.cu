@@ -25,20 +25,25 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;                 // keys a warp takes at a time
 constexpr int kTile = kStep * kWarps;
-constexpr int kCtasPerSm = 2;
 constexpr int kGroup = 16;                // parts joined at a time
 constexpr int kMaxParts = 1024;           // CTAs of a launch at most
 static_assert(3 * kMaxParts == kDecodeCounters, "counters of the three levels");
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kStages = D == 128 ? (NT == 4 ? 5 : 6) : 8;
+  // CTAs that share an SM (registers and shared memory are sized for them) and the
+  // stages of each warp's ring: some 150 KB under way on an SM either way
+  static constexpr int kCtasPerSm = D == 128 ? (NT == 4 ? 2 : 3) : (NT == 4 ? 3 : 4);
+  static constexpr int kStages = D == 128 ? (NT == 4 ? 5 : 4) : 6;
   static constexpr int kStageBytes = 2 * kStep * D;       // K, then V
   static constexpr int kRows = 8 * NT;
   static constexpr int kLd = D + 4;                       // merge buffer row, padded against bank conflicts
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kScales = kRing;                   // [warp][stage][2] floats
   static constexpr int kBuf = kScales + kWarps * kStages * 8;
+  static constexpr bool kSharedQ = NT > 1;                // Q's fragments: in registers for 8 rows, else shared
+  static constexpr int kQ = kBuf;                         // [row / 8][16-deep step][lane] uint2, done with before buf is used
+  static_assert(NT * (D / 16) * 256 <= kRows * kLd * 4, "Q fits where the merge buffer is");
   static constexpr int kSmem = kBuf + kRows * kLd * 4;
 };
 constexpr int kPartFloats = kDecodeRows * (128 + 2);      // one part: m[32], l[32], O[32][dim]
@@ -99,14 +104,15 @@ __device__ __forceinline__ int owner(int64_t u, int64_t W, int C) {
 }
 
 template <bool F16, int D, int NT>
-__global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<D, NT>;
   constexpr int KS = D / 16;              // 16-deep steps of S, and 16-dimension blocks of O
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t scan[kWarps];
   __shared__ int64_t s_u;                 // units before the sequence that holds this CTA's first one
   __shared__ int s_b, s_last;
-  __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows], s_inv[C::kRows];
+  __shared__ __align__(8) float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows], s_inv[C::kRows], s_qs[C::kRows];
+  __shared__ __align__(8) int s_lo[C::kRows], s_hi[C::kRows];          // keys that a row sees
 
   const moe_kv_attention_desc& d = a.d;
   const moe_kv_cache& kc = d.cache;
@@ -172,6 +178,10 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
   int32_t ignored = 0;                     // the scan has told
   Seq p_s = load_seq(d, p_b, &ignored);
   Tiles p_t = tiles_of(a, p_s, C::kRows);
+  // this lane's share of a step's copy: chunk ch of rows r, r + kRowsPer, ...
+  constexpr int kChunks = D / 16, kRowsPer = 32 / kChunks;
+  const int ld_r = lane / kChunks, ld_ch = lane % kChunks;
+  const int64_t k_lane = ld_r * kc.k_slot_ld + ld_ch * 16, v_lane = ld_r * kc.v_slot_ld + ld_ch * 16;
   const auto p_pages = [&] {               // the page of this warp's keys in 32 tiles from p_tile, one per lane
     p_base = p_tile;
     const int key = (p_tile + lane) * kTile + warp * kStep;
@@ -207,16 +217,28 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       }
       if (!on) page = 0;
       const int slot0 = key0 & (P - 1);
-      const uint8_t* kp = kc.k + page * kc.k_page_ld + p_h * kc.k_head_ld + slot0 * kc.k_slot_ld;
-      const uint8_t* vp = kc.v + page * kc.v_page_ld + p_h * kc.v_head_ld + slot0 * kc.v_slot_ld;
+      const uint8_t* kp = kc.k + page * kc.k_page_ld + p_h * kc.k_head_ld + slot0 * kc.k_slot_ld + k_lane;
+      const uint8_t* vp = kc.v + page * kc.v_page_ld + p_h * kc.v_head_ld + slot0 * kc.v_slot_ld + v_lane;
       const uint32_t st = ring + p_stage * C::kStageBytes;
-      constexpr int kChunks = D / 16, kRowsPer = 32 / kChunks;
+      if (on && key0 + kStep <= p_s.len) {
 #pragma unroll
-      for (int i = 0; i < kStep / kRowsPer; ++i) {
-        const int r = lane / kChunks + i * kRowsPer, ch = lane % kChunks;
-        const bool in = on && key0 + r < p_s.len;      // past the end: zeros, nothing is read
-        cp16(st + chunk_at<D>(r, ch), in ? kp + r * kc.k_slot_ld + ch * 16 : kc.k, in);
-        cp16(st + kStep * D + chunk_at<D>(r, ch), in ? vp + r * kc.v_slot_ld + ch * 16 : kc.v, in);
+        for (int i = 0; i < kStep / kRowsPer; ++i) {
+          const uint32_t at = st + chunk_at<D>(ld_r + i * kRowsPer, ld_ch);
+          cp16(at, kp, true);
+          cp16(at + kStep * D, vp, true);
+          kp += kRowsPer * kc.k_slot_ld;
+          vp += kRowsPer * kc.v_slot_ld;
+        }
+      } else {                             // past the end: zeros, nothing is read
+#pragma unroll
+        for (int i = 0; i < kStep / kRowsPer; ++i) {
+          const uint32_t at = st + chunk_at<D>(ld_r + i * kRowsPer, ld_ch);
+          const bool in = on && key0 + ld_r + i * kRowsPer < p_s.len;
+          cp16(at, in ? kp : kc.k, in);
+          cp16(at + kStep * D, in ? vp : kc.v, in);
+          kp += kRowsPer * kc.k_slot_ld;
+          vp += kRowsPer * kc.v_slot_ld;
+        }
       }
       if (lane < 2) {
         const float* sp = (lane ? kc.v_scale : kc.k_scale) + static_cast<int64_t>(page) * H + p_h;
@@ -244,14 +266,18 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
     const int hi_first = end_key(d, s, 0);
 
     // Q as the second operand: lane (g, c) holds row g's dimensions c * D/4 ..., scaled into f16
-    uint32_t q[NT][KS][2];
-    float qs[NT][2], m[NT][2], mu[NT][2], l[NT][2], o[NT][KS][4];
-    int lo[NT][2], hi[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      float amax = 0.0f;
+    uint32_t q[C::kSharedQ ? 1 : KS][2];
+    float qs[C::kSharedQ ? 1 : 2], m[NT][2], l[NT][2], o[NT][KS][4];
+    uint2* s_q = reinterpret_cast<uint2*>(smem + C::kQ);
+    if (tid < C::kRows) {
+      const int i = min(tid / a.G, s.n - 1);
+      s_lo[tid] = first_key(d, s, i);
+      s_hi[tid] = end_key(d, s, i);
+    }
+    if (!C::kSharedQ || warp < NT) {
+      const int r = (C::kSharedQ ? warp * 8 : 0) + g;
       uint4 w[D / 32];
+      float amax = 0.0f;
       if (r < rows) {
         const int i = r / a.G;
         const uint16_t* qp = static_cast<const uint16_t*>(d.q) + (s.c0 + i) * d.q_token_ld +
@@ -277,27 +303,34 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       for (int k = 0; k < D / 32; ++k) {
         float f[8];
         unpack8<F16>(w[k], f);
-        q[nt][2 * k][0] = f16x2(f[0] * mul, f[1] * mul);
-        q[nt][2 * k][1] = f16x2(f[2] * mul, f[3] * mul);
-        q[nt][2 * k + 1][0] = f16x2(f[4] * mul, f[5] * mul);
-        q[nt][2 * k + 1][1] = f16x2(f[6] * mul, f[7] * mul);
+        const uint2 x = make_uint2(f16x2(f[0] * mul, f[1] * mul), f16x2(f[2] * mul, f[3] * mul));
+        const uint2 y = make_uint2(f16x2(f[4] * mul, f[5] * mul), f16x2(f[6] * mul, f[7] * mul));
+        if constexpr (C::kSharedQ) {
+          s_q[(warp * KS + 2 * k) * 32 + lane] = x;
+          s_q[(warp * KS + 2 * k + 1) * 32 + lane] = y;
+        } else {
+          q[2 * k][0] = x.x; q[2 * k][1] = x.y;
+          q[2 * k + 1][0] = y.x; q[2 * k + 1][1] = y.y;
+        }
       }
       inv *= d.softcap > 0.0f ? d.sm_scale / d.softcap : d.sm_scale * kLog2e;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {       // of the columns of S^T that this lane holds
-        qs[nt][e] = __shfl_sync(0xffffffffu, inv, (2 * c + e) * 4);
-        const int i = min((nt * 8 + 2 * c + e) / a.G, s.n - 1);
-        lo[nt][e] = first_key(d, s, i);
-        hi[nt][e] = end_key(d, s, i);
-        m[nt][e] = -INFINITY;
-        mu[nt][e] = 0.0f;
-        l[nt][e] = 0.0f;
+      if constexpr (C::kSharedQ) {
+        if (c == 0) s_qs[r] = inv;
+      } else {
+        qs[0] = __shfl_sync(0xffffffffu, inv, 8 * c);     // of the columns of S^T that this lane holds
+        qs[1] = __shfl_sync(0xffffffffu, inv, 8 * c + 4);
       }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][k][e] = 0.0f;
     }
+    __syncthreads();
 
     uint32_t nan_seen = 0;
 #pragma unroll 1
@@ -326,26 +359,57 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
                                    e4m3x2_to_f16x2(xw[k] >> 16), e4m3x2_to_f16x2(yw[k] >> 16)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              if (nt * 8 < rows) mma(sc[nt], f, q[nt][k4 * 4 + k][0], q[nt][k4 * 4 + k][1]);
+              if (nt == 0 || nt * 8 < rows) {
+                if constexpr (C::kSharedQ) {
+                  const uint2 x = s_q[(nt * KS + k4 * 4 + k) * 32 + lane];
+                  mma(sc[nt], f, x.x, x.y);
+                } else {
+                  mma(sc[nt], f, q[k4 * 4 + k][0], q[k4 * 4 + k][1]);
+                }
+              }
           }
         }
         // scores in powers of two, with the V scale's logarithm
-        bool over = false;
+        float f[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = sc[nt][e] * (qs[nt][e & 1] * k_scale);
-            if (d.softcap > 0.0f) x = capped_log2(x, d.softcap * kLog2e);
-            x += v_log;
-            if (edge) {
-              const int key = key0 + g + (e >> 1) * 8;
-              if (key < lo[nt][e & 1] || key >= hi[nt][e & 1]) x = -INFINITY;
-            }
-            sc[nt][e] = x;
+          if constexpr (C::kSharedQ) {
+            const float2 x = *reinterpret_cast<const float2*>(s_qs + nt * 8 + 2 * c);
+            f[nt][0] = x.x * k_scale;
+            f[nt][1] = x.y * k_scale;
+          } else {
+            f[nt][0] = qs[0] * k_scale;
+            f[nt][1] = qs[1] * k_scale;
           }
-          over |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + kLazy || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + kLazy;
         }
+        if (d.softcap > 0.0f) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sc[nt][e] = capped_log2(sc[nt][e] * f[nt][e & 1], d.softcap * kLog2e) + v_log;
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nt][e] = fmaf(sc[nt][e], f[nt][e & 1], v_log);
+        }
+        if (edge) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int2 lo = *reinterpret_cast<const int2*>(s_lo + nt * 8 + 2 * c);
+            const int2 hi = *reinterpret_cast<const int2*>(s_hi + nt * 8 + 2 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + g + (e >> 1) * 8;
+              if (key < (e & 1 ? lo.y : lo.x) || key >= (e & 1 ? hi.y : hi.x)) sc[nt][e] = -INFINITY;
+            }
+          }
+        }
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          over |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + kLazy || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + kLazy;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -358,7 +422,6 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
               x = fmaxf(x, m[nt][e]);
               const float keep = x == -INFINITY ? 1.0f : ex2(m[nt][e] - x);
               m[nt][e] = x;
-              mu[nt][e] = x == -INFINITY ? 0.0f : x;
               l[nt][e] *= keep;
 #pragma unroll
               for (int k = 0; k < KS; ++k) {
@@ -372,7 +435,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
         for (int nt = 0; nt < NT; ++nt) {
           float w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2(sc[nt][e] - mu[nt][e & 1]);
+          for (int e = 0; e < 4; ++e) w[e] = ex2(sc[nt][e] - (m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1]));
           l[nt][0] = fmaf(w[0] + w[2], v_inv, l[nt][0]);
           l[nt][1] = fmaf(w[1] + w[3], v_inv, l[nt][1]);
           p[nt][0] = transposed(f16x2(w[0], w[1]));
@@ -399,7 +462,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
                                    e4m3x2_to_f16x2(y >> 16)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              if (nt * 8 < rows) mma(o[nt][2 * k2 + i], f, p[nt][0], p[nt][1]);
+              if (nt == 0 || nt * 8 < rows) mma(o[nt][2 * k2 + i], f, p[nt][0], p[nt][1]);
           }
         }
       }
@@ -615,7 +678,7 @@ int launch(const AttnArgs& a, cudaStream_t st) {
     MOE_CUDA_TRY(cudaFuncSetAttribute(kv_decode_kernel<F16, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
   }
-  const int ctas = min(kMaxParts, num_sms() * kCtasPerSm);
+  const int ctas = min(kMaxParts, num_sms() * Cfg<D, NT>::kCtasPerSm);
   return launch_pdl(kv_decode_kernel<F16, D, NT>, dim3(ctas), dim3(kThreads), smem, st, a);
 }
 
@@ -629,7 +692,7 @@ int pick_rows(const AttnArgs& a, int64_t rows, cudaStream_t st) {
 }  // namespace
 
 size_t kv_decode_workspace() {
-  const size_t ctas = static_cast<size_t>(min(kMaxParts, num_sms() * kCtasPerSm));
+  const size_t ctas = static_cast<size_t>(min(kMaxParts, num_sms() * 4));      // of the kernel with most
   return kDecodeCounters * sizeof(int32_t) + ctas * 2 * kPartFloats * sizeof(float);
 }
 
