@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -141,9 +142,9 @@ _sig("moe_ffn_kernel_count", ctypes.c_int, [ctypes.POINTER(moe_ffn_desc)])
 _sig("moe_ffn", ctypes.c_int, [ctypes.POINTER(moe_ffn_desc), _P, ctypes.c_size_t, _P])
 _sig("moe_ffn_noalloc", ctypes.c_int, [ctypes.POINTER(moe_ffn_desc), _P])
 _sig("moe_ffn_noalloc_capacity", ctypes.c_size_t, [])
-_sig("moe_kv_append", ctypes.c_int, [ctypes.POINTER(moe_kv_append_desc), _P])
+_sig("moe_kv_append", ctypes.c_int, [_P, _P])
 _sig("moe_kv_attention_workspace_size", ctypes.c_size_t, [ctypes.POINTER(moe_kv_attention_desc)])
-_sig("moe_kv_attention", ctypes.c_int, [ctypes.POINTER(moe_kv_attention_desc), _P, ctypes.c_size_t, _P])
+_sig("moe_kv_attention", ctypes.c_int, [_P, _P, ctypes.c_size_t, _P])
 
 
 class MoeError(RuntimeError):
@@ -439,51 +440,77 @@ def alloc_workspace(desc: moe_ffn_desc, device=None) -> torch.Tensor:
 _KV_TYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
 
 
+# Descriptors as the C structures lay them out; packing one is what a call costs on
+# the host beside the launch, so the checks below are written to pass quickly and
+# leave the telling of what is wrong to functions that run only then.
+_KV_CACHE_FIELDS = "7Q8q6i"
+_kv_append_pack = struct.Struct("@" + _KV_CACHE_FIELDS + "q6Q8q4i").pack
+_kv_attention_pack = struct.Struct("@" + _KV_CACHE_FIELDS + "q4Q4q2f4i").pack
+
+
 def _kv_rows(t, name, T, heads, dim, dtype, device):
     """Strides (token, head) of a [T, heads, dim] tensor of the step's rows."""
-    if t.shape != (T, heads, dim) or t.dtype != dtype or t.get_device() != device:
-        raise ValueError(f"{name}: expected {dtype} [{T}, {heads}, {dim}] on the cache's GPU, got {t.dtype} {list(t.shape)}")
     st, sh, sd = t.stride()
-    if sd != 1 and t.numel():
-        raise ValueError(f"{name}: the elements of a row must be next to each other")
+    if t.shape != (T, heads, dim) or t.dtype is not dtype or t.get_device() != device or (sd != 1 and t.numel()):
+        raise ValueError(f"{name}: expected {dtype} [{T}, {heads}, {dim}] on the cache's GPU with the elements of a row next to "
+                         f"each other, got {t.dtype} {list(t.shape)}, strides {list(t.stride())}")
     return st, sh
+
+
+def _kv_cache_refused(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype):
+    pages, heads, page, dim = k_cache.shape
+    device = k_cache.get_device()
+    if device < 0:
+        return ValueError("k_cache must be a CUDA tensor")
+    if v_cache.shape != k_cache.shape or k_cache.dtype not in _U8 or v_cache.dtype not in _U8:
+        return ValueError("k_cache and v_cache: expected uint8 or float8_e4m3fn [pages, kv_heads, page_size, dim]")
+    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        return ValueError("k_cache, v_cache: the elements of a row must be next to each other")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.shape != (pages, heads) or t.dtype != torch.float32 or not t.is_contiguous():
+            return ValueError(f"{name}: expected contiguous float32 [{pages}, {heads}]")
+    batch = page_table.shape[0]
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
+        return ValueError("page_table: expected int32 [batch, max_pages], rows contiguous")
+    if (cu_new.shape != (batch + 1,) or kv_len.shape != (batch,) or cu_new.dtype != torch.int32
+            or kv_len.dtype != torch.int32 or not cu_new.is_contiguous() or not kv_len.is_contiguous()):
+        return ValueError(f"cu_new, kv_len: expected contiguous int32 [{batch + 1}] and [{batch}]")
+    if dtype not in _KV_TYPES:
+        return ValueError(f"token tensors: expected bfloat16 or float16, got {dtype}")
+    for t, name in ((v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"), (page_table, "page_table"),
+                    (cu_new, "cu_new"), (kv_len, "kv_len")):
+        if t.get_device() != device:
+            return ValueError(f"{name}: not on the GPU that holds k_cache")
+    return ValueError("paged cache: tensors not as moe_fp8.h has them")
 
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype):
     """The cache part of a descriptor, as a tuple in the order of its fields."""
-    pages, heads, page, dim = k_cache.shape
-    device = k_cache.get_device()
-    if device < 0:
-        raise ValueError("k_cache must be a CUDA tensor")
-    if v_cache.shape != k_cache.shape or k_cache.dtype not in _U8 or v_cache.dtype not in _U8:
-        raise ValueError("k_cache and v_cache: expected uint8 or float8_e4m3fn [pages, kv_heads, page_size, dim]")
+    shape = k_cache.shape
+    pages, heads, page, dim = shape
     kp, kh, ks, kd = k_cache.stride()
     vp, vh, vs, vd = v_cache.stride()
-    if kd != 1 or vd != 1:
-        raise ValueError("k_cache, v_cache: the elements of a row must be next to each other")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.shape != (pages, heads) or t.dtype != torch.float32 or not t.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous float32 [{pages}, {heads}]")
     batch, max_pages = page_table.shape
-    if page_table.dtype != torch.int32 or (max_pages > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table: expected int32 [batch, max_pages], rows contiguous")
-    if (cu_new.shape != (batch + 1,) or kv_len.shape != (batch,) or cu_new.dtype != torch.int32
-            or kv_len.dtype != torch.int32 or not cu_new.is_contiguous() or not kv_len.is_contiguous()):
-        raise ValueError(f"cu_new, kv_len: expected contiguous int32 [{batch + 1}] and [{batch}]")
-    if dtype not in _KV_TYPES:
-        raise ValueError(f"token tensors: expected bfloat16 or float16, got {dtype}")
-    for t, name in ((v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"), (page_table, "page_table"),
-                    (cu_new, "cu_new"), (kv_len, "kv_len")):
-        if t.get_device() != device:
-            raise ValueError(f"{name}: not on the GPU that holds k_cache")
+    table_ld, table_one = page_table.stride()
+    device = k_cache.get_device()
+    i32, f32 = torch.int32, torch.float32
+    if not (v_cache.shape == shape and kd == 1 == vd and table_one == 1 and device >= 0
+            and k_cache.dtype in _U8 and v_cache.dtype in _U8 and dtype in _KV_TYPES
+            and k_scale.shape == (pages, heads) == v_scale.shape and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and cu_new.shape == (batch + 1,) and kv_len.shape == (batch,) and cu_new.is_contiguous() and kv_len.is_contiguous()
+            and k_scale.dtype is f32 and v_scale.dtype is f32
+            and page_table.dtype is i32 and cu_new.dtype is i32 and kv_len.dtype is i32
+            and v_cache.get_device() == device and k_scale.get_device() == device and v_scale.get_device() == device
+            and page_table.get_device() == device and cu_new.get_device() == device and kv_len.get_device() == device):
+        raise _kv_cache_refused(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype)
     return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
-            cu_new.data_ptr(), kv_len.data_ptr(), kp, kh, ks, vp, vh, vs, page_table.stride(0), pages, batch, max_pages,
+            cu_new.data_ptr(), kv_len.data_ptr(), kp, kh, ks, vp, vh, vs, table_ld, pages, batch, max_pages,
             page, heads, dim, _KV_TYPES[dtype])
 
 
 def _kv_err(err, device):
     if err is None:
-        return None
+        return 0
     if err.dtype != torch.int32 or err.get_device() != device:
         raise ValueError("err: expected an int32 word on the cache's GPU (new_error_word)")
     return err.data_ptr()
@@ -498,42 +525,57 @@ def moe_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, 
     tokens are rows cu_new[b] .. cu_new[b + 1] - 1, the last of its kv_len[b].
     cos_sin fp32 [max_pos, rot_dim] rotates the keys, and q [T, q_heads, dim] into
     q_out (which may be q); flags = MOE_KV_INTERLEAVED for adjacent pairs."""
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, k.dtype)
-    device, heads, dim, T = k_cache.get_device(), k_cache.shape[1], k_cache.shape[3], k.shape[0]
-    kl = _kv_rows(k, "k", T, heads, dim, k.dtype, device)
-    vl = _kv_rows(v, "v", T, heads, dim, k.dtype, device)
-    ql = ol = (0, 0)
-    q_heads = max_pos = rot = 0
+    dtype = k.dtype
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype)
+    device, heads, dim, T = k_cache.get_device(), c[18], c[19], k.shape[0]
+    kt, kh = _kv_rows(k, "k", T, heads, dim, dtype, device)
+    vt, vh = _kv_rows(v, "v", T, heads, dim, dtype, device)
+    qt = qh = ot = oh = q_heads = max_pos = rot = q_ptr = o_ptr = cs_ptr = 0
     if q is not None:
         if q_out is None:
             raise ValueError("q_out: queries need a tensor to be written to")
         q_heads = q.shape[1]
-        ql = _kv_rows(q, "q", T, q_heads, dim, k.dtype, device)
-        ol = _kv_rows(q_out, "q_out", T, q_heads, dim, k.dtype, device)
+        qt, qh = _kv_rows(q, "q", T, q_heads, dim, dtype, device)
+        ot, oh = _kv_rows(q_out, "q_out", T, q_heads, dim, dtype, device)
+        q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != device:
+        if (cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous()
+                or cos_sin.get_device() != device):
             raise ValueError("cos_sin: expected contiguous float32 [max_pos, rot_dim] on the cache's GPU")
         max_pos, rot = cos_sin.shape
-    d = moe_kv_append_desc(c, T, k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None,
-                           q_out.data_ptr() if q is not None else None, cos_sin.data_ptr() if rot else None,
-                           _kv_err(err, device), *kl, *vl, *ql, *ol, q_heads, rot, max_pos, flags)
-    _check(_lib.moe_kv_append(ctypes.byref(d), _stream_of(device, stream)), "moe_kv_append")
+        cs_ptr = cos_sin.data_ptr()
+    d = _kv_append_pack(*c, T, k.data_ptr(), v.data_ptr(), q_ptr, o_ptr, cs_ptr, _kv_err(err, device), kt, kh, vt, vh, qt, qh,
+                        ot, oh, q_heads, rot, max_pos, flags)
+    rc = _lib.moe_kv_append(d, _stream_of(device, stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_kv_append")
+
+
+def _kv_attention_fields(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q, window, softcap,
+                         flags, lse, err):
+    dtype = q.dtype
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype)
+    device, dim = k_cache.get_device(), c[19]
+    T, heads, _ = q.shape
+    qt, qh = _kv_rows(q, "q", T, heads, dim, dtype, device)
+    ot, oh = _kv_rows(out, "out", T, heads, dim, dtype, device)
+    lse_ptr = 0
+    if lse is not None:
+        if lse.shape != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != device:
+            raise ValueError(f"lse: expected contiguous float32 [{T}, {heads}] on the cache's GPU")
+        lse_ptr = lse.data_ptr()
+    return c, (T, q.data_ptr(), out.data_ptr(), lse_ptr, _kv_err(err, device), qt, qh, ot, oh, sm_scale, softcap, heads, max_q,
+               window, flags)
 
 
 def make_kv_attention_desc(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q=0, window=0,
                            softcap=0.0, flags=0, lse=None, err=None):
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, q.dtype)
-    device, dim = k_cache.get_device(), k_cache.shape[3]
-    T, heads = q.shape[0], q.shape[1]
-    qs = _kv_rows(q, "q", T, heads, dim, q.dtype, device)
-    os_ = _kv_rows(out, "out", T, heads, dim, q.dtype, device)
-    if lse is not None and (lse.shape != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous()
-                            or lse.get_device() != device):
-        raise ValueError(f"lse: expected contiguous float32 [{T}, {heads}] on the cache's GPU")
-    return moe_kv_attention_desc(c, T, q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                                 _kv_err(err, device), *qs, *os_, sm_scale, softcap, heads, max_q, window, flags)
+    """Descriptor of a moe_kv_attention call, for moe_kv_attention_workspace_size and alloc_kv_workspace."""
+    c, rest = _kv_attention_fields(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q, window,
+                                   softcap, flags, lse, err)
+    return moe_kv_attention_desc(c, *rest)
 
 
 def moe_kv_attention_workspace_size(desc: moe_kv_attention_desc) -> int:
@@ -547,13 +589,14 @@ def moe_kv_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, 
     max_q: the largest number of new tokens of a sequence (0 = not known).
     workspace: a uint8 device tensor of at least moe_kv_attention_workspace_size
     bytes, zeroed once before its first use.  lse: optional fp32 [T, q_heads]."""
-    d = make_kv_attention_desc(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q, window,
-                               softcap, flags, lse, err)
+    c, rest = _kv_attention_fields(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q, window,
+                                   softcap, flags, lse, err)
     device = q.get_device()
     if workspace.get_device() != device:
         raise ValueError("workspace: not on the cache's GPU")
-    _check(_lib.moe_kv_attention(ctypes.byref(d), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 _stream_of(device, stream)), "moe_kv_attention")
+    rc = _lib.moe_kv_attention(_kv_attention_pack(*c, *rest), workspace.data_ptr(), workspace.nbytes, _stream_of(device, stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_kv_attention")
     return out
 
 

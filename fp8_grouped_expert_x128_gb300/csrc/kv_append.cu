@@ -3,18 +3,26 @@
 //
 // Per page, head and K or V: s' = the power-of-two scale of the page's new
 // tokens (and of what the page held before), q = e4m3(x / s').  The maximum has
-// to be known before the first code is written, so a CTA takes one page and one
-// of K or V, keeps the page's rotated rows in registers (fp32, 16 values a
-// thread and row), takes the maximum over the CTA and then writes the codes: the
-// inputs are read once.  It walks over several heads, so that a row's cosines and
-// sines (as many bytes as the row has in 16 bits) are loaded once for all of
-// them.  Query rows need no maximum; further CTAs of the same launch rotate them.
+// to be known before the first code is written.  Bound by HBM for prompts, by the
+// chain of dependent loads (sequence, page, rows) for single tokens; two kernels:
+//
+// kv_append_pages_kernel, for prompts: a CTA takes one page and one of K or V,
+// keeps the page's rotated rows in registers (fp32, 16 values a thread and row),
+// takes the maximum over the CTA and then writes the codes: the inputs are read
+// once.  It walks over several heads, the next head's rows loading meanwhile, so
+// that the chain is paid once for all of them.
+//
+// kv_append_tokens_kernel, for few new tokens a page: a CTA takes one page with all
+// its heads, K and V; 4 or 8 lanes share a row, and the maximum stays among them.
+//
+// Query rows need no maximum; further CTAs of the same launch rotate them.
 #include "kv_common.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kQHeadsPerCta = 8;   // query heads one thread rotates with the same angles
+constexpr int kFewTokens = 4;      // new tokens a sequence, on average, up to which the tokens kernel serves
 
 struct AppendArgs {
   moe_kv_append_desc d;
@@ -117,26 +125,195 @@ __device__ void rotate_queries(const AppendArgs& a, int cta) {
   }
   const uint16_t* q = static_cast<const uint16_t*>(d.q) + t * d.q_token_ld;
   uint16_t* o = static_cast<uint16_t*>(d.q_out) + t * d.qo_token_ld;
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const uint4 u = *reinterpret_cast<const uint4*>(q + h * d.q_head_ld + ra);
-    const uint4 v = *reinterpret_cast<const uint4*>(q + h * d.q_head_ld + rb);
-    uint4 uo = u, vo = v;
-    if (turned) {
-      float x[8], y[8];
-      unpack8<F16>(u, x);
-      unpack8<F16>(v, y);
-      turn(x, y, c, s, inter);
-      uo = pack8<F16>(x);
-      vo = pack8<F16>(y);
+  // four heads' loads before the first store: q_out may be q, so the compiler keeps
+  // loads and stores in order (each thread rewrites only what it has read)
+  constexpr int kAtOnce = 4;
+  for (int h = h0; h < h1; h += kAtOnce) {
+    uint4 u[kAtOnce], v[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (h + k < h1) {
+        u[k] = *reinterpret_cast<const uint4*>(q + (h + k) * d.q_head_ld + ra);
+        v[k] = *reinterpret_cast<const uint4*>(q + (h + k) * d.q_head_ld + rb);
+      }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (h + k < h1) {
+        if (turned) {
+          float x[8], y[8];
+          unpack8<F16>(u[k], x);
+          unpack8<F16>(v[k], y);
+          turn(x, y, c, s, inter);
+          u[k] = pack8<F16>(x);
+          v[k] = pack8<F16>(y);
+        }
+        *reinterpret_cast<uint4*>(o + (h + k) * d.qo_head_ld + ra) = u[k];
+        *reinterpret_cast<uint4*>(o + (h + k) * d.qo_head_ld + rb) = v[k];
+      }
+  }
+}
+
+// What a unit's CTA has to do: the page's new slots and where their rows are.
+struct PageWork {
+  int b, pi, page, s0, s1;   // sequence, its page number, page, slots [s0, s1) of the new tokens
+  int64_t row0;              // token row of slot 0
+};
+
+// Units are numbered so that sequence b's start at cu[b] / P + 2b: as many as it
+// can need wherever its first token falls in a page, with no prefix sum.  False if
+// the unit has nothing to do (faults are told).
+__device__ __forceinline__ bool page_work(const moe_kv_append_desc& d, int unit, PageWork& w) {
+  const moe_kv_cache& kc = d.cache;
+  const int P = kc.page_size;
+  w.b = warp_find(kc.batch, unit, [&](int i) { return __ldg(kc.cu_new + i) / P + 2 * i; });
+  const int c0 = __ldg(kc.cu_new + w.b), c1 = __ldg(kc.cu_new + w.b + 1), len = __ldg(kc.kv_len + w.b);
+  const int n = c1 - c0;
+  if (n == 0) return false;
+  if (c0 < 0 || n < 0 || c1 > d.T || len < n) {
+    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
+    return false;
+  }
+  const int pos0 = len - n;                                  // position of the sequence's first new token
+  const int nth = unit - (c0 / P + 2 * w.b);                 // of the pages the new tokens fall on
+  w.pi = pos0 / P + nth;
+  if (nth < 0 || w.pi > (len - 1) / P) return false;
+  if (w.pi >= kc.max_pages) {
+    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_OVERFLOW);
+    return false;
+  }
+  w.page = __ldg(kc.page_table + w.b * kc.table_ld + w.pi);
+  w.s0 = max(pos0 - w.pi * P, 0);
+  w.s1 = min(len - w.pi * P, P);
+  w.row0 = c0 + (w.pi * P - pos0);
+  if (w.page < 0 || w.page >= kc.pages || (d.rot_dim && w.pi * P + w.s1 > d.max_pos)) {
+    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
+    return false;
+  }
+  return true;
+}
+
+// 16 codes of a slot that was there before, under the page's new scale.
+__device__ __forceinline__ void rescale16(uint4* o, float before, float s, bool pow2) {
+  const uint4 u = *o;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint2 q[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t p = e4m3x2_to_f16x2(static_cast<uint16_t>(w[2 * half + (i >> 1)] >> (16 * (i & 1))));
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p));
+      f[2 * i] = v.x * before;
+      f[2 * i + 1] = v.y * before;
     }
-    *reinterpret_cast<uint4*>(o + h * d.qo_head_ld + ra) = uo;
-    *reinterpret_cast<uint4*>(o + h * d.qo_head_ld + rb) = vo;
+    q[half] = codes8(f, s, pow2);
+  }
+  *o = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+}
+
+// A row's 16 values of group g, rotated.
+template <bool F16>
+__device__ __forceinline__ void rotated16(const uint4& u, const uint4& v, const float* cos_sin, int pos, int g, int rot, bool inter,
+                                          float (&x)[8], float (&y)[8]) {
+  unpack8<F16>(u, x);
+  unpack8<F16>(v, y);
+  if (g < (rot >> 4)) {
+    float c[8], s[8];
+    const float* cs = cos_sin + static_cast<int64_t>(pos) * rot + 8 * g;
+    load8f(cs, c);
+    load8f(cs + (rot >> 1), s);
+    turn(x, y, c, s, inter);
+  }
+}
+__device__ __forceinline__ float finite_max(const float (&x)[8], const float (&y)[8], float amax) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_abs(x[i]), finite_abs(y[i])));
+  return amax;
+}
+
+// A page's scale from the maximum of its new tokens; whether old codes have to follow.
+__device__ __forceinline__ float page_scale(float amax, bool joins, float before, bool& grown, bool& pow2) {
+  uint8_t byte;
+  float s = block_scale_ue8m0(amax, &byte);
+  grown = joins && s > before;
+  if (joins && !grown) s = before;
+  pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+  return s;
+}
+
+template <bool F16, int D>
+__global__ void __launch_bounds__(128) kv_append_tokens_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int TT = 128, kGroups = D / 16;
+  const moe_kv_append_desc& d = a.d;
+  const moe_kv_cache& kc = d.cache;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= a.kv_ctas) {
+    rotate_queries<F16, D, TT>(a, blockIdx.x - a.kv_ctas);
+    return;
+  }
+  PageWork w;
+  if (!page_work(d, blockIdx.x, w)) return;
+  const bool inter = (d.flags & MOE_KV_INTERLEAVED) != 0;
+  const int P = kc.page_size, g = threadIdx.x % kGroups;
+  // rows of (K or V, head), kGroups lanes to each; whole groups of lanes take part or not
+  for (int row = threadIdx.x / kGroups; row < 2 * kc.kv_heads; row += TT / kGroups) {
+    const bool is_v = row >= kc.kv_heads;
+    const int h = is_v ? row - kc.kv_heads : row, rot = is_v ? 0 : d.rot_dim;
+    const int64_t tld = is_v ? d.v_token_ld : d.k_token_ld, sld = is_v ? kc.v_slot_ld : kc.k_slot_ld;
+    int ra, rb;
+    group_runs(g, rot, inter, ra, rb);
+    const uint16_t* src = static_cast<const uint16_t*>(is_v ? d.v : d.k) + w.row0 * tld + h * (is_v ? d.v_head_ld : d.k_head_ld);
+    uint8_t* out = is_v ? kc.v + w.page * kc.v_page_ld + h * kc.v_head_ld : kc.k + w.page * kc.k_page_ld + h * kc.k_head_ld;
+    float* scale = (is_v ? kc.v_scale : kc.k_scale) + static_cast<int64_t>(w.page) * kc.kv_heads + h;
+    const float before = w.s0 > 0 ? *scale : 0.0f;
+    float x[8], y[8], amax = 0.0f;
+    // four slots' loads at once: a sequence of the batch may have many new tokens after all
+    constexpr int kAtOnce = 4;
+    uint4 u[kAtOnce], v[kAtOnce];
+    const auto load = [&](int slot) {
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (slot + k < w.s1) {
+          const uint16_t* p = src + (slot + k) * tld;
+          u[k] = __ldg(reinterpret_cast<const uint4*>(p + ra));
+          v[k] = __ldg(reinterpret_cast<const uint4*>(p + rb));
+        }
+    };
+    for (int slot = w.s0; slot < w.s1; slot += kAtOnce) {
+      load(slot);
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (slot + k < w.s1) {
+          rotated16<F16>(u[k], v[k], d.cos_sin, w.pi * P + slot + k, g, rot, inter, x, y);
+          amax = finite_max(x, y, amax);
+        }
+    }
+    const uint32_t lanes = kGroups == 8 ? 0xFFu << (threadIdx.x & 24) : 0xFu << (threadIdx.x & 28);
+#pragma unroll
+    for (int o = 1; o < kGroups; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
+    bool grown, pow2;
+    const float s = page_scale(amax, w.s0 > 0, before, grown, pow2);
+    for (int slot = w.s0; slot < w.s1; slot += kAtOnce) {
+      if (w.s1 - w.s0 > kAtOnce) load(slot);             // else they are still in registers
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (slot + k < w.s1) {
+          rotated16<F16>(u[k], v[k], d.cos_sin, w.pi * P + slot + k, g, rot, inter, x, y);
+          uint8_t* o = out + (slot + k) * sld;
+          *reinterpret_cast<uint2*>(o + ra) = codes8(x, s, pow2);
+          *reinterpret_cast<uint2*>(o + rb) = codes8(y, s, pow2);
+        }
+    }
+    if (grown)
+      for (int slot = 0; slot < w.s0; ++slot) rescale16(reinterpret_cast<uint4*>(out + slot * sld + 16 * g), before, s, pow2);
+    if (g == 0) *scale = s;
   }
 }
 
 template <bool F16, int D, int TT, int R>
-__global__ void __launch_bounds__(TT) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(TT) kv_append_pages_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ uint32_t red[2][TT / 32];
   const moe_kv_append_desc& d = a.d;
   const moe_kv_cache& kc = d.cache;
@@ -150,41 +327,35 @@ __global__ void __launch_bounds__(TT) kv_append_kernel(const __grid_constant__ A
   const int P = kc.page_size;
   const int hg = blockIdx.x % a.head_groups;
   const bool is_v = (blockIdx.x / a.head_groups) & 1;
-  const int unit = blockIdx.x / (2 * a.head_groups);
-  // Units are numbered so that sequence b's start at cu[b] / P + 2b: as many as
-  // it can need wherever its first token falls in a page, with no prefix sum.
-  const int b = warp_find(kc.batch, unit, [&](int i) { return __ldg(kc.cu_new + i) / P + 2 * i; });
-  const int c0 = __ldg(kc.cu_new + b), c1 = __ldg(kc.cu_new + b + 1), len = __ldg(kc.kv_len + b);
-  const int n = c1 - c0;
-  if (n == 0) return;
-  if (c0 < 0 || n < 0 || c1 > d.T || len < n) {
-    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
-    return;
-  }
-  const int pos0 = len - n;                                  // position of the sequence's first new token
-  const int nth = unit - (c0 / P + 2 * b);                   // of the pages the new tokens fall on
-  const int pi = pos0 / P + nth;
-  if (nth < 0 || pi > (len - 1) / P) return;
-  if (pi >= kc.max_pages) {
-    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_OVERFLOW);
-    return;
-  }
-  const int page = __ldg(kc.page_table + b * kc.table_ld + pi);
-  const int s0 = max(pos0 - pi * P, 0), s1 = min(len - pi * P, P);   // slots of the new tokens
-  if (page < 0 || page >= kc.pages || (d.rot_dim && pi * P + s1 > d.max_pos)) {
-    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
-    return;
-  }
-  const int64_t row0 = c0 + (pi * P - pos0);                 // token row of slot 0
+  PageWork w;
+  if (!page_work(d, blockIdx.x / (2 * a.head_groups), w)) return;
   const uint16_t* src = static_cast<const uint16_t*>(is_v ? d.v : d.k);
   const int64_t src_tld = is_v ? d.v_token_ld : d.k_token_ld, src_hld = is_v ? d.v_head_ld : d.k_head_ld;
-  uint8_t* dst = (is_v ? kc.v + page * kc.v_page_ld : kc.k + page * kc.k_page_ld);
+  uint8_t* dst = (is_v ? kc.v + w.page * kc.v_page_ld : kc.k + w.page * kc.k_page_ld);
   const int64_t dst_hld = is_v ? kc.v_head_ld : kc.k_head_ld, dst_sld = is_v ? kc.v_slot_ld : kc.k_slot_ld;
-  float* scale = (is_v ? kc.v_scale : kc.k_scale) + static_cast<int64_t>(page) * kc.kv_heads;
+  float* scale = (is_v ? kc.v_scale : kc.k_scale) + static_cast<int64_t>(w.page) * kc.kv_heads;
   const int rot = is_v ? 0 : d.rot_dim;
   const bool inter = (d.flags & MOE_KV_INTERLEAVED) != 0;
   const int h0 = hg * a.heads_per, h1 = min(h0 + a.heads_per, kc.kv_heads);
 
+  uint4 u[R], v[R];
+  const auto load = [&](int h) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int item = threadIdx.x + r * TT;
+      const int slot = item / kGroups, g = item % kGroups;
+      int ra, rb;
+      group_runs(g, rot, inter, ra, rb);
+      if (slot >= w.s0 && slot < w.s1) {
+        const uint16_t* p = src + (w.row0 + slot) * src_tld + h * src_hld;
+        u[r] = __ldg(reinterpret_cast<const uint4*>(p + ra));
+        v[r] = __ldg(reinterpret_cast<const uint4*>(p + rb));
+      } else {
+        u[r] = v[r] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  load(h0);
   for (int h = h0; h < h1; ++h) {
     float x[R][8], y[R][8];
     float amax = 0.0f;
@@ -192,23 +363,12 @@ __global__ void __launch_bounds__(TT) kv_append_kernel(const __grid_constant__ A
     for (int r = 0; r < R; ++r) {
       const int item = threadIdx.x + r * TT;
       const int slot = item / kGroups, g = item % kGroups;
-      if (slot < s0 || slot >= s1) continue;
-      int ra, rb;
-      group_runs(g, rot, inter, ra, rb);
-      const uint16_t* p = src + (row0 + slot) * src_tld + h * src_hld;
-      unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(p + ra)), x[r]);
-      unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(p + rb)), y[r]);
-      if (g < (rot >> 4)) {
-        float c[8], s[8];
-        const float* cs = d.cos_sin + static_cast<int64_t>(pi * P + slot) * rot + 8 * g;
-        load8f(cs, c);
-        load8f(cs + (rot >> 1), s);
-        turn(x[r], y[r], c, s, inter);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_abs(x[r][i]), finite_abs(y[r][i])));
+      const bool in = slot >= w.s0 && slot < w.s1;
+      rotated16<F16>(u[r], v[r], d.cos_sin, w.pi * P + (in ? slot : w.s0), g, rot, inter, x[r], y[r]);
+      amax = finite_max(x[r], y[r], amax);             // rows that are none are zeros
     }
     const float before = scale[h];
+    if (h + 1 < h1) load(h + 1);
     // floats that are not negative order as their bit patterns do
     const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
     uint32_t* slot_red = red[h & 1];
@@ -216,64 +376,56 @@ __global__ void __launch_bounds__(TT) kv_append_kernel(const __grid_constant__ A
     __syncthreads();
     uint32_t all = 0;
 #pragma unroll
-    for (int w = 0; w < TT / 32; ++w) all = max(all, slot_red[w]);
-    uint8_t byte;
-    float s = block_scale_ue8m0(__uint_as_float(all), &byte);
-    const bool grown = s0 > 0 && s > before;
-    if (s0 > 0 && !grown) s = before;
-    const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+    for (int k = 0; k < TT / 32; ++k) all = max(all, slot_red[k]);
+    bool grown, pow2;
+    const float s = page_scale(__uint_as_float(all), w.s0 > 0, before, grown, pow2);
     uint8_t* out = dst + h * dst_hld;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int item = threadIdx.x + r * TT;
       const int slot = item / kGroups, g = item % kGroups;
-      if (slot < s0 || slot >= s1) continue;
+      if (slot < w.s0 || slot >= w.s1) continue;
       int ra, rb;
       group_runs(g, rot, inter, ra, rb);
       uint8_t* o = out + slot * dst_sld;
       *reinterpret_cast<uint2*>(o + ra) = codes8(x[r], s, pow2);
       *reinterpret_cast<uint2*>(o + rb) = codes8(y[r], s, pow2);
     }
-    if (grown) {
-      // the slots that were there take the page's new scale
-      for (int item = threadIdx.x; item < s0 * kGroups; item += TT) {
-        uint4* o = reinterpret_cast<uint4*>(out + item / kGroups * dst_sld + 16 * (item % kGroups));
-        const uint4 u = *o;
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint2 q[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t p = e4m3x2_to_f16x2(static_cast<uint16_t>(w[2 * half + (i >> 1)] >> (16 * (i & 1))));
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p));
-            f[2 * i] = v.x * before;
-            f[2 * i + 1] = v.y * before;
-          }
-          q[half] = codes8(f, s, pow2);
-        }
-        *o = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
-      }
-    }
+    if (grown)
+      for (int item = threadIdx.x; item < w.s0 * kGroups; item += TT)
+        rescale16(reinterpret_cast<uint4*>(out + item / kGroups * dst_sld + 16 * (item % kGroups)), before, s, pow2);
     // every thread read the old scale before the barrier above
     if (threadIdx.x == 0) scale[h] = s;
   }
 }
 
-template <bool F16, int D, int TT, int R>
-int launch_append(AppendArgs& a, cudaStream_t st) {
-  const moe_kv_append_desc& d = a.d;
-  a.units = static_cast<int32_t>(d.T / d.cache.page_size) + 2 * d.cache.batch;
-  a.heads_per = 1;
-  a.head_groups = d.cache.kv_heads;
-  const int64_t kv = static_cast<int64_t>(a.units) * 2 * a.head_groups;
-  a.q_groups = (d.q_heads + kQHeadsPerCta - 1) / kQHeadsPerCta;
+// How many CTAs the queries take, TT threads each.
+template <int D, int TT>
+int64_t query_ctas(AppendArgs& a) {
   constexpr int kRows = TT / (D / 16);
-  const int64_t qc = d.q ? (d.T + kRows - 1) / kRows * a.q_groups : 0;
+  a.q_groups = (a.d.q_heads + kQHeadsPerCta - 1) / kQHeadsPerCta;
+  return a.d.q ? (a.d.T + kRows - 1) / kRows * a.q_groups : 0;
+}
+
+template <bool F16, int D, int TT, int R>
+int launch_pages(AppendArgs& a, cudaStream_t st) {
+  // several heads a CTA, as long as some sixteen CTAs an SM are left
+  const int64_t one = 2ll * a.units * a.d.cache.kv_heads;
+  const int64_t per = one / (16ll * num_sms());
+  a.heads_per = static_cast<int32_t>(per < 1 ? 1 : per > a.d.cache.kv_heads ? a.d.cache.kv_heads : per);
+  a.head_groups = (a.d.cache.kv_heads + a.heads_per - 1) / a.heads_per;
+  const int64_t kv = 2ll * a.units * a.head_groups, qc = query_ctas<D, TT>(a);
   if (kv + qc > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   a.kv_ctas = static_cast<int32_t>(kv);
-  return launch_pdl(kv_append_kernel<F16, D, TT, R>, dim3(static_cast<unsigned>(kv + qc)), dim3(TT), 0, st, a);
+  return launch_pdl(kv_append_pages_kernel<F16, D, TT, R>, dim3(static_cast<unsigned>(kv + qc)), dim3(TT), 0, st, a);
+}
+
+template <bool F16, int D>
+int launch_tokens(AppendArgs& a, cudaStream_t st) {
+  const int64_t qc = query_ctas<D, 128>(a);
+  if (a.units + qc > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  a.kv_ctas = a.units;
+  return launch_pdl(kv_append_tokens_kernel<F16, D>, dim3(static_cast<unsigned>(a.units + qc)), dim3(128), 0, st, a);
 }
 
 // One thread holds 16 values of a row, so a page takes page_size * dim / 16
@@ -281,16 +433,19 @@ int launch_append(AppendArgs& a, cudaStream_t st) {
 template <bool F16>
 int pick_append(AppendArgs& a, cudaStream_t st) {
   const int P = a.d.cache.page_size;
+  a.units = static_cast<int32_t>(a.d.T / P) + 2 * a.d.cache.batch;
+  // few new tokens a sequence: all heads of a page in one CTA (see the kernels)
+  if (a.d.T <= kFewTokens * a.d.cache.batch) return a.d.cache.dim == 64 ? launch_tokens<F16, 64>(a, st) : launch_tokens<F16, 128>(a, st);
   if (a.d.cache.dim == 64) {
-    if (P == 16) return launch_append<F16, 64, 64, 1>(a, st);
-    if (P == 32) return launch_append<F16, 64, 128, 1>(a, st);
-    if (P == 64) return launch_append<F16, 64, 256, 1>(a, st);
-    return launch_append<F16, 64, 256, 2>(a, st);
+    if (P == 16) return launch_pages<F16, 64, 64, 1>(a, st);
+    if (P == 32) return launch_pages<F16, 64, 128, 1>(a, st);
+    if (P == 64) return launch_pages<F16, 64, 256, 1>(a, st);
+    return launch_pages<F16, 64, 256, 2>(a, st);
   }
-  if (P == 16) return launch_append<F16, 128, 128, 1>(a, st);
-  if (P == 32) return launch_append<F16, 128, 256, 1>(a, st);
-  if (P == 64) return launch_append<F16, 128, 256, 2>(a, st);
-  return launch_append<F16, 128, 256, 4>(a, st);
+  if (P == 16) return launch_pages<F16, 128, 128, 1>(a, st);
+  if (P == 32) return launch_pages<F16, 128, 256, 1>(a, st);
+  if (P == 64) return launch_pages<F16, 128, 256, 2>(a, st);
+  return launch_pages<F16, 128, 256, 4>(a, st);
 }
 
 }  // namespace

@@ -104,3 +104,11 @@ def test_descriptors_match_the_header(moe):
             skip = {"const", "uint8_t", "float", "int32_t", "int64_t", "void", "moe_kv_cache"}
             fields += [w for w in words if w not in skip]
         assert fields == [f[0] for f in getattr(moe, name)._fields_], name
+
+
+def test_packed_descriptors_have_the_structures_layout(moe):
+    """The bytes that the calls pack are the structures' own."""
+    c = tuple(range(1, 22))
+    for pack, cls, n in ((moe._kv_append_pack, moe.moe_kv_append_desc, 19), (moe._kv_attention_pack, moe.moe_kv_attention_desc, 15)):
+        rest = tuple(range(30, 30 + n))
+        assert pack(*c, *rest) == bytes(cls(c, *rest))
