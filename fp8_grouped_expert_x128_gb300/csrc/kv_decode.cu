@@ -7,7 +7,7 @@
 // kv head) that several CTAs share is joined by the last of them to finish, from
 // the running maximum, sum and unnormalised output that each has left in the
 // workspace; parts are added in the order of their keys, so results repeat bit
-// for bit whichever CTA comes last.  More than 16 parts are joined in two levels.
+// for bit whichever CTA comes last.  More than 32 parts are joined in two levels.
 //
 // A warp takes 16 keys of a tile through a cp.async ring of its own (no barrier
 // inside a CTA's loop).  Both products run transposed on mma.m16n8k16 f16, S^T =
@@ -25,8 +25,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;                 // keys a warp takes at a time
 constexpr int kTile = kStep * kWarps;
-constexpr int kGroup = 16;                // parts joined at a time
+constexpr int kGroup = 32;                // parts joined at a time, one lane each
 constexpr int kMaxParts = 1024;           // CTAs of a launch at most
+static_assert(kMaxParts <= kGroup * kGroup, "two levels");
 static_assert(3 * kMaxParts == kDecodeCounters, "counters of the three levels");
 
 template <int D, int NT>
@@ -172,12 +173,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
   float* ring_scales = reinterpret_cast<float*>(smem + C::kScales) + warp * C::kStages * 2;
   float* buf = reinterpret_cast<float*>(smem + C::kBuf);
 
+  // ---- the first (sequence, kv head), and its queries on their way
+  int32_t ignored = 0;                     // the scan has told
+  int b = first_b;
+  Seq s = load_seq(d, b, &ignored);
+  Tiles t = tiles_of(a, s, C::kRows);
+  int h = static_cast<int>((u0 - first_u) / t.count);
+  int tile = t.first + static_cast<int>((u0 - first_u) % t.count);
+  uint4 qw[D / 32];                        // lane (g, c): a quarter of row g (of 8 rows a warp where they are shared)
+  const auto load_q = [&] {
+    const int r = (C::kSharedQ ? warp * 8 : 0) + g;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) qw[k] = make_uint4(0, 0, 0, 0);
+    if (r < s.n * a.G) {
+      const int i = r / a.G;
+      const uint16_t* qp = static_cast<const uint16_t*>(d.q) + (s.c0 + i) * d.q_token_ld + (h * a.G + r - i * a.G) * d.q_head_ld +
+                           c * (D / 4);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) qw[k] = __ldg(reinterpret_cast<const uint4*>(qp) + k);
+    }
+  };
+  load_q();
+
   // ---- producer: walks the CTA's units, kStages - 1 ahead of the consumer
   int64_t p_left = u1 - u0;
   int p_b = first_b, p_h, p_tile, p_end, p_base, p_stage = 0, p_pid = 0;
-  int32_t ignored = 0;                     // the scan has told
-  Seq p_s = load_seq(d, p_b, &ignored);
-  Tiles p_t = tiles_of(a, p_s, C::kRows);
+  Seq p_s = s;
+  Tiles p_t = t;
   // this lane's share of a step's copy: chunk ch of rows r, r + kRowsPer, ...
   constexpr int kChunks = D / 16, kRowsPer = 32 / kChunks;
   const int ld_r = lane / kChunks, ld_ch = lane % kChunks;
@@ -187,10 +209,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
     const int key = (p_tile + lane) * kTile + warp * kStep;
     p_pid = key < p_s.len ? __ldg(kc.page_table + p_b * kc.table_ld + (key >> page_shift)) : 0;
   };
-  p_h = static_cast<int>((u0 - first_u) / p_t.count);
-  p_tile = p_t.first + static_cast<int>((u0 - first_u) % p_t.count);
-  p_end = p_t.first + p_t.count;
-  const int first_h = p_h, first_tile = p_tile;
+  p_h = h;
+  p_tile = tile;
+  p_end = t.first + t.count;
   p_pages();
   const auto issue = [&] {
     if (p_left > 0) {
@@ -254,10 +275,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
   for (int i = 0; i < C::kStages - 1; ++i) issue();
 
   // ---- consumer: one (sequence, kv head) after the other
-  int stage = 0, b = first_b, h = first_h, tile = first_tile;
+  int stage = 0;
   int64_t u = u0;
-  Seq s = load_seq(d, b, &ignored);
-  Tiles t = tiles_of(a, s, C::kRows);
   while (true) {
     const int rows = s.n * a.G;
     const int tile_begin = tile;
@@ -275,23 +294,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
       s_hi[tid] = end_key(d, s, i);
     }
     if (!C::kSharedQ || warp < NT) {
-      const int r = (C::kSharedQ ? warp * 8 : 0) + g;
-      uint4 w[D / 32];
       float amax = 0.0f;
-      if (r < rows) {
-        const int i = r / a.G;
-        const uint16_t* qp = static_cast<const uint16_t*>(d.q) + (s.c0 + i) * d.q_token_ld +
-                             (h * a.G + r - i * a.G) * d.q_head_ld + c * (D / 4);
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) w[k] = __ldg(reinterpret_cast<const uint4*>(qp) + k);
-      } else {
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) w[k] = make_uint4(0, 0, 0, 0);
-      }
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         float f[8];
-        unpack8<F16>(w[k], f);
+        unpack8<F16>(qw[k], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = f[e] != f[e] ? INFINITY : fmaxf(amax, fabsf(f[e]));
       }
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         float f[8];
-        unpack8<F16>(w[k], f);
+        unpack8<F16>(qw[k], f);
         const uint2 x = make_uint2(f16x2(f[0] * mul, f[1] * mul), f16x2(f[2] * mul, f[3] * mul));
         const uint2 y = make_uint2(f16x2(f[4] * mul, f[5] * mul), f16x2(f[6] * mul, f[7] * mul));
         if constexpr (C::kSharedQ) {
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
       }
       inv *= d.softcap > 0.0f ? d.sm_scale / d.softcap : d.sm_scale * kLog2e;
       if constexpr (C::kSharedQ) {
-        if (c == 0) s_qs[r] = inv;
+        if (c == 0) s_qs[warp * 8 + g] = inv;
       } else {
         qs[0] = __shfl_sync(0xffffffffu, inv, 8 * c);     // of the columns of S^T that this lane holds
         qs[1] = __shfl_sync(0xffffffffu, inv, 8 * c + 4);
@@ -599,20 +606,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
       };
       // parts of CTAs first, first + stride, ... into buf, top and sum
       const auto join = [&](int first, int stride, int count) {
-        if (tid < C::kRows) {
-          top = -INFINITY;
-          sum = 0.0f;
-          if (tid < rows) {
-            for (int k = 0; k < count; ++k) top = fmaxf(top, __ldcg(part_of(first + k * stride) + tid));
-            for (int k = 0; k < count; ++k) {
-              const float* part = part_of(first + k * stride);
-              const float pm = __ldcg(part + tid);
-              sum += __ldcg(part + kDecodeRows + tid) * (pm == -INFINITY ? 1.0f : ex2(pm - top));
-            }
+        for (int r = warp; r < rows; r += kWarps) {
+          const float* part = part_of(first + min(lane, count - 1) * stride);
+          const float pm = lane < count ? __ldcg(part + r) : -INFINITY;
+          float pl = lane < count ? __ldcg(part + kDecodeRows + r) : 0.0f, pt = pm;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) pt = fmaxf(pt, __shfl_xor_sync(0xffffffffu, pt, o));
+          pl *= pm == -INFINITY ? 1.0f : ex2(pm - pt);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) pl += __shfl_xor_sync(0xffffffffu, pl, o);
+          if (lane == 0) {
+            s_m[0][r] = pt;
+            s_l[0][r] = pl;
           }
-          s_m[0][tid] = top;
         }
         __syncthreads();
+        if (tid < rows) {
+          top = s_m[0][tid];
+          sum = s_l[0][tid];
+        }
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
           const int r = x / (D / 4), e = x % (D / 4) * 4;
           float4 acc = make_float4(0, 0, 0, 0);
@@ -663,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
       } while (t.count == 0 && b + 1 < kc.batch);
     }
     tile = t.first;
+    load_q();
     __syncthreads();                       // buf and the statistics are free
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
