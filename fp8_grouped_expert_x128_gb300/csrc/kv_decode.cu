@@ -625,21 +625,43 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
           top = s_m[0][tid];
           sum = s_l[0][tid];
         }
-        for (int x = tid; x < rows * (D / 4); x += kThreads) {
-          const int r = x / (D / 4), e = x % (D / 4) * 4;
-          float4 acc = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-          for (int k = 0; k < count; ++k) {
-            const float* part = part_of(first + k * stride);
-            const float pm = __ldcg(part + r);
-            const float keep = pm == -INFINITY ? 1.0f : ex2(pm - s_m[0][r]);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + 2 * kDecodeRows + r * D + e));
-            acc.x = fmaf(v.x, keep, acc.x);
-            acc.y = fmaf(v.y, keep, acc.y);
-            acc.z = fmaf(v.z, keep, acc.z);
-            acc.w = fmaf(v.w, keep, acc.w);
+        // some 16 loads a thread under way; rows that are none load the last one's
+        constexpr int kItems = C::kRows * (D / 4) / kThreads, kAtOnce = kItems >= 8 ? 2 : 16 / kItems;
+        float4 acc[kItems];
+#pragma unroll
+        for (int y = 0; y < kItems; ++y) acc[y] = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int k0 = 0; k0 < count; k0 += kAtOnce) {
+          float pm[kAtOnce][kItems];
+          float4 v[kAtOnce][kItems];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            const float* part = part_of(first + min(k0 + k, count - 1) * stride);
+#pragma unroll
+            for (int y = 0; y < kItems; ++y) {
+              const int r = min((tid + y * kThreads) / (D / 4), rows - 1), e = tid % (D / 4) * 4;
+              pm[k][y] = __ldcg(part + r);
+              v[k][y] = __ldcg(reinterpret_cast<const float4*>(part + 2 * kDecodeRows + r * D + e));
+            }
           }
-          *reinterpret_cast<float4*>(buf + r * C::kLd + e) = acc;
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+            for (int y = 0; y < kItems; ++y) {
+              const int r = min((tid + y * kThreads) / (D / 4), rows - 1);
+              float keep = pm[k][y] == -INFINITY ? 1.0f : ex2(pm[k][y] - s_m[0][r]);
+              if (k0 + k < count) {
+                acc[y].x = fmaf(v[k][y].x, keep, acc[y].x);
+                acc[y].y = fmaf(v[k][y].y, keep, acc[y].y);
+                acc[y].z = fmaf(v[k][y].z, keep, acc[y].z);
+                acc[y].w = fmaf(v[k][y].w, keep, acc[y].w);
+              }
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < kItems; ++y) {
+          const int r = (tid + y * kThreads) / (D / 4), e = tid % (D / 4) * 4;
+          *reinterpret_cast<float4*>(buf + r * C::kLd + e) = acc[y];
         }
         __syncthreads();
       };
