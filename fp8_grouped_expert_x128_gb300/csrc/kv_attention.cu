@@ -24,7 +24,9 @@ int check_attention(const moe_kv_attention_desc* d) {
 using namespace moe;
 
 extern "C" size_t moe_kv_attention_workspace_size(const moe_kv_attention_desc* d) {
-  return check_attention(d) == MOE_OK ? kv_decode_workspace() : 0;
+  if (check_attention(d) != MOE_OK) return 0;
+  const size_t few = kv_decode_workspace(), many = kv_prefill_workspace();
+  return kDecodeCounters * sizeof(int32_t) + (few > many ? few : many);
 }
 
 extern "C" int moe_kv_attention(const moe_kv_attention_desc* d, void* workspace, size_t workspace_bytes, void* stream) {

@@ -21,7 +21,9 @@ struct AttnArgs {
 };
 
 int kv_decode_launch(const AttnArgs& a, int64_t max_rows, cudaStream_t st);
+// Bytes of parts that each may leave (one after the other, in the same place).
 size_t kv_decode_workspace();
+size_t kv_prefill_workspace();
 int kv_prefill_launch(const AttnArgs& a, cudaStream_t st);
 
 namespace {

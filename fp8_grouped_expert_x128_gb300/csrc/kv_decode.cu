@@ -728,7 +728,7 @@ int pick_rows(const AttnArgs& a, int64_t rows, cudaStream_t st) {
 
 size_t kv_decode_workspace() {
   const size_t ctas = static_cast<size_t>(min(kMaxParts, num_sms() * 4));      // of the kernel with most
-  return kDecodeCounters * sizeof(int32_t) + ctas * 2 * kPartFloats * sizeof(float);
+  return ctas * 2 * kPartFloats * sizeof(float);
 }
 
 int kv_decode_launch(const AttnArgs& a, int64_t max_rows, cudaStream_t st) {

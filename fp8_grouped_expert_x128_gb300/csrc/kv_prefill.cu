@@ -157,8 +157,49 @@ __device__ __forceinline__ Steps steps_of(const AttnArgs& a, const Seq& s, int r
   return {first_key(a.d, s, r0 / a.G) / kKeys, (end_key(a.d, s, (r1 - 1) / a.G) + kKeys - 1) / kKeys};
 }
 
+// A unit: up to 256 rows of a sequence.  Units of sequence b start at cu[b] * G / 256 +
+// b: enough for its rows whatever cu is, and nothing has to be summed.  Its keys are
+// cut into `splits` runs of `chunk` steps (an even number: whole blocks), fewer than
+// asked for where they would be short.
+struct Unit {
+  int b, rows, row0, row_end, splits, chunk;
+  Seq s;
+  Steps all;
+};
+constexpr int kMinChunk = 8;             // steps
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int unit, int splits) {
+  const moe_kv_cache& kc = a.d.cache;
+  const auto unit0 = [&](int b) {
+    return static_cast<int>(static_cast<int64_t>(__ldg(kc.cu_new + b)) * a.G / (2 * kTileRows)) + b;
+  };
+  Unit u;
+  u.splits = 0;
+  u.b = warp_find(kc.batch, unit, unit0);
+  int32_t bad = 0;
+  u.s = load_seq(a.d, u.b, &bad);          // faults are told by the decode kernel
+  u.rows = u.s.n * a.G;
+  if (u.rows <= kDecodeRows) return u;
+  const int tiles2 = (u.rows + 2 * kTileRows - 1) / (2 * kTileRows);
+  const int nth = tiles2 - 1 - (unit - unit0(u.b));         // the last rows, with the most keys, first
+  if (nth < 0 || nth >= tiles2) return u;
+  u.row0 = nth * 2 * kTileRows;
+  u.row_end = min(u.rows, u.row0 + 2 * kTileRows);
+  u.all = steps_of(a, u.s, u.row0, u.row_end);
+  const int steps = u.all.end - u.all.first;
+  u.chunk = steps;
+  if (splits > 1) {
+    u.all.first &= ~1;
+    u.chunk = max(kMinChunk, ((u.all.end - u.all.first + splits - 1) / splits + 1) & ~1);
+  }
+  u.splits = (u.all.end - u.all.first + u.chunk - 1) / u.chunk;
+  return u;
+}
+// A split's part: m[256], l[256], O[256][D], O not divided by l.
+template <int D>
+constexpr int64_t kSplitFloats = 2 * kTileRows * (D + 2);
+
 template <bool F16, int D, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_constant__ AttnArgs a, uint64_t wait_ns) {
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_constant__ AttnArgs a, int splits) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -170,25 +211,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // ---- the unit's rows.  Units of sequence b start at cu[b] * G / 256 + b: enough
-  // for its rows whatever cu is, and nothing has to be summed.
-  const int h = blockIdx.x % H, unit = blockIdx.x / H;
-  const auto unit0 = [&](int b) {
-    return static_cast<int>(static_cast<int64_t>(__ldg(kc.cu_new + b)) * a.G / (2 * kTileRows)) + b;
-  };
-  const int b = warp_find(kc.batch, unit, unit0);
-  int32_t bad = 0;
-  const Seq s = load_seq(d, b, &bad);    // faults are told by the decode kernel
-  const int rows = s.n * a.G;
-  if (rows <= kDecodeRows) return;
-  const int tiles2 = (rows + 2 * kTileRows - 1) / (2 * kTileRows);
-  const int nth = tiles2 - 1 - (unit - unit0(b));           // the last rows, with the most keys, first
-  if (nth < 0 || nth >= tiles2) return;
-  const int row0 = nth * 2 * kTileRows, row_end = min(rows, row0 + 2 * kTileRows);
+  const int split = blockIdx.x % splits, h = blockIdx.x / splits % H;
+  const Unit w = unit_of(a, blockIdx.x / splits / H, splits);
+  if (split >= w.splits) return;           // the unit has no rows, or needs fewer splits
+  const int b = w.b, rows = w.rows, row0 = w.row0, row_end = w.row_end;
+  const Seq s = w.s;
   const int tiles = row_end - row0 > kTileRows ? 2 : 1;
-  const Steps all = steps_of(a, s, row0, row_end);
-  const Steps mine0 = steps_of(a, s, row0, min(row0 + kTileRows, row_end));
-  const Steps mine1 = tiles == 2 ? steps_of(a, s, row0 + kTileRows, row_end) : Steps{all.end, all.end};
+  // this CTA's steps, of all rows and of each tile's (a tile may have none in a split)
+  const Steps all = {w.all.first + split * w.chunk, min(w.all.end, w.all.first + (split + 1) * w.chunk)};
+  const auto mine = [&](int r0, int r1) {
+    const Steps m = steps_of(a, s, r0, r1);
+    return Steps{max(m.first, all.first), min(m.end, all.end)};
+  };
+  const Steps mine0 = mine(row0, min(row0 + kTileRows, row_end));
+  const Steps mine1 = tiles == 2 ? mine(row0 + kTileRows, row_end) : Steps{all.end, all.end};
   const int block0 = all.first >> 1, block1 = (all.end + 1) >> 1;   // blocks to widen
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -214,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const auto wait = [&](int i, int phase) { return mbar_wait_bounded(bar(i), phase & 1, abort, d.err, wait_ns); };
+  const auto wait = [&](int i, int phase) { return mbar_wait_bounded(bar(i), phase & 1, abort, d.err, kWaitLimitNs); };
 
   if (wg == 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -276,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         int dummy = 0;
         umma_commit(bar(kQFull));        // completes phase 1 of a barrier that nobody else waits on any more
         for (int k = 1; k < 128 * tiles; ++k) mbar_arrive(bar(kQFull));
-        mbar_wait_bounded(bar(kQFull), 1, &dummy, nullptr, wait_ns / 10);
+        mbar_wait_bounded(bar(kQFull), 1, &dummy, nullptr, kWaitLimitNs / 10);
       }
       __syncwarp();
     }
@@ -538,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       tc_fence_before();
       mbar_arrive(bar(kPFull + 2 * wg + buf));
     }
-    if (ok) ok = wait(kOFull + 2 * wg + ((m.end - 1) & 1), (m.end - m.first - 1) >> 1);
+    const bool none = m.first >= m.end;                  // of this split's keys; O was never written then
+    if (ok && !none) ok = wait(kOFull + 2 * wg + ((m.end - 1) & 1), (m.end - m.first - 1) >> 1);
     if (ok) {
       tc_fence_after();
       uint32_t nans[D / 32];
@@ -547,7 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       if (*static_cast<volatile int*>(&s_nan)) {
         // NaN codes that were taken out of blocks with rows that do not see them all
         const int hi_all = end_key(d, s, row0 / a.G), lo_all = first_key(d, s, (row_end - 1) / a.G);
-        for (int key = lo; key < hi; ++key) {
+        const int to = min(hi, all.end * kKeys);
+        for (int key = max(lo, all.first * kKeys); key < to; ++key) {
           const int k0 = key & ~(kBlock - 1);
           if (!(k0 < lo_all || k0 + kBlock > hi_all)) {
             key = max(key, (hi_all & ~(kBlock - 1)) - 1);
@@ -562,8 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
               if ((vp[32 * k + e] & 0x7F) == 0x7F) nans[k] |= 1u << e;
         }
       }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = w.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
       uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(d.out) + (s.c0 + i) * d.o_token_ld + head * d.o_head_ld);
+      float* part = a.parts + static_cast<int64_t>(blockIdx.x) * kSplitFloats<D> + wg * kTileRows + t;
+      if (w.splits > 1 && live) {
+        part[0] = top;
+        part[2 * kTileRows] = sum;
+      }
+      float4* part_o = reinterpret_cast<float4*>(part - (wg * kTileRows + t) + 4 * kTileRows + (wg * kTileRows + t) * D);
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         uint32_t o[32];
@@ -575,12 +619,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
             float f[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-              f[y] = (nans[k] >> (e + y)) & 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(o[e + y]) * inv;
-            op[4 * k + e / 8] = pack8<F16>(f);
+              f[y] = (nans[k] >> (e + y)) & 1u ? __uint_as_float(0x7FC00000u) : none ? 0.0f : __uint_as_float(o[e + y]) * inv;
+            if (w.splits > 1) {
+              part_o[8 * k + e / 4] = make_float4(f[0], f[1], f[2], f[3]);
+              part_o[8 * k + e / 4 + 1] = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+              op[4 * k + e / 8] = pack8<F16>(f);
+            }
           }
         }
       }
-      if (live && d.lse != nullptr)
+      if (live && w.splits == 1 && d.lse != nullptr)
         d.lse[static_cast<int64_t>(s.c0 + i) * d.q_heads + head] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
     }
   } else {
@@ -593,6 +642,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Fewer units than SMs: their keys are split so that every SM has some, if they are
+// long enough for it (what the page table can hold is all the host knows of them).
+int prefill_splits(const AttnArgs& a, int64_t units) {
+  const int64_t keys = static_cast<int64_t>(a.d.cache.max_pages) * a.d.cache.page_size;
+  const int64_t by_sms = num_sms() / units, by_keys = keys / (kMinChunk * kKeys);
+  const int64_t n = by_sms < by_keys ? by_sms : by_keys;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+// Joins the splits' parts, a warp to a row, in the order of the keys.
+constexpr int kJoinRows = 8;             // rows (warps) of a CTA
+template <bool F16, int D>
+__global__ void __launch_bounds__(32 * kJoinRows) kv_prefill_join_kernel(const __grid_constant__ AttnArgs a, int splits) {
+  const moe_kv_attention_desc& d = a.d;
+  const int H = d.cache.kv_heads, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  constexpr int kPer = 2 * kTileRows / kJoinRows;
+  const int at = blockIdx.x / kPer, h = at % H;
+  const Unit w = unit_of(a, at / H, splits);
+  const int local = blockIdx.x % kPer * kJoinRows + (threadIdx.x >> 5);
+  if (w.splits <= 1 || w.row0 + local >= w.row_end) return;
+  const float* part = a.parts + static_cast<int64_t>(at) * splits * kSplitFloats<D>;
+  float top = -INFINITY;
+  for (int k = lane; k < w.splits; k += 32) top = fmaxf(top, __ldcg(part + k * kSplitFloats<D> + local));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  constexpr int E = D / 32;
+  float acc[E], sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 8
+  for (int k = 0; k < w.splits; ++k) {
+    const float* p = part + k * kSplitFloats<D>;
+    const float pm = __ldcg(p + local), pl = __ldcg(p + 2 * kTileRows + local);
+    const float keep = pm == -INFINITY ? 1.0f : ex2(pm - top);   // a part without weights may hold a NaN
+    sum = fmaf(pl, keep, sum);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(p + 4 * kTileRows + static_cast<int64_t>(local) * D + lane * E + e));
+      acc[e] = fmaf(v.x, keep, acc[e]);
+      acc[e + 1] = fmaf(v.y, keep, acc[e + 1]);
+    }
+  }
+  const int r = w.row0 + local, i = r / a.G, head = h * a.G + r - i * a.G;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t* op = static_cast<uint16_t*>(d.out) + (w.s.c0 + i) * d.o_token_ld + head * d.o_head_ld + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(op + e) = pair_from_float<F16>(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && d.lse != nullptr)
+    d.lse[static_cast<int64_t>(w.s.c0 + i) * d.q_heads + head] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 template <bool F16, int D, bool CAP>
@@ -610,8 +712,13 @@ int launch(const AttnArgs& a, cudaStream_t st) {
     __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
   }
   const int64_t units = (a.d.T * a.G / (2 * kTileRows) + a.d.cache.batch) * a.d.cache.kv_heads;
-  if (units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(units)), dim3(kThreads), Cfg<D>::kSmem, st, a, kWaitLimitNs);
+  const int splits = prefill_splits(a, units);
+  if (units * splits * (2 * kTileRows / kJoinRows) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(units * splits));
+  if (int rc = launch_pdl(kernel, grid, dim3(kThreads), Cfg<D>::kSmem, st, a, splits)) return rc;
+  if (splits == 1) return MOE_OK;
+  return launch_pdl(kv_prefill_join_kernel<F16, D>, dim3(static_cast<unsigned>(units * (2 * kTileRows / kJoinRows))),
+                    dim3(32 * kJoinRows), 0, st, a, splits);
 }
 
 template <bool F16, int D>
@@ -620,6 +727,8 @@ int pick_cap(const AttnArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+size_t kv_prefill_workspace() { return static_cast<size_t>(num_sms()) * kSplitFloats<128> * sizeof(float); }
 
 int kv_prefill_launch(const AttnArgs& a, cudaStream_t st) {
   const bool f16 = a.d.cache.dtype == MOE_DTYPE_F16;

@@ -372,6 +372,24 @@ def test_attention_long_sequence_splits(lib):
     check_attention(lib, [9000, 5000], [20, 12], 1, 8, 128, 128, "f16")
 
 
+@pytest.mark.parametrize("dim,dtype,window,softcap,full", [
+    (128, "bf16", 0, 0.0, False), (64, "f16", 3000, 0.0, False), (128, "f16", 0, 20.0, False), (64, "bf16", 0, 0.0, True),
+    (128, "bf16", 700, 0.0, False)])
+def test_attention_many_rows_split_over_keys(lib, dim, dtype, window, softcap, full):
+    # more rows than the decode kernel takes, too few for all SMs; runs of keys that some rows or a whole tile do not see
+    check_attention(lib, [7013, 40, 900, 2500], [40, 40, 33, 9], 1, 4, dim, 64, dtype, window=window, softcap=softcap, full=full)
+    check_attention(lib, [5000], [300], 1, 1, dim, 32, dtype, window=window, softcap=softcap, full=full)
+
+
+def test_attention_nan_in_a_split(lib):
+    c = Cache([6000], [50], 1, 64, 16)
+    for j, d in ((5990, 5), (3000, 9), (20, 63)):
+        c.v[int(c.table[0, j // 16]), 0, j % 16, d] = 0x7F
+    got = check_attention(lib, [6000], [50], 1, 2, 64, 16, cache=c)
+    assert torch.isnan(got[:, :, 9]).all() and torch.isnan(got[:, :, 63]).all()
+    assert torch.isnan(got[40:, :, 5]).all() and not torch.isnan(got[:40, :, 5]).any()
+
+
 def test_attention_sharp_and_large_scores(lib):
     # one token takes all the weight; scores of some hundreds
     check_attention(lib, [300, 70], [1, 40], 2, 4, 128, 32, q_gain=8.0)
