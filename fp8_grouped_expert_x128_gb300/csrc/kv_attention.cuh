@@ -30,10 +30,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Weights are exponentials relative to a reference that follows the running
-// maximum only once it is this far (in powers of two) behind: up to 2^8, well
-// inside f16, and a column is rescaled rarely.
-constexpr float kLazy = 8.0f;
+// Weights are exponentials relative to a reference that follows the running maximum
+// only once it is this far (in powers of two) behind: weights stay below 2^14, inside
+// f16, and what a row has so far is rescaled rarely.  (A larger lag costs no precision:
+// what f16 loses of small weights lies that much further below the maximum.)
+constexpr float kLazy = 14.0f;
 // A V scale this small counts as this: weights carry the scale as its logarithm.
 constexpr float kMinScale = 7.888609e-31f;   // 2^-100
 

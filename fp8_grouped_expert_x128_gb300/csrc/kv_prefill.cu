@@ -149,6 +149,28 @@ __device__ __forceinline__ float4 lds16f(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The largest |x| of 8 elements; NaN if one is.
+template <bool F16>
+__device__ __forceinline__ float abs_max8(const uint4& u) {
+  uint32_t m;
+  if constexpr (F16) {
+    const auto h = [](uint32_t x) { return *reinterpret_cast<const __half2*>(&x); };
+    const __half2 r = __hmax2_nan(__hmax2_nan(__habs2(h(u.x)), __habs2(h(u.y))), __hmax2_nan(__habs2(h(u.z)), __habs2(h(u.w))));
+    m = *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const auto h = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    const __nv_bfloat162 r = __hmax2_nan(__hmax2_nan(__habs2(h(u.x)), __habs2(h(u.y))), __hmax2_nan(__habs2(h(u.z)), __habs2(h(u.w))));
+    m = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const float2 f = pair_to_float<F16>(m);
+  return fmax_nan(f.x, f.y);
+}
+
 // Steps [first, end) of kKeys keys that the rows [r0, r1) of a sequence see.
 struct Steps {
   int first, end;
@@ -342,13 +364,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     pages = look_up(pages_from);
     pages_next = look_up(pages_from + 32);
     uint4 reg[2][kIter];                               // K's and V's codes, loaded a block ahead
-    const auto load = [&](uint4& r, int i, int j, const uint8_t* base, int64_t page_ld, int64_t slot_ld) {
-      const int key = j * kBlock + i * kRowsPer + r0;
-      const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
+    // Address of a 16-key group's rows: a 32 x 32 bit product for the page (strides are
+    // multiples of 16), a term for the group that all lanes share and one for the lane.
+    // The row within its page is (i, j)'s part plus r0's, whatever the page size.
+    const auto load = [&](uint4& r, int i, int j, const uint8_t* base, uint32_t page_ld16, int64_t slot_ld) {
+      const int key0 = j * kBlock + i * kRowsPer;
+      const int page = __shfl_sync(0xffffffffu, pages, ((key0 + r0) >> 4) - pages_from);
+      const uint8_t* p = base + (static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_ld16 << 4) + (key0 & (P - 1)) * slot_ld;
       // past the end, or a page that is none: zeros
-      r = ldg_stream(base + page * page_ld + (key & (P - 1)) * slot_ld, key < s.len && page >= 0);
+      r = ldg_stream(p, key0 + r0 < s.len && page >= 0);
     };
-    const uint8_t* base[2] = {kc.k + h * kc.k_head_ld + ch * 16, kc.v + h * kc.v_head_ld + ch * 16};
+    const uint8_t* base[2] = {kc.k + h * kc.k_head_ld + (r0 & (P - 1)) * kc.k_slot_ld + ch * 16,
+                              kc.v + h * kc.v_head_ld + (r0 & (P - 1)) * kc.v_slot_ld + ch * 16};
+    const uint32_t page_ld16[2] = {static_cast<uint32_t>(kc.k_page_ld >> 4), static_cast<uint32_t>(kc.v_page_ld >> 4)};
     // scales of a block's 16-key groups, by the first warp's first lanes: (K, V)
     float2 scales;
     const auto load_scales = [&](int j) {
@@ -362,9 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     };
     load_scales(block0);
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) load(reg[0][i], i, block0, base[0], kc.k_page_ld, kc.k_slot_ld);
+    for (int i = 0; i < kIter; ++i) load(reg[0][i], i, block0, base[0], page_ld16[0], kc.k_slot_ld);
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) load(reg[1][i], i, block0, base[1], kc.v_page_ld, kc.v_slot_ld);
+    for (int i = 0; i < kIter; ++i) load(reg[1][i], i, block0, base[1], page_ld16[1], kc.v_slot_ld);
     bool ok = true;
 #pragma unroll 1
     for (int j = block0; ok && j < block1; ++j) {
@@ -412,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         for (int i = 0; i < kIter; ++i) {
           const uint4 w = reg[is_v][i];
           if (more)
-            load(reg[is_v][i], i, j + 1, base[is_v], is_v ? kc.v_page_ld : kc.k_page_ld, is_v ? kc.v_slot_ld : kc.k_slot_ld);
+            load(reg[is_v][i], i, j + 1, base[is_v], page_ld16[is_v], is_v ? kc.v_slot_ld : kc.k_slot_ld);
           sts16(at_lo + i * kRowsPer * 128,
                 make_uint4(e4m3x2_to_f16x2(w.x & 0xFFFF), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y & 0xFFFF),
                            e4m3x2_to_f16x2(w.y >> 16)));
@@ -452,25 +480,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d.q) + (s.c0 + i0 + up) * d.q_token_ld +
                                                     (h * a.G + x - up * a.G) * d.q_head_ld) + c16);
       }
+      // The rows' maxima: of each lane's 8 elements, then over a row's lanes for all rows
+      // at once -- halves of the rows change sides at every step, until a lane has one row.
+      float amax[kLanes];
+#pragma unroll
+      for (int k = 0; k < kLanes; ++k) amax[k] = abs_max8<F16>(w[k]);
+#pragma unroll
+      for (int half = kLanes / 2; half > 0; half >>= 1)
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+          const bool up = (c16 & half) != 0;
+          const float give = up ? amax[k] : amax[k + half], keep = up ? amax[k + half] : amax[k];
+          const float got = __shfl_xor_sync(0xffffffffu, give, half);
+          amax[k] = fmax_nan(keep, got);
+        }
+      float mul, inv;
+      row_scale(amax[0], mul, inv);        // of row c16 * kAtOnce + sub
+      mul = copysignf(mul, d.sm_scale);
+      // this thread's own row is row lane of the 32
+      qs = __shfl_sync(0xffffffffu, inv, lane % kAtOnce * kLanes + lane / kAtOnce);
       const uint32_t tile = sbase + C::kQ + wg * C::kTileBytes + (c16 >> 3) * 16384;
 #pragma unroll
       for (int k = 0; k < kLanes; ++k) {
-        float f[8], amax = 0.0f;
+        float f[8];
         unpack8<F16>(w[k], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = f[e] != f[e] ? INFINITY : fmaxf(amax, fabsf(f[e]));
-#pragma unroll
-        for (int x = 1; x < kLanes; x <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
-        float mul, inv;
-        row_scale(amax, mul, inv);
-        // row lane belongs to group lane / kAtOnce, there to the lanes from lane % kAtOnce * kLanes on
-        const float got = __shfl_sync(0xffffffffu, inv, lane % kAtOnce * kLanes);
-        if (lane / kAtOnce == k) qs = got;
-        mul = copysignf(mul, d.sm_scale);
+        const float m = __shfl_sync(0xffffffffu, mul, sub * kLanes + k);
         const int row = (warp & 3) * 32 + k * kAtOnce + sub;           // of the tile
         sts16(tile + row * 128 + (((c16 & 7) ^ (row & 7)) << 4),
-              make_uint4(f16x2(f[0] * mul, f[1] * mul), f16x2(f[2] * mul, f[3] * mul), f16x2(f[4] * mul, f[5] * mul),
-                         f16x2(f[6] * mul, f[7] * mul)));
+              make_uint4(f16x2(f[0] * m, f[1] * m), f16x2(f[2] * m, f[3] * m), f16x2(f[4] * m, f[5] * m),
+                         f16x2(f[6] * m, f[7] * m)));
       }
       qs *= fabsf(CAP ? d.sm_scale / d.softcap : d.sm_scale * kLog2e);
       fence_proxy_async_shared();
