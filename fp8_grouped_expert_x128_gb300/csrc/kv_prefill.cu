@@ -28,7 +28,7 @@ constexpr int kStages = 2;               // of K and of V blocks
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kMinQScale = 8.6736174e-19f, kMinKScale = 8.6736174e-19f;   // 2^-60 each
-constexpr int kRegsSoftmax = 152, kRegsWiden = 72, kRegsIssue = 32;
+constexpr int kRegsSoftmax = 136, kRegsWiden = 80, kRegsIssue = 48;
 static_assert(256 * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreads * kLaunchRegs, "register split");
 
 template <int D>
@@ -46,8 +46,8 @@ struct Cfg {
 
 // mbarriers, in order.  S, P and O have one for each buffer of a tile: two steps can be
 // under way, and a barrier must not get two phases ahead of who waits for it.
-enum { kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
-       kPFull = kSFull + 4, kOFull = kPFull + 4, kBarCount = kOFull + 4 };
+enum { kQFull, kEmpty = kQFull + 2, kKFull, kVFull = kKFull + 2, kSFull = kVFull + 2, kPFull = kSFull + 4,
+       kOFull = kPFull + 4, kBarCount = kOFull + 4 };
 
 // Instruction descriptor, kind::f16: D fp32, A and B f16, A K-major; B K-major or
 // (mn) with its N dimension contiguous.
@@ -256,9 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   volatile int* abort = &s_abort;
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
-      const bool widen = i == kKFull || i == kKFull + 1 || i == kVFull || i == kVFull + 1;
-      const bool soft = i >= kPFull && i < kPFull + 4;
-      mbar_init(bar(i), i == kQFull ? 128 * tiles : widen ? kWidenThreads : soft ? 128 : 1);
+      const bool widen = i >= kKFull && i < kVFull + 2, rows128 = i < kQFull + 2 || (i >= kPFull && i < kPFull + 4);
+      mbar_init(bar(i), widen ? kWidenThreads : rows128 ? 128 : i == kEmpty ? tiles : 1);
     }
     s_abort = 0;
     s_nan = 0;
@@ -276,65 +275,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
 
   if (wg == 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == kIssueWarp) {
-      // ------------------------------------------------------------ MMA issue
-      // S has two buffers a tile: step g + 2 goes where step g was.  Per step and tile:
-      // P V of step g, then S of step g + 2 over the space that its P took (MMAs of one
-      // thread run in order), so that S of step g + 1 is there when its softmax begins.
+    const int i = warp - kIssueWarp;
+    if (i < tiles) {
+      // ------------------------------------------------------------ MMA issue, a warp for each tile
+      // S has two buffers a tile: step g + 2 goes where step g was.  Per step: P V of
+      // step g, then S of step g + 2 over the space that its P took (MMAs of one thread
+      // run in order), so that S of step g + 1 is there when its softmax begins.  The
+      // commit of S tells of that P V too; the last two steps, which have no S after
+      // them, have a commit of their own.  Every block is waited for and released by
+      // both warps, whether its tile reads it or not.
       const uint32_t id_s = idesc_f16(kKeys, false), id_o = idesc_f16(D, true);
       const uint32_t lead = elect_one();
-      bool ok = __all_sync(0xffffffffu, wait(kQFull, 0)), any = false;
-      int k_at = block0 - 1, v_at = block0 - 1;            // last blocks that were waited for
+      const auto all_wait = [&](int which, int phase) { return __all_sync(0xffffffffu, wait(which, phase)); };
+      const Steps m = i ? mine1 : mine0;
+      const uint32_t to = tmem + C::kTmemO + i * D, ts = tmem + i * 128;
+      const uint32_t qd = desc_lo(sbase + C::kQ + i * C::kTileBytes, 16);
+      bool ok = all_wait(kQFull + i, 0), any = false;
 #pragma unroll 1
-      for (int g = all.first - 2; ok && g < all.end; ++g) {
-        const int buf = g & 1, x = g + 2;
-        const int vst = ((g >> 1) - block0) & 1, kst = ((x >> 1) - block0) & 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Steps m = i ? mine1 : mine0;
-          if (ok && g >= m.first && g < m.end) {
-            if (v_at < (g >> 1)) {
-              v_at = g >> 1;
-              ok = wait(kVFull + vst, (v_at - block0) >> 1);
-            }
-            ok = __all_sync(0xffffffffu, ok && wait(kPFull + 2 * i + buf, (g - m.first) >> 1));
+      for (int g2 = (all.first & ~1) - 2; ok && g2 < all.end; g2 += 2) {
+        const int vb = (g2 >> 1) - block0, kb = vb + 1;               // blocks that are read (V of -1: none)
+        const bool more = kb < block1 - block0;
+        if (vb >= 0) ok = all_wait(kVFull + (vb & 1), vb >> 1);
+        if (ok && more) ok = all_wait(kKFull + (kb & 1), kb >> 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int buf = 0; buf < 2; ++buf) {
+          const int g = g2 + buf;
+          const uint32_t half = buf * kKeys;
+          const bool next = g + 2 >= m.first && g + 2 < m.end;
+          if (g >= m.first && g < m.end) {
+            ok = all_wait(kPFull + 2 * i + buf, (g - m.first) >> 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t vd = desc_lo(sbase + C::kV + vst * C::kTileBytes + buf * kKeys * 128, 16384);
+            const uint32_t vd = desc_lo(sbase + C::kV + (vb & 1) * C::kTileBytes + half * 128, 16384);
             const uint32_t acc = g > m.first;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + C::kTmemO + i * D, tmem + i * 128 + buf * kKeys + 8 * k, vd + 128 * k, id_o, k > 0 ? 1u : acc, lead);
-            commit(bar(kOFull + 2 * i + buf), lead);
+            for (int k = 0; k < kKeys / 16; ++k) mma_ts(to, ts + half + 8 * k, vd + 128 * k, id_o, k > 0 ? 1u : acc, lead);
+            if (!next) commit(bar(kOFull + 2 * i + buf), lead);
           }
-          if (ok && x >= m.first && x < m.end) {
-            if (k_at < (x >> 1)) {
-              k_at = x >> 1;
-              ok = __all_sync(0xffffffffu, wait(kKFull + kst, (k_at - block0) >> 1));
-              if (!ok) break;
-              tc_fence_after();
-            }
-            const uint32_t qd = desc_lo(sbase + C::kQ + i * C::kTileBytes, 16);
-            const uint32_t kd = desc_lo(sbase + C::kK + kst * C::kTileBytes + buf * kKeys * 128, 16);
+          if (next) {
+            const uint32_t kd = desc_lo(sbase + C::kK + (kb & 1) * C::kTileBytes + half * 128, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t at = (k >> 2) * 1024 + (k & 3) * 2;
-              mma_ss(tmem + i * 128 + buf * kKeys, qd + at, kd + at, id_s, k > 0 ? 1u : 0u, lead);
+              mma_ss(ts + half, qd + at, kd + at, id_s, k > 0 ? 1u : 0u, lead);
             }
             commit(bar(kSFull + 2 * i + buf), lead);
             any = true;
           }
         }
-        if (!ok) break;
-        if (g >= all.first && (buf || g == all.end - 1)) commit(bar(kVEmpty + vst), lead);
-        if (x < all.end && (buf || x == all.end - 1)) commit(bar(kKEmpty + kst), lead);
+        if (ok) commit(bar(kEmpty), lead);
       }
       if (!ok && any && lead) {
         // the MMAs in flight end before TMEM is freed: the commit below follows them
         int dummy = 0;
-        umma_commit(bar(kQFull));        // completes phase 1 of a barrier that nobody else waits on any more
-        for (int k = 1; k < 128 * tiles; ++k) mbar_arrive(bar(kQFull));
-        mbar_wait_bounded(bar(kQFull), 1, &dummy, nullptr, kWaitLimitNs / 10);
+        umma_commit(bar(kQFull + i));    // completes phase 1 of a barrier that nobody else waits on any more
+        for (int k = 1; k < 128; ++k) mbar_arrive(bar(kQFull + i));
+        mbar_wait_bounded(bar(kQFull + i), 1, &dummy, nullptr, kWaitLimitNs / 10);
       }
       __syncwarp();
     }
@@ -396,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     bool ok = true;
 #pragma unroll 1
     for (int j = block0; ok && j < block1; ++j) {
-      const int n = j - block0, st = n & 1, use = n >> 1;
+      const int n = j - block0, st = n & 1;
       const bool more = j + 1 < block1;
       float2 now = scales;
       if (more) {
@@ -409,7 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       }
 #pragma unroll
       for (int is_v = 0; is_v < 2; ++is_v) {
-        if (use > 0) ok = ok && wait((is_v ? kVEmpty : kKEmpty) + st, use - 1);
+        // kEmpty's phase e: K up to block e and V up to block e - 1 are read.  V of block
+        // n takes the place of n - 2's; K of block n + 1, which comes next, that of n - 1's.
+        if (is_v && n > 0) ok = wait(kEmpty, n - 1);
         if (!ok) break;
         if (!is_v && t < 8) {
           // the V scale as its logarithm and inverse, which is what the weights take
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       }
       qs *= fabsf(CAP ? d.sm_scale / d.softcap : d.sm_scale * kLog2e);
       fence_proxy_async_shared();
-      mbar_arrive(bar(kQFull));
+      mbar_arrive(bar(kQFull + wg));
     }
     // with the caps, f is never so small that -inf (a key that is not seen) times f
     // would be no number; scores that small are all 0 to fp32 anyway
@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         ref = next == -INFINITY ? 0.0f : next;
         sum *= keep;
         if (n > 0) {
-          ok = wait(kOFull + 2 * wg + (buf ^ 1), (n - 1) >> 1);          // P V of the step before is in
+          // P V of the step before is in: by the commit of S of the step after, if there is one
+          ok = g + 1 < m.end ? wait(kSFull + 2 * wg + (buf ^ 1), (n + 1) >> 1) : wait(kOFull + 2 * wg + (buf ^ 1), 0);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       mbar_arrive(bar(kPFull + 2 * wg + buf));
     }
     const bool none = m.first >= m.end;                  // of this split's keys; O was never written then
-    if (ok && !none) ok = wait(kOFull + 2 * wg + ((m.end - 1) & 1), (m.end - m.first - 1) >> 1);
+    if (ok && !none) ok = wait(kOFull + 2 * wg + ((m.end - 1) & 1), 0);
     if (ok) {
       tc_fence_after();
       uint32_t nans[D / 32];
