@@ -468,12 +468,15 @@ int moe_ffn_noalloc(const moe_ffn_desc *desc, void *stream);
  * new token i has position kv_len[b] - n + i.  n may be 0.
  *
  * Limits: dim 64 or 128; page_size 16, 32, 64 or 128; strides in bytes,
- * multiples of 16, not negative; q_heads a multiple of kv_heads; page, row and
- * head offsets are 64-bit.  Device-side faults of the descriptors set bits in
- * `err` and skip what they touch: a sequence that does not lie in the token
- * rows (cu_new decreasing, negative or past T), that is shorter than its new
- * tokens, or that has a page id outside [0, pages) -- MOE_DEV_BAD_INDEX; more
- * pages than max_pages -- MOE_DEV_OVERFLOW.
+ * multiples of 16, not negative, page strides below 2^35; q_heads a multiple of
+ * kv_heads; at most 2^24 rows and 2^30 / q_heads of them, 2^20 sequences, 1024 kv
+ * heads.  Offsets into the cache and the rows are 64-bit.  Device-side faults of
+ * the descriptors set bits in `err` (which may be NULL), and nothing out of range
+ * is read or written: a sequence that does not lie in the token rows (cu_new
+ * decreasing, negative or past T) or that is shorter than its new tokens --
+ * MOE_DEV_BAD_INDEX, and one with more pages than max_pages -- MOE_DEV_OVERFLOW,
+ * are skipped; a page id outside [0, pages) -- MOE_DEV_BAD_INDEX -- is skipped by
+ * an append, and leaves the sequence's attention output unspecified.
  */
 #define MOE_DTYPE_BF16 0              /* element types of q, k, v and out */
 #define MOE_DTYPE_F16 1
@@ -548,15 +551,16 @@ int moe_kv_append(const moe_kv_append_desc *desc, void *stream);
  *   visible: 0 <= j < kv_len[b]; j <= p unless MOE_KV_FULL; j > p - window if
  *            window > 0 (not together with MOE_KV_FULL)
  *   out = sum_j softmax_j(score) V[j, h, :],  lse = log sum_j exp(score_j)
- * over the visible j; a row that sees nothing gives out = 0 and lse = -inf.
- * Codes that are not visible to a row, whatever they hold (NaN too), do not
- * reach it; a visible NaN does.
+ * over the visible j (a row always sees its own token).  Codes that are not
+ * visible to a row, whatever they hold (NaN too), do not reach it; a visible NaN
+ * does, and a q row with an element that is not finite gives NaN.
  * Arithmetic: the products run on the tensor cores on f16 operands with fp32
  * sums.  E4M3 codes are exact in f16; a q row is first scaled by a power of two
  * that takes its largest element into [1, 2), so bf16 rows fit (elements below
  * 2^-14 of the largest lose bits below 2^-24 of it).  Scores, softmax statistics
  * and outputs are held in fp32; the softmax weights are rounded to f16 for the
- * second product, and out once to its type.  Scales must be positive, finite.
+ * second product, and out once to its type.  Scales must be positive and finite
+ * (below 2^-100 a V scale counts as that).  Results repeat bit for bit.
  * q, out: device rows as in moe_kv_append; lse: device fp32 [T, q_heads] or NULL.
  * max_q: no sequence has more new tokens than this (0 = T): a hint that picks
  * the kernels; a sequence with more is skipped with MOE_DEV_OVERFLOW.

@@ -492,6 +492,31 @@ def test_attention_flags_bad_descriptors(lib, what, bits, new):
     check_attention(lib, [90, 45], [new, new], 2, 4, 64, 16, cache=good, workspace=ws)
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_offsets_past_32_bits(lib, new):
+    # pages a gigabyte apart: the last one's bytes lie past 2^32
+    c = Cache([64], [new], 2, 64, 16, scale=1.0)
+    assert c.pages_of == [4]
+    far = [torch.zeros((5 << 30) + (1 << 20), dtype=torch.uint8, device="cuda").as_strided((6, 2, 16, 64), (1 << 30, 1024, 64, 1))
+           for _ in range(2)]
+    c.table[0, :4] = torch.tensor([1, 3, 4, 5], dtype=torch.int32)
+    c.k, c.v = far
+    c.ks, c.vs = (torch.ones((6, 2), device="cuda") for _ in range(2))
+    x = torch.randn((64, 2, 64), generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    whole = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    lib.moe_kv_append(x, x, c.k, c.v, c.ks, c.vs, c.table, whole, c.kv_len)
+    ref = to_codes(x.double().transpose(0, 1) / c.ks[c.table[0, :4].long()].double().repeat_interleave(16, 0).t()[:, :, None])
+    got = table_of_codes()[c.k[c.table[0, :4].long()].long()].transpose(0, 1).reshape(2, 64, 64)
+    assert torch.equal(got, ref)
+    check_attention(lib, [64], [new], 2, 4, 64, 16, cache=c)
+
+
+def test_append_many_new_tokens_in_a_batch_of_single_ones(lib):
+    # few new tokens on average: the kernel for single tokens meets whole pages
+    check_append(lib, [200] + [50 + i for i in range(60)], [131] + [1] * 60, 2, 4, 128, 64, 128, False, "bf16")
+    check_append(lib, [200] + [50 + i for i in range(60)], [131] + [2] * 60, 3, 0, 64, 16, 32, True, "f16")
+
+
 def test_append_then_attend_matches_plain_layer(lib):
     # a decode loop of a few steps: what was appended is what attention reads
     heads, q_heads, dim, page = 2, 6, 64, 16
