@@ -15,7 +15,8 @@
 // kv_append_tokens_kernel, for few new tokens a page: a CTA takes one page with all
 // its heads, K and V; 4 or 8 lanes share a row, and the maximum stays among them.
 //
-// Query rows need no maximum; further CTAs of the same launch rotate them.
+// Query rows need no maximum: further CTAs of the tokens kernel's launch rotate them,
+// and for prompts a kernel of its own, with the registers that suit it.
 #include "kv_common.cuh"
 
 namespace moe {
@@ -29,7 +30,7 @@ struct AppendArgs {
   int32_t units;        // page units: floor(T / page_size) + 2 * batch
   int32_t head_groups;  // CTAs per unit and kind
   int32_t heads_per;    // kv heads per CTA
-  int32_t kv_ctas;      // units * 2 * head_groups
+  int32_t kv_ctas;      // tokens kernel: CTAs before those of the queries
   int32_t q_groups;     // CTAs per run of query rows
 };
 
@@ -313,16 +314,12 @@ __global__ void __launch_bounds__(128) kv_append_tokens_kernel(const __grid_cons
 }
 
 template <bool F16, int D, int TT, int R>
-__global__ void __launch_bounds__(TT) kv_append_pages_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(TT, R == 1 ? 1024 / TT : R == 2 ? 3 : 2) kv_append_pages_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ uint32_t red[2][TT / 32];
   const moe_kv_append_desc& d = a.d;
   const moe_kv_cache& kc = d.cache;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (static_cast<int>(blockIdx.x) >= a.kv_ctas) {
-    rotate_queries<F16, D, TT>(a, blockIdx.x - a.kv_ctas);
-    return;
-  }
   constexpr int kGroups = D / 16;
   const int P = kc.page_size;
   const int hg = blockIdx.x % a.head_groups;
@@ -399,6 +396,13 @@ __global__ void __launch_bounds__(TT) kv_append_pages_kernel(const __grid_consta
   }
 }
 
+template <bool F16, int D>
+__global__ void __launch_bounds__(256, 3) kv_rotate_queries_kernel(const __grid_constant__ AppendArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  rotate_queries<F16, D, 256>(a, blockIdx.x);
+}
+
 // How many CTAs the queries take, TT threads each.
 template <int D, int TT>
 int64_t query_ctas(AppendArgs& a) {
@@ -414,10 +418,11 @@ int launch_pages(AppendArgs& a, cudaStream_t st) {
   const int64_t per = one / (16ll * num_sms());
   a.heads_per = static_cast<int32_t>(per < 1 ? 1 : per > a.d.cache.kv_heads ? a.d.cache.kv_heads : per);
   a.head_groups = (a.d.cache.kv_heads + a.heads_per - 1) / a.heads_per;
-  const int64_t kv = 2ll * a.units * a.head_groups, qc = query_ctas<D, TT>(a);
-  if (kv + qc > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  a.kv_ctas = static_cast<int32_t>(kv);
-  return launch_pdl(kv_append_pages_kernel<F16, D, TT, R>, dim3(static_cast<unsigned>(kv + qc)), dim3(TT), 0, st, a);
+  const int64_t kv = 2ll * a.units * a.head_groups, qc = query_ctas<D, 256>(a);
+  if (kv > INT32_MAX || qc > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (int rc = launch_pdl(kv_append_pages_kernel<F16, D, TT, R>, dim3(static_cast<unsigned>(kv)), dim3(TT), 0, st, a)) return rc;
+  if (qc == 0) return MOE_OK;
+  return launch_pdl(kv_rotate_queries_kernel<F16, D>, dim3(static_cast<unsigned>(qc)), dim3(256), 0, st, a);
 }
 
 template <bool F16, int D>
