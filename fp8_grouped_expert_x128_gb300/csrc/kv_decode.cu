@@ -626,16 +626,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
                  *reinterpret_cast<const float4*>(buf + r * C::kLd + e));
         }
       };
+      // The barrier orders the CTA's stores before thread 0's release, and its acquire
+      // before their loads.
       const auto arrive_last = [&](int32_t* counter, int count) {
-        __threadfence();
         __syncthreads();
         if (tid == 0) {
-          const int before = atomicAdd(counter, 1);
+          int before;
+          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
           s_last = before == count - 1;
           if (s_last) *counter = 0;                          // as the next call wants it
         }
         __syncthreads();
-        __threadfence();
         return s_last != 0;
       };
       // parts of CTAs first, first + stride, ... into buf, top and sum
