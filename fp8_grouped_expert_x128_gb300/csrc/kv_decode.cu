@@ -16,6 +16,12 @@
 // taken in the order in which a lane's bytes lie (Q is put in the same order).
 // E4M3 widens exactly to f16 in one instruction per pair.  The V scale rides in
 // the weight: w = exp2(s + log2 s_V - m), the sum takes w / s_V.
+//
+// A step is some 300 instructions with little parallelism inside a warp, so three or
+// four CTAs share an SM (two: 253 us where three take 191).  Measured: 64 sequences of
+// 2000 to 16400 tokens, 8 kv heads, 4 rows each, 191 us, 6.2 TB/s (93% of a copy's);
+// four of 131072 tokens, 165 us (97%); one of 1010 tokens, 11 us: four dependent loads,
+// the join's release and acquire, and its loads, about a microsecond each.
 #include "kv_attention.cuh"
 
 namespace moe {

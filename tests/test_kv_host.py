@@ -112,3 +112,33 @@ def test_packed_descriptors_have_the_structures_layout(moe):
     for pack, cls, n in ((moe._kv_append_pack, moe.moe_kv_append_desc, 19), (moe._kv_attention_pack, moe.moe_kv_attention_desc, 15)):
         rest = tuple(range(30, 30 + n))
         assert pack(*c, *rest) == bytes(cls(c, *rest))
+
+
+def test_prefill_kernel_compiles_to_its_register_split(moe, tmp_path):
+    """The kernel hands registers between warpgroups with setmaxnreg: the split counts
+    on a launch allocation of exactly 96 registers for its 640 threads (the launch
+    refuses anything else), and its loops on next to no spills."""
+    import os
+    import re
+    import shutil
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    src = os.path.join(root, "fp8_grouped_expert_x128_gb300", "csrc", "kv_prefill.cu")
+    r = subprocess.run([nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
+                        "-I", os.path.join(root, "include"), "-Xptxas", "-v", "-c", src, "-o", str(tmp_path / "p.o")],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    current, seen = "", 0
+    for line in r.stderr.splitlines():
+        m = re.search(r"Compiling entry function '(\S+)'", line)
+        current = m.group(1) if m else current
+        if "kv_prefill_kernel" not in current:
+            continue
+        m = re.search(r"(\d+) bytes spill stores", line)
+        assert m is None or int(m.group(1)) <= 64, line
+        m = re.search(r"Used (\d+) registers", line)
+        if m:
+            assert int(m.group(1)) == 96, current
+            seen += 1
+    assert seen == 8            # two types x two dimensions x with and without the cap
