@@ -457,6 +457,17 @@ def _kv_rows(t, name, T, heads, dim, dtype, device):
     return st, sh
 
 
+def _kv_rows2(a, a_name, b, b_name, T, heads, dim, dtype, device):
+    """_kv_rows of two tensors of one shape: (token, head) strides of each."""
+    shape = (T, heads, dim)
+    at, ah, ad = a.stride()
+    bt, bh, bd = b.stride()
+    if not (a.shape == shape == b.shape and a.dtype is dtype is b.dtype and ad == 1 == bd
+            and a.get_device() == device == b.get_device()):
+        return (*_kv_rows(a, a_name, T, heads, dim, dtype, device), *_kv_rows(b, b_name, T, heads, dim, dtype, device))
+    return at, ah, bt, bh
+
+
 def _kv_cache_refused(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype):
     pages, heads, page, dim = k_cache.shape
     device = k_cache.get_device()
@@ -528,15 +539,13 @@ def moe_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, 
     dtype = k.dtype
     c = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype)
     device, heads, dim, T = k_cache.get_device(), c[18], c[19], k.shape[0]
-    kt, kh = _kv_rows(k, "k", T, heads, dim, dtype, device)
-    vt, vh = _kv_rows(v, "v", T, heads, dim, dtype, device)
+    kt, kh, vt, vh = _kv_rows2(k, "k", v, "v", T, heads, dim, dtype, device)
     qt = qh = ot = oh = q_heads = max_pos = rot = q_ptr = o_ptr = cs_ptr = 0
     if q is not None:
         if q_out is None:
             raise ValueError("q_out: queries need a tensor to be written to")
         q_heads = q.shape[1]
-        qt, qh = _kv_rows(q, "q", T, q_heads, dim, dtype, device)
-        ot, oh = _kv_rows(q_out, "q_out", T, q_heads, dim, dtype, device)
+        qt, qh, ot, oh = _kv_rows2(q, "q", q_out, "q_out", T, q_heads, dim, dtype, device)
         q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -559,8 +568,7 @@ def _kv_attention_fields(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_n
     c = _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype)
     device, dim = k_cache.get_device(), c[19]
     T, heads, _ = q.shape
-    qt, qh = _kv_rows(q, "q", T, heads, dim, dtype, device)
-    ot, oh = _kv_rows(out, "out", T, heads, dim, dtype, device)
+    qt, qh, ot, oh = _kv_rows2(q, "q", out, "out", T, heads, dim, dtype, device)
     lse_ptr = 0
     if lse is not None:
         if lse.shape != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != device:

@@ -15,19 +15,21 @@
 // kv_append_tokens_kernel, for few new tokens a page: a CTA takes one page with all
 // its heads, K and V; 4 or 8 lanes share a row, and the maximum stays among them.
 //
-// Measured: 256 single tokens with 32 query and 8 kv heads 6.2 us on the GPU; 32768
-// prompt tokens with 64 and 8 heads 225 us, 5.7 TB/s (85% of a copy's rate); ragged
-// chunks of 64-dimension heads, f16, token-major pages 49 us, 3.4 TB/s, bound by the
-// latency of a page's chain (4 KB a head and CTA).
+// Measured: 256 single tokens with 32 query and 8 kv heads 5.4 us on the GPU; 32768
+// prompt tokens with 64 and 8 heads 210 us, 6.1 TB/s (91% of a copy's rate), of which
+// the queries 154 at the copy's rate and the pages 56; ragged chunks of 64-dimension
+// heads, f16, token-major pages 44 us, 3.7 TB/s (4 KB a head and CTA, a barrier each).
 //
 // Query rows need no maximum: further CTAs of the tokens kernel's launch rotate them,
 // and for prompts a kernel of its own, with the registers that suit it.
+#include <float.h>
+
 #include "kv_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kQHeadsPerCta = 8;   // query heads one thread rotates with the same angles
+constexpr int kQHeadsPerCta = 4;   // query heads one thread rotates with the same angles
 constexpr int kFewTokens = 4;      // new tokens a sequence, on average, up to which the tokens kernel serves
 
 struct AppendArgs {
@@ -84,15 +86,32 @@ __device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (
 // |x| where x is finite, else 0: what counts toward a page's maximum.
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.0f;
+  return a <= FLT_MAX ? a : 0.0f;
+}
+// max(amax, |x|, |y|): NaN takes no part, infinity does; with an infinite maximum the
+// caller takes it again over the finite values.
+__device__ __forceinline__ float abs_max(const float (&x)[8], const float (&y)[8], float amax) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(fmaxf(amax, fabsf(x[i])), fabsf(y[i]));
+  return amax;
+}
+__device__ __forceinline__ float finite_max(const float (&x)[8], const float (&y)[8], float amax) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(fmaxf(amax, finite_abs(x[i])), finite_abs(y[i]));
+  return amax;
 }
 
 // e4m3(x / s): a product with the exact reciprocal where s is a power of two.
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, bool pow2) {
   float q[8];
-  const float r = pow2 ? __frcp_rn(s) : 0.0f;
+  if (pow2) {
+    const float r = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = pow2 ? x[i] * r : __fdiv_rn(x[i], s);
+    for (int i = 0; i < 8; ++i) q[i] = x[i] * r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], s);
+  }
   return pack_e4m3x8(q);
 }
 
@@ -232,11 +251,6 @@ __device__ __forceinline__ void rotated16(const uint4& u, const uint4& v, const 
     turn(x, y, c, s, inter);
   }
 }
-__device__ __forceinline__ float finite_max(const float (&x)[8], const float (&y)[8], float amax) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_abs(x[i]), finite_abs(y[i])));
-  return amax;
-}
 
 // A page's scale from the maximum of its new tokens; whether old codes have to follow.
 __device__ __forceinline__ float page_scale(float amax, bool joins, float before, bool& grown, bool& pow2) {
@@ -287,18 +301,22 @@ __global__ void __launch_bounds__(128) kv_append_tokens_kernel(const __grid_cons
           v[k] = __ldg(reinterpret_cast<const uint4*>(p + rb));
         }
     };
-    for (int slot = w.s0; slot < w.s1; slot += kAtOnce) {
-      load(slot);
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k)
-        if (slot + k < w.s1) {
-          rotated16<F16>(u[k], v[k], d.cos_sin, w.pi * P + slot + k, g, rot, inter, x, y);
-          amax = finite_max(x, y, amax);
-        }
-    }
     const uint32_t lanes = kGroups == 8 ? 0xFFu << (threadIdx.x & 24) : 0xFu << (threadIdx.x & 28);
+    for (int finite = 0; finite < 2; ++finite) {
+      amax = 0.0f;
+      for (int slot = w.s0; slot < w.s1; slot += kAtOnce) {
+        load(slot);
 #pragma unroll
-    for (int o = 1; o < kGroups; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
+        for (int k = 0; k < kAtOnce; ++k)
+          if (slot + k < w.s1) {
+            rotated16<F16>(u[k], v[k], d.cos_sin, w.pi * P + slot + k, g, rot, inter, x, y);
+            amax = finite ? finite_max(x, y, amax) : abs_max(x, y, amax);
+          }
+      }
+#pragma unroll
+      for (int o = 1; o < kGroups; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
+      if (amax <= FLT_MAX) break;          // nearly always
+    }
     bool grown, pow2;
     const float s = page_scale(amax, w.s0 > 0, before, grown, pow2);
     for (int slot = w.s0; slot < w.s1; slot += kAtOnce) {
@@ -318,9 +336,13 @@ __global__ void __launch_bounds__(128) kv_append_tokens_kernel(const __grid_cons
   }
 }
 
+// CTAs of the pages kernel that share an SM (its registers are limited to that).
+template <int TT, int R>
+constexpr int kPagesPerSm = R == 1 ? 1024 / TT : 1;
+
 template <bool F16, int D, int TT, int R>
-__global__ void __launch_bounds__(TT, R == 1 ? 1024 / TT : R == 2 ? 3 : 2) kv_append_pages_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ uint32_t red[2][TT / 32];
+__global__ void __launch_bounds__(TT, kPagesPerSm<TT, R>) kv_append_pages_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ uint32_t red[3][TT / 32];
   const moe_kv_append_desc& d = a.d;
   const moe_kv_cache& kc = d.cache;
   grid_dependency_wait();
@@ -367,20 +389,30 @@ __global__ void __launch_bounds__(TT, R == 1 ? 1024 / TT : R == 2 ? 3 : 2) kv_ap
       const int slot = item / kGroups, g = item % kGroups;
       const bool in = slot >= w.s0 && slot < w.s1;
       rotated16<F16>(u[r], v[r], d.cos_sin, w.pi * P + (in ? slot : w.s0), g, rot, inter, x[r], y[r]);
-      amax = finite_max(x[r], y[r], amax);             // rows that are none are zeros
+      amax = abs_max(x[r], y[r], amax);                // rows that are none are zeros
     }
     const float before = scale[h];
     if (h + 1 < h1) load(h + 1);
-    // floats that are not negative order as their bit patterns do
-    const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-    uint32_t* slot_red = red[h & 1];
-    if ((threadIdx.x & 31) == 0) slot_red[threadIdx.x >> 5] = wmax;
-    __syncthreads();
-    uint32_t all = 0;
+    // over the CTA: floats that are not negative order as their bit patterns do
+    const auto all_max = [&](float m, uint32_t* slots) {
+      const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+      if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = wmax;
+      __syncthreads();
+      uint32_t all = 0;
 #pragma unroll
-    for (int k = 0; k < TT / 32; ++k) all = max(all, slot_red[k]);
+      for (int k = 0; k < TT / 32; ++k) all = max(all, slots[k]);
+      return __uint_as_float(all);
+    };
+    amax = all_max(amax, red[h & 1]);
+    if (amax > FLT_MAX) {                  // an infinity among them
+      amax = 0.0f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) amax = finite_max(x[r], y[r], amax);
+      amax = all_max(amax, red[2]);
+      __syncthreads();                     // red[2] may be used again
+    }
     bool grown, pow2;
-    const float s = page_scale(__uint_as_float(all), w.s0 > 0, before, grown, pow2);
+    const float s = page_scale(amax, w.s0 > 0, before, grown, pow2);
     uint8_t* out = dst + h * dst_hld;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -418,11 +450,12 @@ int64_t query_ctas(AppendArgs& a) {
 
 template <bool F16, int D, int TT, int R>
 int launch_pages(AppendArgs& a, cudaStream_t st) {
-  // several heads a CTA, as long as some sixteen CTAs an SM are left
-  const int64_t one = 2ll * a.units * a.d.cache.kv_heads;
-  const int64_t per = one / (16ll * num_sms());
-  a.heads_per = static_cast<int32_t>(per < 1 ? 1 : per > a.d.cache.kv_heads ? a.d.cache.kv_heads : per);
-  a.head_groups = (a.d.cache.kv_heads + a.heads_per - 1) / a.heads_per;
+  // several heads a CTA, so that a page's chain of loads is paid once for them, as long
+  // as there is a CTA for every place on the GPU (32768 prompt
+  // tokens' keys and values: 56 us)
+  const int64_t heads = a.d.cache.kv_heads, per = 2 * a.units * heads / (kPagesPerSm<TT, R> * num_sms());
+  a.head_groups = static_cast<int32_t>(per <= 1 ? heads : (heads + per - 1) / per);
+  a.heads_per = static_cast<int32_t>((heads + a.head_groups - 1) / a.head_groups);
   const int64_t kv = 2ll * a.units * a.head_groups, qc = query_ctas<D, 256>(a);
   if (kv > INT32_MAX || qc > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (int rc = launch_pdl(kv_append_pages_kernel<F16, D, TT, R>, dim3(static_cast<unsigned>(kv)), dim3(TT), 0, st, a)) return rc;
@@ -439,7 +472,7 @@ int launch_tokens(AppendArgs& a, cudaStream_t st) {
 }
 
 // One thread holds 16 values of a row, so a page takes page_size * dim / 16
-// threads; above 256 a thread holds 2 or 4 rows.
+// threads, or half as many with two rows each above 512.
 template <bool F16>
 int pick_append(AppendArgs& a, cudaStream_t st) {
   const int P = a.d.cache.page_size;
@@ -450,12 +483,12 @@ int pick_append(AppendArgs& a, cudaStream_t st) {
     if (P == 16) return launch_pages<F16, 64, 64, 1>(a, st);
     if (P == 32) return launch_pages<F16, 64, 128, 1>(a, st);
     if (P == 64) return launch_pages<F16, 64, 256, 1>(a, st);
-    return launch_pages<F16, 64, 256, 2>(a, st);
+    return launch_pages<F16, 64, 512, 1>(a, st);
   }
   if (P == 16) return launch_pages<F16, 128, 128, 1>(a, st);
   if (P == 32) return launch_pages<F16, 128, 256, 1>(a, st);
-  if (P == 64) return launch_pages<F16, 128, 256, 2>(a, st);
-  return launch_pages<F16, 128, 256, 4>(a, st);
+  if (P == 64) return launch_pages<F16, 128, 512, 1>(a, st);
+  return launch_pages<F16, 128, 512, 2>(a, st);
 }
 
 }  // namespace

@@ -203,10 +203,11 @@ def test_append_in_place_queries(lib):
     assert (x.double() - ref.double()).abs().max() <= 2.0 ** -7 * ref.abs().max().double()
 
 
-def test_append_non_finite_values(lib):
+@pytest.mark.parametrize("n", [3, 16])
+def test_append_non_finite_values(lib, n):
     # infinities saturate and take no part in the page's maximum, NaN is kept
-    c = Cache([3], [3], 1, 64, 16)
-    v = torch.ones((3, 1, 64), device="cuda").bfloat16()
+    c = Cache([n], [n], 1, 64, 16)
+    v = torch.ones((n, 1, 64), device="cuda").bfloat16()
     v[1, 0, 3], v[1, 0, 4], v[2, 0, 5] = math.inf, -math.inf, math.nan
     lib.moe_kv_append(v, v, *c.args())
     p = int(c.table[0, 0])
