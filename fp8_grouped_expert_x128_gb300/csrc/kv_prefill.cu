@@ -55,9 +55,11 @@ struct Cfg {
   static constexpr uint32_t kTmemO = 256;              // S0, S1 (and P over them) at 0, 128; O0, O1 here
 };
 
-// mbarriers, in order.  S, P and O have one for each buffer of a tile: two steps can be
-// under way, and a barrier must not get two phases ahead of who waits for it.
-enum { kQFull, kEmpty = kQFull + 2, kKFull, kVFull = kKFull + 2, kSFull = kVFull + 2, kPFull = kSFull + 4,
+// mbarriers, in order.  S, P and O have one for each buffer of a tile, and each tile's
+// issuing warp two for the blocks that it releases: two steps can be under way, and a
+// barrier must neither count one warp's next arrival for another's missing one nor get
+// two phases ahead of who waits for it.
+enum { kQFull, kEmpty = kQFull + 2, kKFull = kEmpty + 4, kVFull = kKFull + 2, kSFull = kVFull + 2, kPFull = kSFull + 4,
        kOFull = kPFull + 4, kBarCount = kOFull + 4 };
 
 // Instruction descriptor, kind::f16: D fp32, A and B f16, A K-major; B K-major or
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
       const bool widen = i >= kKFull && i < kVFull + 2, rows128 = i < kQFull + 2 || (i >= kPFull && i < kPFull + 4);
-      mbar_init(bar(i), widen ? kWidenThreads : rows128 ? 128 : i == kEmpty ? tiles : 1);
+      mbar_init(bar(i), widen ? kWidenThreads : rows128 ? 128 : 1);
     }
     s_abort = 0;
     s_nan = 0;
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
             any = true;
           }
         }
-        if (ok) commit(bar(kEmpty), lead);
+        if (ok) commit(bar(kEmpty + 2 * i + (kb & 1)), lead);
       }
       if (!ok && any && lead) {
         // the MMAs in flight end before TMEM is freed: the commit below follows them
@@ -434,9 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       }
 #pragma unroll
       for (int is_v = 0; is_v < 2; ++is_v) {
-        // kEmpty's phase e: K up to block e and V up to block e - 1 are read.  V of block
+        // A tile's e-th release: K up to block e and V up to block e - 1 are read.  V of block
         // n takes the place of n - 2's; K of block n + 1, which comes next, that of n - 1's.
-        if (is_v && n > 0) ok = wait(kEmpty, n - 1);
+        if (is_v && n > 0) {
+          ok = wait(kEmpty + ((n - 1) & 1), (n - 1) >> 1);
+          if (ok && tiles == 2) ok = wait(kEmpty + 2 + ((n - 1) & 1), (n - 1) >> 1);
+        }
         if (!ok) break;
         if (!is_v && t < 8) {
           // the V scale as its logarithm and inverse, which is what the weights take

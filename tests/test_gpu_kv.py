@@ -373,6 +373,38 @@ def test_attention_long_sequence_splits(lib):
     check_attention(lib, [9000, 5000], [20, 12], 1, 8, 128, 128, "f16")
 
 
+@pytest.mark.parametrize("dim,window,softcap", [(128, 600, 50.0), (128, 600, 0.0), (64, 600, 0.0), (128, 0, 0.0), (64, 130, 20.0)])
+def test_attention_prompts_fill_the_gpu(lib, dim, window, softcap):
+    # more CTAs than SMs, the two tiles of each with different keys: a tile's work does
+    # not disturb the other's, whichever is ahead; again and again the same bits
+    new = [1380, 777, 300]
+    c = Cache([n + 300 for n in new], new, 4, dim, 64)
+    q = (torch.randn((sum(new), 32, dim), generator=torch.Generator().manual_seed(3)) * 2).bfloat16().cuda()
+    out = torch.empty_like(q)
+    sm_scale = dim ** -0.5
+    ws = lib.alloc_kv_workspace(lib.make_kv_attention_desc(q, *c.args(), out, sm_scale, max(new)))
+    first = None
+    for _ in range(10):
+        out.fill_(math.nan)
+        lib.moe_kv_attention(q, *c.args(), out, ws, sm_scale, max_q=max(new), window=window, softcap=softcap)
+        first = out.clone() if first is None else first
+        assert torch.equal(out, first)
+    # against the plain form in 32 bits, row block by row block (the 64-bit one above is for small cases)
+    for b, n in enumerate(new):
+        t0, t = int(c.cu[b]), c.total[b]
+        j, pos = torch.arange(t, device="cuda"), torch.arange(t - n, t, device="cuda")[:, None]
+        seen = (j <= pos) & ((j > pos - window) if window else (j >= 0))
+        for h in range(4):
+            k, v = (c.values(b, w, t)[h].float() for w in ("k", "v"))
+            s = torch.einsum("igd,jd->gij", q[t0:t0 + n, 8 * h:8 * h + 8].float(), k) * sm_scale
+            if softcap:
+                s = softcap * torch.tanh(s / softcap)
+            p = torch.softmax(s.masked_fill(~seen, -math.inf), -1)
+            ref, mag = torch.einsum("gij,jd->igd", p, v), torch.einsum("gij,jd->igd", p, v.abs())
+            err = (first[t0:t0 + n, 8 * h:8 * h + 8].float() - ref).abs()
+            assert (err <= (2.0 ** -11 + 2.0 ** -14) * (mag + ref.abs()) + 2.0 ** -8 * ref.abs() + 1e-5).all()
+
+
 @pytest.mark.parametrize("dim,dtype,window,softcap,full", [
     (128, "bf16", 0, 0.0, False), (64, "f16", 3000, 0.0, False), (128, "f16", 0, 20.0, False), (64, "bf16", 0, 0.0, True),
     (128, "bf16", 700, 0.0, False)])
