@@ -300,7 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const auto wait = [&](int i, int phase) { return wait_for(bar(i), phase & 1, &s_abort, d.err); };
+  // A warp of the issuing role goes on or gives up as one.  The other roles go on with
+  // their loops when a lane has given up (every later wait ends at once then), so that no
+  // lane leaves its warp, and look at s_abort in the end.
+  const auto wait_lane = [&](int i, int phase) { return wait_for(bar(i), phase & 1, &s_abort, d.err); };
+  const auto wait = [&](int i, int phase) { return static_cast<bool>(__all_sync(0xffffffffu, wait_lane(i, phase))); };
 
   if (wg == 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -315,17 +319,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       // both warps, whether its tile reads it or not.
       const uint32_t id_s = idesc_f16(kKeys, false), id_o = idesc_f16(D, true);
       const uint32_t lead = elect_one();
-      const auto all_wait = [&](int which, int phase) { return __all_sync(0xffffffffu, wait(which, phase)); };
       const Steps m = i ? mine1 : mine0;
       const uint32_t to = tmem + C::kTmemO + i * D, ts = tmem + i * 128;
       const uint32_t qd = desc_lo(sbase + C::kQ + i * C::kTileBytes, 16);
-      bool ok = all_wait(kQFull + i, 0), any = false;
+      bool ok = wait(kQFull + i, 0), any = false;
 #pragma unroll 1
       for (int g2 = (all.first & ~1) - 2; ok && g2 < all.end; g2 += 2) {
         const int vb = (g2 >> 1) - block0, kb = vb + 1;               // blocks that are read (V of -1: none)
         const bool more = kb < block1 - block0;
-        if (vb >= 0) ok = all_wait(kVFull + (vb & 1), vb >> 1);
-        if (ok && more) ok = all_wait(kKFull + (kb & 1), kb >> 1);
+        if (vb >= 0) ok = wait(kVFull + (vb & 1), vb >> 1);
+        if (ok && more) ok = wait(kKFull + (kb & 1), kb >> 1);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           const uint32_t half = buf * kKeys;
           const bool next = g + 2 >= m.first && g + 2 < m.end;
           if (g >= m.first && g < m.end) {
-            ok = all_wait(kPFull + 2 * i + buf, (g - m.first) >> 1);
+            ok = wait(kPFull + 2 * i + buf, (g - m.first) >> 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t vd = desc_lo(sbase + C::kV + (vb & 1) * C::kTileBytes + half * 128, 16384);
@@ -420,9 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     for (int i = 0; i < kIter; ++i) load(reg[0][i], i, block0, base[0], page_ld16[0], kc.k_slot_ld);
 #pragma unroll
     for (int i = 0; i < kIter; ++i) load(reg[1][i], i, block0, base[1], page_ld16[1], kc.v_slot_ld);
-    bool ok = true;
 #pragma unroll 1
-    for (int j = block0; ok && j < block1; ++j) {
+    for (int j = block0; j < block1; ++j) {
       const int n = j - block0, st = n & 1;
       const bool more = j + 1 < block1;
       float2 now = scales;
@@ -439,10 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         // A tile's e-th release: K up to block e and V up to block e - 1 are read.  V of block
         // n takes the place of n - 2's; K of block n + 1, which comes next, that of n - 1's.
         if (is_v && n > 0) {
-          ok = wait(kEmpty + ((n - 1) & 1), (n - 1) >> 1);
-          if (ok && tiles == 2) ok = wait(kEmpty + 2 + ((n - 1) & 1), (n - 1) >> 1);
+          wait_lane(kEmpty + ((n - 1) & 1), (n - 1) >> 1);
+          if (tiles == 2) wait_lane(kEmpty + 2 + ((n - 1) & 1), (n - 1) >> 1);
         }
-        if (!ok) break;
         if (!is_v && t < 8) {
           // the V scale as its logarithm and inverse, which is what the weights take
           const float k = fmaxf(now.x, kMinKScale), v = fmaxf(now.y, kMinScale);
@@ -558,12 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     const int lo_last = first_key(d, s, tile_r1 / a.G), hi_first = end_key(d, s, (row0 + wg * kTileRows) / a.G);
     const Steps m = wg ? mine1 : mine0;
     float top = -INFINITY, ref = 0.0f, sum = 0.0f;       // running reference (ref: the same, 0 while -inf) and sum
-    bool ok = true;
 #pragma unroll 1
     for (int g = m.first; g < m.end; ++g) {
       const int n = g - m.first, buf = g & 1;
-      ok = wait(kSFull + 2 * wg + buf, n >> 1);
-      if (!ok) break;
+      wait_lane(kSFull + 2 * wg + buf, n >> 1);
       tc_fence_after();
       uint32_t x[2][32];
       const uint32_t at = ts + buf * kKeys;
@@ -601,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         sum *= keep;
         if (n > 0) {
           // P V of the step before is in: by the commit of S of the step after, if there is one
-          ok = g + 1 < m.end ? wait(kSFull + 2 * wg + (buf ^ 1), (n + 1) >> 1) : wait(kOFull + 2 * wg + (buf ^ 1), 0);
-          if (!ok) break;
+          const bool last = g + 1 == m.end;
+          wait_lane((last ? kOFull : kSFull) + 2 * wg + (buf ^ 1), last ? 0 : (n + 1) >> 1);
           tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < D / 16; ++k) {
@@ -646,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       mbar_arrive(bar(kPFull + 2 * wg + buf));
     }
     const bool none = m.first >= m.end;                  // of this split's keys; O was never written then
-    if (ok && !none) ok = wait(kOFull + 2 * wg + ((m.end - 1) & 1), 0);
-    if (ok) {
+    if (!none) wait_lane(kOFull + 2 * wg + ((m.end - 1) & 1), 0);
+    if (__all_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort) == 0)) {
       tc_fence_after();
       uint32_t nans[D / 32];
 #pragma unroll
