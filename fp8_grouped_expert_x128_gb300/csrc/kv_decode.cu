@@ -19,8 +19,8 @@
 //
 // A step is some 300 instructions with little parallelism inside a warp, so three or
 // four CTAs share an SM (two: 253 us where three take 191).  Measured: 64 sequences of
-// 2000 to 16400 tokens, 8 kv heads, 4 rows each, 191 us, 6.2 TB/s (93% of a copy's);
-// four of 131072 tokens, 165 us (97%); one of 1010 tokens, 11 us: four dependent loads,
+// 2000 to 16400 tokens, 8 kv heads, 4 rows each, 191 us, 6.2 TB/s (92% of a copy's);
+// four of 131072 tokens, 167 us (95%); one of 1010 tokens, 11 us: four dependent loads,
 // the join's release and acquire, and its loads, about a microsecond each.
 #include "kv_attention.cuh"
 

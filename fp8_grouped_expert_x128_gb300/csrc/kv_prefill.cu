@@ -15,9 +15,10 @@
 // kernel.  Where there are fewer 256-row units than SMs, the keys are split as well,
 // and kv_prefill_join_kernel adds the parts.
 //
-// Measured: an 8192-token prompt with 64 / 8 heads of 128 in 0.96 ms, 1.14 PFLOP/s,
-// 58% of the bf16 rate that a large matrix product has.  No single role binds: with
-// one taken out (widening, softmax, MMAs) it is 10 to 20% less, with all three 320 us.
+// Measured: an 8192-token prompt with 64 / 8 heads of 128 in 0.97 ms, 1.13 PFLOP/s,
+// 57% of the bf16 rate that a large matrix product has; 1.50 ms under a cap.  No single
+// role binds: with one taken out (widening, softmax, MMAs) it is 10 to 20% less, with all
+// three 320 us; 60% of the issue slots, 22% of the exponentials' rate.
 // 128-key steps with one S buffer take the same (their MMAs are quicker, N = 64 takes
 // as long as N = 128, but a softmax waits for its S), and so do four warpgroups of
 // softmax; one that takes weights before the maximum of the block is known, 20% more.
@@ -143,10 +144,10 @@ __device__ __forceinline__ float keep_hidden(float x, float y) {
   asm("{\n\t.reg .pred p;\n\tsetp.eq.f32 p, %1, 0fFF800000;\n\tselp.f32 %0, %1, %2, p;\n\t}" : "=f"(r) : "f"(x), "f"(y));
   return r;
 }
-// capped_log2(x f, cap) + add of four scores of S.  The four reciprocals
-// of 1 + exp(2y) are one reciprocal of their product, which stays below 2^121: from
-// exp(2y) = 2^30 on, tanh is 1 to fp32.  f and cap_log2 are those of capped_log2, f times
-// 2 log2(e).  (A reciprocal for each score: 90 us for the windowed prompts instead of 84, 1704 for an
+// capped_log2(x f, cap) + add of four scores of S.  The four reciprocals of 1 + exp(2y)
+// are one reciprocal of their product, which stays below 2^121: from exp(2y) = 2^30 on,
+// tanh is 1 to fp32.  f and cap_log2 are those of capped_log2, f times 2 log2(e).  (A
+// reciprocal for each score: 90 us for the windowed prompts instead of 84, 1704 for an
 // 8192-token prompt under a cap instead of 1503.)
 __device__ __forceinline__ void capped4(const uint32_t* x, float f, float cap_log2, float add, float* y) {
   float a[4];
