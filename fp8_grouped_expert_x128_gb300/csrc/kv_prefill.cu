@@ -15,8 +15,8 @@
 // kernel.  Where there are fewer 256-row units than SMs, the keys are split as well,
 // and kv_prefill_join_kernel adds the parts.
 //
-// Measured: an 8192-token prompt with 64 / 8 heads of 128 in 0.97 ms, 1.13 PFLOP/s,
-// 57% of the bf16 rate that a large matrix product has; 1.50 ms under a cap.  No single
+// Measured: an 8192-token prompt with 64 / 8 heads of 128 in 0.96 ms, 1.15 PFLOP/s,
+// 58% of the bf16 rate that a large matrix product has; 1.50 ms under a cap.  No single
 // role binds: with one taken out (widening, softmax, MMAs) it is 10 to 20% less, with all
 // three 320 us; 60% of the issue slots, 22% of the exponentials' rate.
 // 128-key steps with one S buffer take the same (their MMAs are quicker, N = 64 takes
@@ -180,6 +180,11 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p, bool on) {
 __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ float4 lds16f(uint32_t a) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
@@ -284,24 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   const moe_kv_cache& kc = d.cache;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
   const int H = kc.kv_heads, P = kc.page_size, page_shift = 31 - __clz(P);
-  grid_dependency_wait();
-  grid_launch_dependents();
-
-  const int split = blockIdx.x % splits, h = blockIdx.x / splits % H;
-  const Unit w = unit_of(a, blockIdx.x / splits / H, splits);
-  if (split >= w.splits) return;           // the unit has no rows, or needs fewer splits
-  const int b = w.b, rows = w.rows, row0 = w.row0, row_end = w.row_end;
-  const Seq s = w.s;
-  const int tiles = row_end - row0 > kTileRows ? 2 : 1;
-  // this CTA's steps, of all rows and of each tile's (a tile may have none in a split)
-  const Steps all = {w.all.first + split * w.chunk, min(w.all.end, w.all.first + (split + 1) * w.chunk)};
-  const auto mine = [&](int r0, int r1) {
-    const Steps m = steps_of(a, s, r0, r1);
-    return Steps{max(m.first, all.first), min(m.end, all.end)};
-  };
-  const Steps mine0 = mine(row0, min(row0 + kTileRows, row_end));
-  const Steps mine1 = tiles == 2 ? mine(row0 + kTileRows, row_end) : Steps{all.end, all.end};
-  const int block0 = all.first >> 1, block1 = (all.end + 1) >> 1;   // blocks to widen
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -316,6 +303,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     s_nan = 0;
     fence_barrier_init();
   }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int split = blockIdx.x % splits, h = blockIdx.x / splits % H;
+  const Unit w = unit_of(a, blockIdx.x / splits / H, splits);
+  if (split >= w.splits) return;           // the unit has no rows, or needs fewer splits
+  // (not before the wait above: a CTA of the kernel before this one may still want TMEM)
   if (warp == kIssueWarp) {
     tmem_alloc(smem_u32(&s_tmem), kTmemCols);
     tmem_relinquish();
@@ -324,6 +317,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  const int b = w.b, rows = w.rows, row0 = w.row0, row_end = w.row_end;
+  const Seq s = w.s;
+  const int tiles = row_end - row0 > kTileRows ? 2 : 1;
+  // this CTA's steps, of all rows and of each tile's (a tile may have none in a split)
+  const Steps all = {w.all.first + split * w.chunk, min(w.all.end, w.all.first + (split + 1) * w.chunk)};
+  const auto mine = [&](int r0, int r1) {
+    const Steps m = steps_of(a, s, r0, r1);
+    return Steps{max(m.first, all.first), min(m.end, all.end)};
+  };
+  const Steps mine0 = mine(row0, min(row0 + kTileRows, row_end));
+  const Steps mine1 = tiles == 2 ? mine(row0 + kTileRows, row_end) : Steps{all.end, all.end};
+  const int block0 = all.first >> 1, block1 = (all.end + 1) >> 1;   // blocks to widen
+
   // A warp of the issuing role goes on or gives up as one.  The other roles go on with
   // their loops when a lane has given up (every later wait ends at once then), so that no
   // lane leaves its warp, and look at s_abort in the end.
@@ -679,14 +685,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     if (!none) wait_lane(kOFull + 2 * wg + ((m.end - 1) & 1), 0);
     if (__all_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort) == 0)) {
       tc_fence_after();
-      uint32_t nans[D / 32];
+      const float inv = none ? 0.0f : w.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      // Output rows go through shared memory, where Q was (no MMA is left to read it), so
+      // that a store takes whole rows and not 16 bytes of each of 32 (8192-token prompt 972
+      // -> 960 us); in short loops, as their code is fetched for a single use.
+      const uint32_t stage = sbase + C::kQ + wg * C::kTileBytes + (warp & 3) * (32 * 2 * D), own = stage + lane * (2 * D);
+      float* part = a.parts + static_cast<int64_t>(blockIdx.x) * kSplitFloats<D> + wg * kTileRows + t;
+      if (w.splits > 1 && live) {
+        part[0] = top;
+        part[2 * kTileRows] = sum;
+      }
+      part += 4 * kTileRows + (wg * kTileRows + t) * (D - 1);
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(to + 32 * k, o);
+        tmem_ld_wait_for(o);
+        float f[4][8];
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) nans[k] = 0;
-      if (*static_cast<volatile int*>(&s_nan)) {
+        for (int e = 0; e < 32; ++e) f[e >> 3][e & 7] = none ? 0.0f : __uint_as_float(o[e]) * inv;
+        if (w.splits == 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sts16(own + (((4 * k + e) ^ (lane & 7)) << 4), pack8<F16>(f[e]));
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float* x = &f[e >> 1][(e & 1) * 4];
+            reinterpret_cast<float4*>(part)[8 * k + e] = make_float4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+      if (live && *static_cast<volatile int*>(&s_nan)) {
         // NaN codes that were taken out of blocks with rows that do not see them all
         const int hi_all = end_key(d, s, row0 / a.G), lo_all = first_key(d, s, (row_end - 1) / a.G);
-        const int to = min(hi, all.end * kKeys);
-        for (int key = max(lo, all.first * kKeys); key < to; ++key) {
+        const int to_key = min(hi, all.end * kKeys);
+        for (int key = max(lo, all.first * kKeys); key < to_key; ++key) {
           const int k0 = key & ~(kBlock - 1);
           if (!(k0 < lo_all || k0 + kBlock > hi_all)) {
             key = max(key, (hi_all & ~(kBlock - 1)) - 1);
@@ -695,39 +728,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           const int page = __ldg(kc.page_table + b * kc.table_ld + (key >> page_shift));
           if (page < 0 || page >= kc.pages) continue;
           const uint8_t* vp = kc.v + page * kc.v_page_ld + h * kc.v_head_ld + (key & (P - 1)) * kc.v_slot_ld;
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            for (int e = 0; e < 32; ++e)
-              if ((vp[32 * k + e] & 0x7F) == 0x7F) nans[k] |= 1u << e;
-        }
-      }
-      const float inv = w.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-      uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(d.out) + (s.c0 + i) * d.o_token_ld + head * d.o_head_ld);
-      float* part = a.parts + static_cast<int64_t>(blockIdx.x) * kSplitFloats<D> + wg * kTileRows + t;
-      if (w.splits > 1 && live) {
-        part[0] = top;
-        part[2 * kTileRows] = sum;
-      }
-      float4* part_o = reinterpret_cast<float4*>(part - (wg * kTileRows + t) + 4 * kTileRows + (wg * kTileRows + t) * D);
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(to + 32 * k, o);
-        tmem_ld_wait_for(o);
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float f[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              f[y] = (nans[k] >> (e + y)) & 1u ? __uint_as_float(0x7FC00000u) : none ? 0.0f : __uint_as_float(o[e + y]) * inv;
-            if (w.splits > 1) {
-              part_o[8 * k + e / 4] = make_float4(f[0], f[1], f[2], f[3]);
-              part_o[8 * k + e / 4 + 1] = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll 1
+          for (int e = 0; e < D; ++e) {
+            if ((vp[e] & 0x7F) != 0x7F) continue;
+            if (w.splits == 1) {
+              const uint32_t at = own + (((e >> 3) ^ (lane & 7)) << 4) + 2 * (e & 7);
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0x7FFF)) : "memory");   // of either type
             } else {
-              op[4 * k + e / 8] = pack8<F16>(f);
+              part[e] = __uint_as_float(0x7FC00000u);
             }
           }
+        }
+      }
+      if (w.splits == 1) {
+        __syncwarp();
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;           // as Q was read
+        const int sub = lane / kLanes, c16 = lane % kLanes, first = row0 + wg * kTileRows + (warp & 3) * 32;
+        const int i0 = first / a.G, g0 = first - i0 * a.G;
+        const float inv_g = 1.0f / static_cast<float>(a.G);
+        uint16_t* op = static_cast<uint16_t*>(d.out) + (s.c0 + i0) * d.o_token_ld + h * a.G * d.o_head_ld + c16 * 8;
+#pragma unroll 4
+        for (int local = sub; local < 32; local += kAtOnce) {
+          const int x = g0 + local, up = static_cast<int>((static_cast<float>(x) + 0.5f) * inv_g);
+          const uint4 v = lds16(stage + local * (2 * D) + ((c16 ^ (local & 7)) << 4));
+          if (first + local < rows)
+            *reinterpret_cast<uint4*>(op + up * d.o_token_ld + (x - up * a.G) * d.o_head_ld) = v;
         }
       }
       if (live && w.splits == 1 && d.lse != nullptr)
