@@ -36,9 +36,6 @@ constexpr int kBlock = 128;               // keys widened at a time
 constexpr int kStages = 2;                // of K and of V blocks
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmemCols = 512;
-// Smallest factors of a score: -inf, which stands for a key that is not seen, must not
-// meet a zero.
-constexpr float kMinQScale = 8.6736174e-19f, kMinKScale = 8.6736174e-19f;   // 2^-60 each
 // Registers by role (setmaxnreg); the launch refuses any other launch allocation.
 constexpr int kRegsSoftmax = 136, kRegsWiden = 80, kRegsIssue = 48;
 static_assert(256 * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreads * kLaunchRegs, "register split");
@@ -476,9 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         }
         if (!is_v && t < 8) {
           // the V scale as its logarithm and inverse, which is what the weights take
-          const float k = fmaxf(now.x, kMinKScale), v = fmaxf(now.y, kMinScale);
+          const float v = fmaxf(now.y, kMinScale);
           *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + t) * 16) =
-              make_float4(k, __log2f(v), __fdividef(1.0f, v), 0.0f);
+              make_float4(now.x, __log2f(v), __fdividef(1.0f, v), 0.0f);
         }
         if (is_v && (j * kBlock < lo_all || (j + 1) * kBlock > hi_all)) {
           // A NaN must not meet the zero weight of a row that does not see it (as in the
@@ -577,9 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       fence_proxy_async_shared();
       mbar_arrive(bar(kQFull + wg));
     }
-    // with the caps, f is never so small that -inf (a key that is not seen) times f
-    // would be no number; scores that small are all 0 to fp32 anyway
-    if (qs < kMinQScale) qs = kMinQScale;
+    // What a row's S takes to be a score, of the keys with this scale.  -inf, which stands
+    // for a key that is not seen, must not meet a zero; scores so small are 0 anyway.
+    const auto factor = [&](float k_scale) { return fmax_nan(qs * k_scale, FLT_MIN); };
     const auto score = [&](float x, float f, float add) {
       if constexpr (CAP) return keep_hidden(x, capped_log2(x * f, d.softcap * kLog2e) + add);
       return fmaf(x, f, add);
@@ -610,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       }
       // A score is a function of S that does not fall within a group of one scale (q has
       // taken sm_scale's sign), so the maximum needs it once for each group.
-      float best = -INFINITY;
+      float best = -INFINITY, factors[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t* y = &x[k >> 1][(k & 1) * 16];
@@ -620,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           top16 = fmaxf(fmaxf(top16, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
         top16 = fmaxf(top16, __uint_as_float(y[15]));
         const float4 sc = lds16f(scale + k * 16);
-        best = fmaxf(best, score(top16, qs * sc.x, sc.y));
+        factors[k] = factor(sc.x);
+        best = fmaxf(best, score(top16, factors[k], sc.y));
       }
       if (__any_sync(0xffffffffu, best > top + kLazy)) {
         const float next = best > top + kLazy ? best : top;
@@ -648,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       for (int k = 0; k < 4; ++k) {
         uint32_t p[8];
         const float4 sc = lds16f(scale + k * 16);
-        const float f = qs * sc.x, v = sc.y - ref;
+        const float f = factors[k], v = sc.y - ref;
         const uint64_t f2 = f2_pack(f, f), v2 = f2_pack(v, v);
         uint64_t acc[2] = {0, 0};
         const uint32_t* xk = &x[k >> 1][(k & 1) * 16];

@@ -1,0 +1,29 @@
+"""The cache operators at the ends of their ranges.
+
+The tolerance of attention is that of test_gpu_kv (a softmax weight off by at most 2^-11
++ 2^-14, the output's rounding, 1e-7)."""
+import pytest
+import torch
+
+from tests.test_gpu_kv import Cache, plain_attention
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -11 + 2.0 ** -14
+
+
+@pytest.mark.parametrize("new", [1, 40, 150])
+@pytest.mark.parametrize("power", [70, -70])
+def test_attention_key_scales_far_from_one(lib, new, power):
+    # queries as large as the keys are small, or the other way round: scores of a few units
+    t = new + 300
+    c = Cache([t], [new], 2, 64, 16)
+    c.ks.mul_(2.0 ** -power)
+    T, q_heads = new, 4
+    q = (torch.randn((T, q_heads, 64), generator=torch.Generator().manual_seed(5)) * 2.0 ** power).bfloat16().cuda()
+    out, lse = torch.zeros_like(q), torch.zeros((T, q_heads), device="cuda")
+    ws = lib.alloc_kv_workspace(lib.make_kv_attention_desc(q, *c.args(), out, 0.125, new))
+    lib.moe_kv_attention(q, *c.args(), out, ws, 0.125, max_q=new, lse=lse)
+    ref, mag, ref_lse = plain_attention(c, q, 0.125, 0, 0.0, False)
+    assert ((out.double() - ref).abs() <= U * (mag + ref.abs()) + 2.0 ** -8 * ref.abs() + 1e-7).all()
+    assert ((lse.double() - ref_lse).abs() <= 2.0 ** -16 * (ref_lse.abs() + 16)).all()
