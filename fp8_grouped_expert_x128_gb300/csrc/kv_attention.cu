@@ -38,6 +38,7 @@ extern "C" int moe_kv_attention(const moe_kv_attention_desc* d, void* workspace,
   if (int rc = check_device()) return rc;
   AttnArgs a{};
   a.d = *d;
+  if (d->softcap > 0.0f) a.d.softcap = fminf(fmaxf(d->softcap, kMinCap), kMaxCap);
   a.G = d->q_heads / d->cache.kv_heads;
   a.counters = static_cast<int32_t*>(workspace);
   a.parts = reinterpret_cast<float*>(a.counters + kDecodeCounters);

@@ -45,11 +45,26 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // cap * log2(e) * tanh(y) for y = score / cap: tanh(y) = 1 - 2 / (exp(2y) + 1),
-// which ends at +-1 for any y and passes NaN on.
+// which ends at +-1 for any y and passes NaN on.  Its error is absolute, some 2^-22 of
+// the cap, however small the score: for caps up to kCapDirect, where that is below 2^-15.
 __device__ __forceinline__ float capped_log2(float y, float cap_log2) {
   const float e = ex2(2.0f * kLog2e * y);
   return fmaf(-2.0f * cap_log2, __fdividef(1.0f, e + 1.0f), cap_log2);
 }
+// Larger caps take tanh(y) / y times the score, whose error is relative to the score:
+// below |y| = 1/4 by the series 1 - y^2/3 + 2 y^4/15 - 17 y^6/315 + 62 y^8/2835, whose
+// next term is below 2^-26 there.
+constexpr float kCapDirect = 64.0f;
+__device__ __forceinline__ float tanh_ratio(float y) {
+  const float z = y * y;
+  const float p = fmaf(fmaf(fmaf(z, 62.0f / 2835.0f, -17.0f / 315.0f), z, 2.0f / 15.0f), z, -1.0f / 3.0f);
+  const float large = fmaf(-2.0f, __fdividef(1.0f, ex2(2.0f * kLog2e * y) + 1.0f), 1.0f);
+  return fabsf(y) < 0.25f ? fmaf(z, p, 1.0f) : __fdividef(large, y);
+}
+// Caps beyond these are as good as these: below, no score differs from 0 in a weight;
+// above, none is bent within fp32 that is below 2^50.  In between score / cap and its
+// factors stay in fp32's range.
+constexpr float kMinCap = 9.3132257e-10f, kMaxCap = 1.8446744e19f;   // 2^-30, 2^64
 
 // What a sequence's part of the descriptors says, checked.
 struct Seq {

@@ -429,7 +429,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
             f[nt][1] = qs[1] * k_scale;
           }
         }
-        if (d.softcap > 0.0f) {
+        if (d.softcap > kCapDirect) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y = sc[nt][e] * f[nt][e & 1];
+              sc[nt][e] = fmaf(y * tanh_ratio(y), d.softcap * kLog2e, v_log);
+            }
+        } else if (d.softcap > 0.0f) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

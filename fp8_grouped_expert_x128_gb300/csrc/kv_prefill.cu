@@ -276,8 +276,11 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int unit, int splits)
 template <int D>
 constexpr int64_t kSplitFloats = 2 * kTileRows * (D + 2);
 
-template <bool F16, int D, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_constant__ AttnArgs a, int splits) {
+// Caps: none; up to kCapDirect, on the way to the weights; past it, by bending S first.
+enum Cap { kNoCap, kCap, kBend };
+template <bool F16, int D, Cap MODE>
+__device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
+  constexpr bool CAP = MODE == kCap;
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -591,11 +594,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       const int n = g - m.first, buf = g & 1;
       wait_lane(kSFull + 2 * wg + buf, n >> 1);
       tc_fence_after();
-      uint32_t x[2][32];
       const uint32_t at = ts + buf * kKeys;
+      const uint32_t scale = sbase + C::kScale + (((g >> 1) - block0) & (kScaleSlots - 1)) * 128 + buf * 64;
+      if constexpr (MODE == kBend) {
+        // S as if the score had been capped, x tanh(y) / y, in its place
+        const float bend = 1.0f / (d.softcap * kLog2e);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t x[16];
+          tmem_ld_32x32b_x16(at + 16 * k, x);
+          tmem_ld_wait_for(x);
+          const float f = factor(lds16f(scale + k * 16).x) * bend;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x[e] = __float_as_uint(__uint_as_float(x[e]) * tanh_ratio(__uint_as_float(x[e]) * f));
+          tmem_st_x16(at + 16 * k, x);
+        }
+        tmem_st_wait();
+      }
+      uint32_t x[2][32];
       tmem_ld_32x32b_x32(at, x[0]);
       tmem_ld_32x32b_x32(at + 32, x[1]);
-      const uint32_t scale = sbase + C::kScale + (((g >> 1) - block0) & (kScaleSlots - 1)) * 128 + buf * 64;
       const bool edge = g * kKeys < lo_last || (g + 1) * kKeys > hi_first;
       tmem_ld_wait_for(x[0]);
       tmem_ld_wait_for(x[1]);
@@ -768,6 +787,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   }
 }
 
+template <bool F16, int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_constant__ AttnArgs a, int splits) {
+  prefill<F16, D, CAP ? kCap : kNoCap>(a, splits);
+}
+// A kernel of its own: as a branch of the two above its code alone costs their calls up
+// to 7% (windowed prompts under a cap 84 -> 90 us, chunks 573 -> 584).
+template <bool F16, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_bend_kernel(const __grid_constant__ AttnArgs a, int splits) {
+  prefill<F16, D, kBend>(a, splits);
+}
+
 // Fewer units than SMs: their keys are split so that every SM has some, if they are
 // long enough for it (what the page table can hold is all the host knows of them).
 int prefill_splits(const AttnArgs& a, int64_t units) {
@@ -821,12 +851,14 @@ __global__ void __launch_bounds__(32 * kJoinRows) kv_prefill_join_kernel(const _
     d.lse[static_cast<int64_t>(w.s.c0 + i) * d.q_heads + head] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
-template <bool F16, int D, bool CAP>
+template <bool F16, int D, Cap MODE>
 int launch(const AttnArgs& a, cudaStream_t st) {
   static int prepared[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
-  const auto kernel = kv_prefill_kernel<F16, D, CAP>;
+  void (*kernel)(AttnArgs, int);
+  if constexpr (MODE == kBend) kernel = kv_prefill_bend_kernel<F16, D>;
+  else kernel = kv_prefill_kernel<F16, D, MODE == kCap>;
   if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
     // the register split counts on exactly the launch allocation
     cudaFuncAttributes attr;
@@ -847,7 +879,8 @@ int launch(const AttnArgs& a, cudaStream_t st) {
 
 template <bool F16, int D>
 int pick_cap(const AttnArgs& a, cudaStream_t st) {
-  return a.d.softcap > 0.0f ? launch<F16, D, true>(a, st) : launch<F16, D, false>(a, st);
+  if (a.d.softcap > kCapDirect) return launch<F16, D, kBend>(a, st);
+  return a.d.softcap > 0.0f ? launch<F16, D, kCap>(a, st) : launch<F16, D, kNoCap>(a, st);
 }
 
 }  // namespace

@@ -547,7 +547,8 @@ int moe_kv_append(const moe_kv_append_desc *desc, void *stream);
  * For new token i of sequence b at position p, query head hq, kv head
  * h = hq / (q_heads / kv_heads):
  *   score_j = sm_scale * sum_d q[d] * K[j, h, d]
- *   score_j = softcap * tanh(score_j / softcap)                if softcap > 0
+ *   score_j = softcap * tanh(score_j / softcap)                if softcap > 0 (of any
+ *             size: what is lost is small beside the score, or below 2^-15)
  *   visible: 0 <= j < kv_len[b]; j <= p unless MOE_KV_FULL; j > p - window if
  *            window > 0 (not together with MOE_KV_FULL)
  *   out = sum_j softmax_j(score) V[j, h, :],  lse = log sum_j exp(score_j)

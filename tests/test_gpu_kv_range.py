@@ -5,7 +5,7 @@ The tolerance of attention is that of test_gpu_kv (a softmax weight off by at mo
 import pytest
 import torch
 
-from tests.test_gpu_kv import Cache, plain_attention
+from tests.test_gpu_kv import Cache, check_attention, plain_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +27,19 @@ def test_attention_key_scales_far_from_one(lib, new, power):
     ref, mag, ref_lse = plain_attention(c, q, 0.125, 0, 0.0, False)
     assert ((out.double() - ref).abs() <= U * (mag + ref.abs()) + 2.0 ** -8 * ref.abs() + 1e-7).all()
     assert ((lse.double() - ref_lse).abs() <= 2.0 ** -16 * (ref_lse.abs() + 16)).all()
+
+
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("softcap", [63.0, 65.0, 300.0, 1e4, 1e6, 1e9, 1e30])
+def test_attention_large_caps(lib, new, softcap):
+    # tanh(s / cap) is nearly s / cap: what is lost must be small beside s, not beside the cap
+    check_attention(lib, [new + 80, 300], [new, new], 2, 4, 128, 32, softcap=softcap, q_gain=3.0)
+    check_attention(lib, [new + 500], [new], 1, 2, 64, 16, "f16", softcap=softcap, window=100, q_gain=10.0)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("softcap", [1e-3, 1e-20, 1e-42])
+@pytest.mark.parametrize("q_gain", [0.0, 1.0])
+def test_attention_small_caps(lib, new, softcap, q_gain):
+    # all scores are next to nothing: the mean of the values
+    check_attention(lib, [new + 80, 300], [new, new], 2, 4, 128, 32, softcap=softcap, q_gain=q_gain)
