@@ -30,11 +30,13 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Weights are exponentials relative to a reference that follows the running maximum
-// only once it is this far (in powers of two) behind: weights stay below 2^14, inside
-// f16, and what a row has so far is rescaled rarely.  (A larger lag costs no precision:
-// what f16 loses of small weights lies that much further below the maximum.)
-constexpr float kLazy = 14.0f;
+// Weights are exponentials relative to a reference kHead powers of two below the running
+// maximum, which follows it only once a weight would reach 2^kLazy: weights stay inside
+// f16, and what a row has so far is rescaled rarely.  f16 is normal down to 2^-14, so a
+// weight keeps its 11 bits down to 2^-22 of the row's largest, and below that is rounded
+// to multiples of 2^-32 of it, so that keys by the thousand under a dominant one still
+// count.  (With the reference at the maximum those were 2^-14 and 2^-24.)
+constexpr float kHead = 8.0f, kLazy = 15.5f;
 // A V scale this small counts as this: weights carry the scale as its logarithm.
 constexpr float kMinScale = 7.888609e-31f;   // 2^-100
 

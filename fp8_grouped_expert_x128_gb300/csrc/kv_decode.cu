@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              x = fmaxf(x, m[nt][e]);
+              x = fmaxf(x - kHead, m[nt][e]);
               const float keep = x == -INFINITY ? 1.0f : ex2(m[nt][e] - x);
               m[nt][e] = x;
               l[nt][e] *= keep;

@@ -36,6 +36,14 @@ constexpr int kBlock = 128;               // keys widened at a time
 constexpr int kStages = 2;                // of K and of V blocks
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmemCols = 512;
+// Rescaling O takes a step's time, so the reference begins kFirstHead below the maximum,
+// from where it seldom has to move, and is put kHead below after kSettle steps, when a
+// maximum seldom rises by much; until then there are 4096 keys at most, whose rounding to
+// multiples of 2^-26 of the largest weight amounts to 2^-15.  (kHead from the start: 1006
+// us for an 8192-token prompt instead of 972; never, which is not right for long contexts
+// under a dominant key: 959.)
+constexpr float kFirstHead = 2.0f;
+constexpr int kSettle = 64;
 // Registers by role (setmaxnreg); the launch refuses any other launch allocation.
 constexpr int kRegsSoftmax = 136, kRegsWiden = 80, kRegsIssue = 48;
 static_assert(256 * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreads * kLaunchRegs, "register split");
@@ -588,7 +596,8 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
     const int tile_r1 = min(rows, row0 + (wg + 1) * kTileRows) - 1;
     const int lo_last = first_key(d, s, tile_r1 / a.G), hi_first = end_key(d, s, (row0 + wg * kTileRows) / a.G);
     const Steps m = wg ? mine1 : mine0;
-    float top = -INFINITY, ref = 0.0f, sum = 0.0f;       // running reference (ref: the same, 0 while -inf) and sum
+    // running reference (ref: the same, 0 while -inf), sum, and the largest score so far
+    float top = -INFINITY, ref = 0.0f, sum = 0.0f, peak = -INFINITY;
 #pragma unroll 1
     for (int g = m.first; g < m.end; ++g) {
       const int n = g - m.first, buf = g & 1;
@@ -639,8 +648,10 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
         factors[k] = factor(sc.x);
         best = fmaxf(best, score(top16, factors[k], sc.y));
       }
-      if (__any_sync(0xffffffffu, best > top + kLazy)) {
-        const float next = best > top + kLazy ? best : top;
+      peak = fmaxf(peak, best);
+      const bool move = best > top + kLazy || n == kSettle;
+      if (__any_sync(0xffffffffu, move)) {
+        const float next = move ? peak - (n >= kSettle ? kHead : kFirstHead) : top;
         const float keep = next == -INFINITY ? 1.0f : ex2(top - next);
         top = next;
         ref = next == -INFINITY ? 0.0f : next;

@@ -2,6 +2,8 @@
 
 The tolerance of attention is that of test_gpu_kv (a softmax weight off by at most 2^-11
 + 2^-14, the output's rounding, 1e-7)."""
+import math
+
 import pytest
 import torch
 
@@ -43,3 +45,36 @@ def test_attention_large_caps(lib, new, softcap):
 def test_attention_small_caps(lib, new, softcap, q_gain):
     # all scores are next to nothing: the mean of the values
     check_attention(lib, [new + 80, 300], [new, new], 2, 4, 128, 32, softcap=softcap, q_gain=q_gain)
+
+
+def one_long_row_beside_many(lib, new, dim, dtype, page=16):
+    """Sequences whose first keys take nearly all of the weight but hold zeros: the output
+    is what a thousand others bring, each at 78.5 * 2^-24 of the largest weight."""
+    heads, batch, t = 8, 20 if new > 32 else 64, 1024
+    c = Cache([t] * batch, [new] * batch, heads, dim, page, scale=1.0)
+    c.k.zero_()
+    c.v.copy_(torch.randint(0x30, 0x38, c.v.shape, device="cuda", dtype=torch.uint8))     # 0.5 .. 0.9375, all of one sign
+    for b in range(batch):
+        for j in range(0, 64, 16):                # keys 0, 16, 32, 48: one for each warp of a decode CTA
+            p = int(c.table[b, j // page])
+            c.k[p, :, j % page, 0] = 0x38         # 1.0
+            c.v[p, :, j % page] = 0
+    c.ks.fill_(1.0)
+    c.vs.fill_(1.0)
+    q = torch.zeros((batch * new, heads, dim))
+    q[..., 0] = math.log(2.0) * (24 - math.log2(78.5))
+    q = q.to(dtype).cuda()
+    out = torch.zeros_like(q)
+    err = lib.new_error_word()
+    ws = lib.alloc_kv_workspace(lib.make_kv_attention_desc(q, *c.args(), out, 1.0, new))
+    lib.moe_kv_attention(q, *c.args(), out, ws, 1.0, max_q=new, flags=lib.MOE_KV_FULL, err=err)
+    assert lib.moe_read_device_status(err) == (lib.MOE_OK, 0)
+    ref, mag, _ = plain_attention(c, q, 1.0, 0, 0.0, True)
+    bound = U * (mag + ref.abs()) + (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -11) * ref.abs() + 1e-7
+    return ((out.double() - ref).abs() / bound).max().item()
+
+
+@pytest.mark.parametrize("new", [1, 33])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_one_dominant_key(lib, new, dim):
+    assert one_long_row_beside_many(lib, new, dim, torch.float16) <= 1.0
