@@ -46,6 +46,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// V scales ride in the weights, which are f16, so where they lie far apart a page with
+// small values has to be kept from falling under a large one's: outputs may be its alone.
+// Scales within 2^kNear of each other count as one size.
+constexpr int kNear = 4;
+
 // cap * log2(e) * tanh(y) for y = score / cap: tanh(y) = 1 - 2 / (exp(2y) + 1),
 // which ends at +-1 for any y and passes NaN on.  Its error is absolute, some 2^-22 of
 // the cap, however small the score: for caps up to kCapDirect, where that is below 2^-15.

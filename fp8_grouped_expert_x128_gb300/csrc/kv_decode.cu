@@ -15,7 +15,8 @@
 // 16, and K fragments are read straight from shared memory, the head's dimensions
 // taken in the order in which a lane's bytes lie (Q is put in the same order).
 // E4M3 widens exactly to f16 in one instruction per pair.  The V scale rides in
-// the weight: w = exp2(s + log2 s_V - m), the sum takes w / s_V.
+// the weight: w = exp2(s + log2 s_V - m), the sum takes w / s_V; m follows the largest
+// score, and the size of s_V both ways.
 //
 // A step is some 300 instructions with little parallelism inside a warp, so three or
 // four CTAs share an SM (two: 253 us where three take 191).  Measured: 64 sequences of
@@ -380,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
     __syncthreads();
 
     uint32_t nan_seen = 0;
+    float size = -INFINITY, largest = -INFINITY;   // logarithm of the V scales that m goes with; of the largest
 #pragma unroll 1
     for (; tile < tile_stop; ++tile) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
@@ -461,11 +463,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
             }
           }
         }
-        bool over = false;
+        bool over = fabsf(v_log - size) > kNear;           // another size of V: the same for the warp
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           over |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + kLazy || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + kLazy;
         if (__any_sync(0xffffffffu, over)) {
+          // The reference goes with the size of the V scales, down as well as up, so that the
+          // weights are as precise as before; fp32 holds what there is (but not below 2^-60 of
+          // the largest, where it might not).  Then it goes with the maximum.
+          float by = 0.0f;
+          if (fabsf(v_log - size) > kNear) {
+            largest = fmaxf(largest, v_log);
+            const float to = fmaxf(v_log, largest - 60.0f);
+            if (size > -INFINITY) by = to - size;
+            size = to;
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -474,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) kv_decode_ke
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              x = fmaxf(x - kHead, m[nt][e]);
+              x = fmaxf(x - kHead, m[nt][e] + by);
               const float keep = x == -INFINITY ? 1.0f : ex2(m[nt][e] - x);
               m[nt][e] = x;
               l[nt][e] *= keep;

@@ -10,10 +10,10 @@
 // buffers, so that a step's S is there when its softmax begins.  Two more
 // warpgroups widen E4M3 K and V to f16 (exact), 128 keys at a time, on the way into
 // shared memory, straight from global memory through registers, so pages and
-// strides cost little; a warp for each tile issues its MMAs.  Page scales stay out
-// of the operands: K's multiply the scores, V's ride in the weights as in the decode
-// kernel.  Where there are fewer 256-row units than SMs, the keys are split as well,
-// and kv_prefill_join_kernel adds the parts.
+// strides cost little; a warp for each tile issues its MMAs, and one more brings the page
+// scales, which stay out of the operands: K's multiply the scores, V's ride in the weights
+// as in the decode kernel.  Where there are fewer 256-row units than SMs, the keys are
+// split as well, and kv_prefill_join_kernel adds the parts.
 //
 // Measured: an 8192-token prompt with 64 / 8 heads of 128 in 0.96 ms, 1.15 PFLOP/s,
 // 58% of the bf16 rate that a large matrix product has; 1.50 ms under a cap.  No single
@@ -27,7 +27,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 640;             // two warpgroups of softmax, two that widen, one that issues
+constexpr int kThreads = 640;             // two warpgroups of softmax, two that widen, one that issues and brings scales
 constexpr int kWidenThreads = 256, kIssueWarp = 16;
 constexpr int kLaunchRegs = 96;           // registers a thread at launch, split over the warpgroups
 constexpr int kTileRows = 128;
@@ -304,8 +304,9 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
   const auto bar = [&](int i) { return bars + 8 * i; };
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
-      const bool widen = i >= kKFull && i < kVFull + 2, rows128 = i < kQFull + 2 || (i >= kPFull && i < kPFull + 4);
-      mbar_init(bar(i), widen ? kWidenThreads : rows128 ? 128 : 1);
+      const bool rows128 = i < kQFull + 2 || (i >= kPFull && i < kPFull + 4);
+      const int widen = i >= kKFull && i < kVFull ? kWidenThreads + 1 : i >= kVFull && i < kVFull + 2 ? kWidenThreads : 0;
+      mbar_init(bar(i), widen ? widen : rows128 ? 128 : 1);
     }
     s_abort = 0;
     s_nan = 0;
@@ -405,6 +406,55 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
         mbar_wait_bounded(bar(kQFull + i), 1, &dummy, nullptr, kWaitLimitNs / 10);
       }
       __syncwarp();
+    } else if (i == 2) {
+      // ------------------------------------------------------------ scales, a lane for each 16-key group
+      // of a block: K's, and V's as its logarithm and inverse, which is what the weights
+      // take.  Then, of each step's four groups: the size of its largest V scale (its
+      // exponent, not below 2^-60 of the largest of all), and in place of the first one's
+      // NaN where that is a new one, else how far a maximum may lead the reference.
+      const auto page_of = [&](int j) {
+        const int key = j * kBlock + lane * 16;
+        return lane < 8 && key < s.len ? __ldg(kc.page_table + b * kc.table_ld + (key >> page_shift)) : -1;
+      };
+      const auto scales_of = [&](int page) {             // 0 where there are no keys
+        if (page < 0 || page >= kc.pages) return make_float2(0.0f, 0.0f);
+        const int64_t at = static_cast<int64_t>(page) * H + h;
+        return make_float2(__ldg(kc.k_scale + at), __ldg(kc.v_scale + at));
+      };
+      float2 next = scales_of(page_of(block0));
+      int page = page_of(block0 + 1), size = 0, largest = 0;
+#pragma unroll 1
+      for (int j = block0; j < block1; ++j) {
+        const int n = j - block0;
+        const float2 now = next;
+        next = scales_of(page);                          // under way during the wait
+        page = page_of(j + 2);
+        const float v = fmaxf(now.y, kMinScale);
+        int most = now.y > 0.0f ? __float_as_int(v) >> 23 : 0;
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        float w = kLazy;
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+          const int of = __shfl_sync(0xffffffffu, most, 4 * step);
+          const bool other = of != 0 && abs(of - size) > kNear;
+          if (other) {
+            largest = max(largest, of);
+            size = max(of, largest - 60);
+          }
+          if (lane >> 2 == step) w = lane & 3 ? static_cast<float>(size) : other ? __uint_as_float(0x7FC00000u) : kLazy;
+        }
+        // a tile's e-th release: V up to block e - 1 is read, so the weights of that are done
+        if (n >= 2) {
+          wait_lane(kEmpty + (n & 1), (n - 2) >> 1);
+          if (tiles == 2) wait_lane(kEmpty + 2 + (n & 1), (n - 2) >> 1);
+        }
+        if (lane < 8)
+          *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + lane) * 16) =
+              make_float4(now.x, __log2f(v), __fdividef(1.0f, v), w);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kKFull + (n & 1)));
+      }
     }
   } else if (wg >= 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
@@ -445,18 +495,6 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
     const uint8_t* base[2] = {kc.k + h * kc.k_head_ld + (r0 & (P - 1)) * kc.k_slot_ld + ch * 16,
                               kc.v + h * kc.v_head_ld + (r0 & (P - 1)) * kc.v_slot_ld + ch * 16};
     const uint32_t page_ld16[2] = {static_cast<uint32_t>(kc.k_page_ld >> 4), static_cast<uint32_t>(kc.v_page_ld >> 4)};
-    // scales of a block's 16-key groups, by the first warp's first lanes: (K, V)
-    float2 scales;
-    const auto load_scales = [&](int j) {
-      const int key = j * kBlock + (lane & 7) * 16;
-      const int page = __shfl_sync(0xffffffffu, pages, (key >> 4) - pages_from);
-      scales = make_float2(0.0f, 0.0f);
-      if (t < 8 && key < s.len && page >= 0) {
-        const int64_t at = static_cast<int64_t>(page) * H + h;
-        scales = make_float2(__ldg(kc.k_scale + at), __ldg(kc.v_scale + at));
-      }
-    };
-    load_scales(block0);
 #pragma unroll
     for (int i = 0; i < kIter; ++i) load(reg[0][i], i, block0, base[0], page_ld16[0], kc.k_slot_ld);
 #pragma unroll
@@ -465,14 +503,12 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
     for (int j = block0; j < block1; ++j) {
       const int n = j - block0, st = n & 1;
       const bool more = j + 1 < block1;
-      float2 now = scales;
       if (more) {
         if ((j + 1) * 8 - pages_from == 32) {
           pages_from += 32;
           pages = pages_next;
           pages_next = look_up(pages_from + 32);
         }
-        load_scales(j + 1);
       }
 #pragma unroll
       for (int is_v = 0; is_v < 2; ++is_v) {
@@ -481,12 +517,6 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
         if (is_v && n > 0) {
           wait_lane(kEmpty + ((n - 1) & 1), (n - 1) >> 1);
           if (tiles == 2) wait_lane(kEmpty + 2 + ((n - 1) & 1), (n - 1) >> 1);
-        }
-        if (!is_v && t < 8) {
-          // the V scale as its logarithm and inverse, which is what the weights take
-          const float v = fmaxf(now.y, kMinScale);
-          *reinterpret_cast<float4*>(smem + C::kScale + ((n & (kScaleSlots - 1)) * 8 + t) * 16) =
-              make_float4(now.x, __log2f(v), __fdividef(1.0f, v), 0.0f);
         }
         if (is_v && (j * kBlock < lo_all || (j + 1) * kBlock > hi_all)) {
           // A NaN must not meet the zero weight of a row that does not see it (as in the
@@ -598,6 +628,7 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
     const Steps m = wg ? mine1 : mine0;
     // running reference (ref: the same, 0 while -inf), sum, and the largest score so far
     float top = -INFINITY, ref = 0.0f, sum = 0.0f, peak = -INFINITY;
+    float size = 0.0f;                                   // of the V scales that it goes with
 #pragma unroll 1
     for (int g = m.first; g < m.end; ++g) {
       const int n = g - m.first, buf = g & 1;
@@ -635,7 +666,7 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
       }
       // A score is a function of S that does not fall within a group of one scale (q has
       // taken sm_scale's sign), so the maximum needs it once for each group.
-      float best = -INFINITY, factors[4];
+      float best = -INFINITY, factors[4], lead = 0.0f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t* y = &x[k >> 1][(k & 1) * 16];
@@ -646,12 +677,17 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
         top16 = fmaxf(top16, __uint_as_float(y[15]));
         const float4 sc = lds16f(scale + k * 16);
         factors[k] = factor(sc.x);
+        if (k == 0) lead = sc.w;
         best = fmaxf(best, score(top16, factors[k], sc.y));
       }
-      peak = fmaxf(peak, best);
-      const bool move = best > top + kLazy || n == kSettle;
-      if (__any_sync(0xffffffffu, move)) {
-        const float next = move ? peak - (n >= kSettle ? kHead : kFirstHead) : top;
+      if (__any_sync(0xffffffffu, !(best <= top + lead) || n == kSettle)) {
+        // The reference goes with the size of the V scales, down as well as up, so that weights
+        // are as precise as before (fp32 holds what there is), and then with the maximum.
+        const float now = lds16f(scale + 16).w, base = top + (now - size);
+        peak += now - size;
+        size = now;
+        float next = base;
+        if (best > base + kLazy || n == kSettle) next = fmaxf(peak, best) - (n >= kSettle ? kHead : kFirstHead);
         const float keep = next == -INFINITY ? 1.0f : ex2(top - next);
         top = next;
         ref = next == -INFINITY ? 0.0f : next;
@@ -672,6 +708,7 @@ __device__ __forceinline__ void prefill(const AttnArgs& a, int splits) {
           }
         }
       }
+      peak = fmaxf(peak, best);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t p[8];

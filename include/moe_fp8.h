@@ -559,12 +559,13 @@ int moe_kv_append(const moe_kv_append_desc *desc, void *stream);
  * sums.  E4M3 codes are exact in f16; a q row is first scaled by a power of two
  * that takes its largest element into [1, 2), so bf16 rows fit (elements below
  * 2^-14 of the largest lose bits below 2^-24 of it).  Scores, softmax statistics
- * and outputs are held in fp32; out is rounded once to its type.  The softmax
- * weights, which carry the V scale, are rounded to f16 for the second product: to 11
- * bits, and where weight times scale is below 2^-22 of the row's largest (2^-16 within
- * the first 4096 keys of a run) to multiples of 2^-32 (2^-26) of that.  Scales must be
- * positive and finite (below 2^-100 a V scale counts as that).  Results repeat bit for
- * bit.
+ * and outputs are held in fp32; out is rounded once to its type.  The softmax weights
+ * are rounded to f16 for the second product: to 11 bits, and where one is below 2^-18
+ * of the row's largest (2^-12 within the first 4096 keys) to multiples of 2^-28 (2^-22)
+ * of that.  V scales may lie up to 2^60 apart without taking part in this, but for pages
+ * of 16 and 32 tokens under more than 32 rows: of these, weight times scale counts
+ * within each 64 keys.  Scales must be positive and finite (below 2^-100 a V scale
+ * counts as that).  Results repeat bit for bit.
  * q, out: device rows as in moe_kv_append; lse: device fp32 [T, q_heads] or NULL.
  * max_q: no sequence has more new tokens than this (0 = T): a hint that picks
  * the kernels; a sequence with more is skipped with MOE_DEV_OVERFLOW.

@@ -78,3 +78,28 @@ def one_long_row_beside_many(lib, new, dim, dtype, page=16):
 @pytest.mark.parametrize("dim", [64, 128])
 def test_attention_one_dominant_key(lib, new, dim):
     assert one_long_row_beside_many(lib, new, dim, torch.float16) <= 1.0
+
+
+@pytest.mark.parametrize("new", [1, 5, 40, 200])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 16), (128, 64)])
+@pytest.mark.parametrize("low,high", [(-22, 9), (9, -22), (-20, -7), (0, -13)])
+def test_attention_small_pages_under_large_ones(lib, new, dim, page, low, high):
+    # runs of 64 keys have one V scale and the other by turns; those with the larger one
+    # hold zeros in half of the dimensions, where the output is the others' alone
+    heads, batch, t = (8, 64, 1024) if new <= 5 else (2, 1, new + 700)      # several runs for every warp
+    c = Cache([t] * batch, [new] * batch, heads, dim, page, scale=2.0 ** -7)
+    table = c.table[:, : c.pages_of[0]].long()
+    turn = (torch.arange(table.shape[1], device="cuda") * page // 64) % 2 == 1
+    one, other = table[:, ~turn].flatten(), table[:, turn].flatten()
+    c.vs[one], c.vs[other] = 1.25 * 2.0 ** low, 1.5 * 2.0 ** high
+    c.v[other if high > low else one, :, :, : dim // 2] = 0
+    check_attention(lib, c.total, c.new, heads, 2 * heads, dim, page, q_gain=0.5, cache=c)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_scales_of_neighbouring_pages(lib, new):
+    # each 16 keys another scale, within one step of the kernel for prompts
+    c = Cache([new + 500], [new], 2, 128, 16, scale=2.0 ** -7)
+    c.vs.copy_(torch.exp2(torch.randint(-11, 12, c.vs.shape, generator=torch.Generator().manual_seed(2)).float()))
+    c.v[(c.vs > 1)[:, 0], :, :, :64] = 0
+    check_attention(lib, [new + 500], [new], 2, 4, 128, 16, q_gain=0.5, cache=c)
