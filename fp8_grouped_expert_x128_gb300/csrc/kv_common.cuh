@@ -21,9 +21,11 @@ inline int check_kv_cache(const moe_kv_cache& c, int64_t T) {
   MOE_CHECK_ARG(c.table_ld >= 0);
   if (c.dim != 64 && c.dim != 128) return MOE_ERR_UNSUPPORTED;
   if (c.page_size != 16 && c.page_size != 32 && c.page_size != 64 && c.page_size != 128) return MOE_ERR_UNSUPPORTED;
-  // positions, rows and units of work are 32-bit numbers
+  // positions, rows and units of work are 32-bit numbers; the kernels look up pages some
+  // thousand positions ahead of a sequence's end, which must not wrap around
+  constexpr int32_t kMaxTokens = INT32_MAX - 65535;
   if (c.batch > (1 << 20) || T > (1 << 24) || c.kv_heads > 1024 || c.pages > INT32_MAX ||
-      c.max_pages > INT32_MAX / c.page_size || c.k_page_ld >= (1ll << 35) || c.v_page_ld >= (1ll << 35))
+      c.max_pages > kMaxTokens / c.page_size || c.k_page_ld >= (1ll << 35) || c.v_page_ld >= (1ll << 35))
     return MOE_ERR_UNSUPPORTED;
   if (T == 0 || c.batch == 0) return MOE_OK;
   MOE_CHECK_ARG(c.k && c.v && c.k_scale && c.v_scale && c.page_table && c.cu_new && c.kv_len);

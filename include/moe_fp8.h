@@ -470,7 +470,7 @@ int moe_ffn_noalloc(const moe_ffn_desc *desc, void *stream);
  * Limits: dim 64 or 128; page_size 16, 32, 64 or 128; strides in bytes,
  * multiples of 16, not negative, page strides below 2^35; q_heads a multiple of
  * kv_heads; at most 2^24 rows and 2^30 / q_heads of them, 2^20 sequences, 1024 kv
- * heads.  Offsets into the cache and the rows are 64-bit.  Device-side faults of
+ * heads, max_pages * page_size up to 2^31 - 2^16.  Offsets into the cache and the rows are 64-bit.  Device-side faults of
  * the descriptors set bits in `err` (which may be NULL), and nothing out of range
  * is read or written: a sequence that does not lie in the token rows (cu_new
  * decreasing, negative or past T) or that is shorter than its new tokens --
