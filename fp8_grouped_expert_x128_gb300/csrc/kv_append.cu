@@ -115,6 +115,12 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, bool pow2)
   return pack_e4m3x8(q);
 }
 
+// What is wrong with a sequence that has new tokens, so that it is skipped whole; 0: nothing.
+__device__ __forceinline__ int32_t sequence_fault(const moe_kv_append_desc& d, int c0, int c1, int len) {
+  if (c0 < 0 || c1 < c0 || c1 > d.T || len < c1 - c0) return MOE_DEV_BAD_INDEX;
+  return len > d.cache.max_pages * d.cache.page_size ? MOE_DEV_OVERFLOW : 0;
+}
+
 template <bool F16, int D, int TT>
 __device__ void rotate_queries(const AppendArgs& a, int cta) {
   const moe_kv_append_desc& d = a.d;
@@ -131,10 +137,10 @@ __device__ void rotate_queries(const AppendArgs& a, int cta) {
     const int mid = (lo + hi) >> 1;
     if (__ldg(d.cache.cu_new + mid) <= t_warp) lo = mid; else hi = mid;
   }
-  const int c0 = __ldg(d.cache.cu_new + lo), c1 = __ldg(d.cache.cu_new + lo + 1);
-  if (t >= d.T || t < c0 || t >= c1 || c1 > d.T) return;
-  const int pos = __ldg(d.cache.kv_len + lo) - (c1 - t);
-  if (pos < 0 || (d.rot_dim && pos >= d.max_pos)) {
+  const int c0 = __ldg(d.cache.cu_new + lo), c1 = __ldg(d.cache.cu_new + lo + 1), len = __ldg(d.cache.kv_len + lo);
+  if (t >= d.T || t < c0 || t >= c1 || sequence_fault(d, c0, c1, len)) return;   // the pages' CTAs tell of faults
+  const int pos = len - (c1 - t);
+  if (d.rot_dim && pos >= d.max_pos) {
     set_err(d.err, MOE_DEV_BAD_INDEX);
     return;
   }
@@ -194,18 +200,14 @@ __device__ __forceinline__ bool page_work(const moe_kv_append_desc& d, int unit,
   const int c0 = __ldg(kc.cu_new + w.b), c1 = __ldg(kc.cu_new + w.b + 1), len = __ldg(kc.kv_len + w.b);
   const int n = c1 - c0;
   if (n == 0) return false;
-  if (c0 < 0 || n < 0 || c1 > d.T || len < n) {
-    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_BAD_INDEX);
+  if (const int32_t fault = sequence_fault(d, c0, c1, len)) {
+    if (threadIdx.x == 0) set_err(d.err, fault);
     return false;
   }
   const int pos0 = len - n;                                  // position of the sequence's first new token
   const int nth = unit - (c0 / P + 2 * w.b);                 // of the pages the new tokens fall on
   w.pi = pos0 / P + nth;
   if (nth < 0 || w.pi > (len - 1) / P) return false;
-  if (w.pi >= kc.max_pages) {
-    if (threadIdx.x == 0) set_err(d.err, MOE_DEV_OVERFLOW);
-    return false;
-  }
   w.page = __ldg(kc.page_table + w.b * kc.table_ld + w.pi);
   w.s0 = max(pos0 - w.pi * P, 0);
   w.s1 = min(len - w.pi * P, P);

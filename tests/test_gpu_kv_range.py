@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_kv import Cache, check_attention, plain_attention
+from tests.test_gpu_kv import Cache, angles, check_attention, plain_attention, rotated
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +103,39 @@ def test_attention_scales_of_neighbouring_pages(lib, new):
     c.vs.copy_(torch.exp2(torch.randint(-11, 12, c.vs.shape, generator=torch.Generator().manual_seed(2)).float()))
     c.v[(c.vs > 1)[:, 0], :, :, :64] = 0
     check_attention(lib, [new + 500], [new], 2, 4, 128, 16, q_gain=0.5, cache=c)
+
+
+# ---------------------------------------------------------------- sequences that are skipped
+def appended(lib, c, cs, q_heads=2, seed=3):
+    """One append; what was there before, the rows, the queries' output and the status bits."""
+    T = int(c.cu.max())
+    x = torch.randn((T, 2 * c.heads + q_heads, c.dim), generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+    q = x[:, :q_heads]
+    out = torch.full((T, q_heads, c.dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    before = [t.clone() for t in (c.k, c.v, c.ks, c.vs)]
+    err = lib.new_error_word()
+    lib.moe_kv_append(x[:, q_heads:q_heads + c.heads], x[:, q_heads + c.heads:], *c.args(), cos_sin=cs, q=q, q_out=out, err=err)
+    return before, x, out, lib.moe_read_device_status(err)[1]
+
+
+@pytest.mark.parametrize("batch", [2, 40])          # the kernel for prompts, the one for few tokens
+@pytest.mark.parametrize("what,bit", [("long", 1), ("short", 4)])
+def test_append_skips_a_bad_sequence_whole(lib, batch, what, bit):
+    # 20 new tokens that fall on a page inside the table and on one past it; or more new tokens than tokens
+    c = Cache([40] + [17] * (batch - 1), [20] + [1] * (batch - 1), 2, 64, 16, scale=2.0 ** -9)
+    if what == "long":
+        c.table = c.table[:, :2].contiguous()
+    else:
+        c.kv_len[0] = 19
+    cs = angles(64, 64)
+    before, x, out, status = appended(lib, c, cs)
+    assert status == bit
+    own = c.table[0, : min(c.table.shape[1], 3)].long()
+    for now, was in zip((c.k, c.v, c.ks, c.vs), before):
+        assert torch.equal(now[own], was[own])
+    assert (out[:20] == 7).all()
+    # the others are served
+    ref = rotated(x[20:, :2], cs, torch.full((batch - 1,), 16, device="cuda"), 64, False)
+    assert ((out[20:].double() - ref).abs() <= 2.0 ** -8 * 1.001 * ref.abs() + 1e-6).all()
+    page = c.table[1:, 1].long()
+    assert (c.vs[page] == torch.exp2(torch.ceil(torch.log2(x[20:, 4:].double().abs().amax(2) / 448)))).all()
