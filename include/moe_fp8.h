@@ -472,11 +472,12 @@ int moe_ffn_noalloc(const moe_ffn_desc *desc, void *stream);
  * kv_heads; at most 2^24 rows and 2^30 / q_heads of them, 2^20 sequences, 1024 kv
  * heads, max_pages * page_size up to 2^31 - 2^16.  Offsets into the cache and the rows are 64-bit.  Device-side faults of
  * the descriptors set bits in `err` (which may be NULL), and nothing out of range
- * is read or written: a sequence that does not lie in the token rows (cu_new
- * decreasing, negative or past T) or that is shorter than its new tokens --
- * MOE_DEV_BAD_INDEX, and one with more pages than max_pages -- MOE_DEV_OVERFLOW,
- * are skipped; a page id outside [0, pages) -- MOE_DEV_BAD_INDEX -- is skipped by
- * an append, and leaves the sequence's attention output unspecified.
+ * is read or written: a sequence that ends past row T or that is shorter than its
+ * new tokens -- MOE_DEV_BAD_INDEX, and one with more pages than max_pages --
+ * MOE_DEV_OVERFLOW, are skipped, the others are served; a page id outside [0, pages)
+ * -- MOE_DEV_BAD_INDEX -- is skipped by an append, and leaves the sequence's attention
+ * output unspecified; where cu_new decreases or is negative -- MOE_DEV_BAD_INDEX --
+ * the whole call's results are unspecified.
  */
 #define MOE_DTYPE_BF16 0              /* element types of q, k, v and out */
 #define MOE_DTYPE_F16 1

@@ -139,3 +139,30 @@ def test_append_skips_a_bad_sequence_whole(lib, batch, what, bit):
     assert ((out[20:].double() - ref).abs() <= 2.0 ** -8 * 1.001 * ref.abs() + 1e-6).all()
     page = c.table[1:, 1].long()
     assert (c.vs[page] == torch.exp2(torch.ceil(torch.log2(x[20:, 4:].double().abs().amax(2) / 448)))).all()
+
+
+@pytest.mark.parametrize("cu", [[0, 100, 50, 150], [0, 30, -3, 150], [-5, 20, 30, 150], [60, 60, 59, 150], [0, 150, 0, 150]])
+def test_offsets_that_decrease_are_told(lib, cu):
+    # whatever the units' search lands on; nothing outside the rows and pages is touched
+    T = 150
+    c = Cache([160, 160, 160], [1, 1, 1], 2, 64, 16)
+    c.cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    spare = [p for p in range(c.k.shape[0]) if p not in set(c.table.flatten().tolist())]
+    assert spare
+    for batch_of_units in (1, 60):
+        if batch_of_units > 1:                      # a batch with few tokens a sequence: the other kernel
+            c.cu = torch.cat([c.cu, torch.full((57,), 150, dtype=torch.int32, device="cuda")])
+            c.kv_len = torch.cat([c.kv_len, c.kv_len.new_zeros(57)])
+            c.table = torch.cat([c.table, c.table.new_full((57, c.table.shape[1]), -1)])
+        x = torch.randn((T, 2, 64), generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+        before = c.k[spare].clone(), c.ks[spare].clone()
+        q = torch.zeros_like(x)
+        err = lib.new_error_word()
+        lib.moe_kv_append(x, x, *c.args(), cos_sin=angles(160, 64), q=x, q_out=q, err=err)
+        assert lib.moe_read_device_status(err)[1] & 4
+        assert torch.equal(c.k[spare], before[0]) and torch.equal(c.ks[spare], before[1])
+        out = torch.zeros_like(x)
+        err = lib.new_error_word()
+        ws = lib.alloc_kv_workspace(lib.make_kv_attention_desc(x, *c.args(), out, 0.125))
+        lib.moe_kv_attention(x, *c.args(), out, ws, 0.125, err=err)
+        assert lib.moe_read_device_status(err)[1] & 4
