@@ -172,7 +172,11 @@ def _stream(stream=None):
 
 def _stream_of(device: int, stream=None) -> int:
     """The handle of `stream`, or of the current stream of GPU `device`."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream: on GPU {stream.device_index}, the cache on GPU {device}")
+    return stream.cuda_stream
 
 
 def _check(rc: int, where: str):
@@ -492,6 +496,8 @@ def _kv_cache_refused(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv
                     (cu_new, "cu_new"), (kv_len, "kv_len")):
         if t.get_device() != device:
             return ValueError(f"{name}: not on the GPU that holds k_cache")
+    if torch.cuda.current_device() != device:        # the library launches on the current one
+        return ValueError(f"k_cache: on GPU {device}, but GPU {torch.cuda.current_device()} is current (torch.cuda.set_device)")
     return ValueError("paged cache: tensors not as moe_fp8.h has them")
 
 
@@ -512,7 +518,8 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dt
             and k_scale.dtype is f32 and v_scale.dtype is f32
             and page_table.dtype is i32 and cu_new.dtype is i32 and kv_len.dtype is i32
             and v_cache.get_device() == device and k_scale.get_device() == device and v_scale.get_device() == device
-            and page_table.get_device() == device and cu_new.get_device() == device and kv_len.get_device() == device):
+            and page_table.get_device() == device and cu_new.get_device() == device and kv_len.get_device() == device
+            and torch.cuda.current_device() == device):
         raise _kv_cache_refused(k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, dtype)
     return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
             cu_new.data_ptr(), kv_len.data_ptr(), kp, kh, ks, vp, vh, vs, table_ld, pages, batch, max_pages,

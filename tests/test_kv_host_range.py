@@ -1,5 +1,8 @@
 """Limits of the key/value cache calls, checked on the host before any CUDA call."""
+import types
+
 import pytest
+import torch
 
 from tests.test_kv_host import append, attention, cache, moe  # noqa: F401
 
@@ -16,3 +19,68 @@ def test_positions_do_not_wrap_around(moe, page_size):  # noqa: F811
     for pages in (longest + 1, ((1 << 31) - 1) // page_size):
         assert append(moe, cache(moe, page_size=page_size, max_pages=pages)) == -2
         assert attention(moe, cache(moe, page_size=page_size, max_pages=pages))[0] == -2
+
+
+class OnGpu:
+    """As much of a tensor on some GPU as the binding looks at; there is no memory behind it."""
+
+    def __init__(self, shape, dtype, device):
+        self.meta, self.device_number = torch.empty(shape, dtype=dtype, device="meta"), device
+
+    def get_device(self):
+        return self.device_number
+
+    def data_ptr(self):
+        return 4096
+
+    def __getattr__(self, name):
+        return getattr(self.meta, name)
+
+
+def calls(moe, device):  # noqa: F811
+    def t(*shape, dtype):
+        return OnGpu(shape, dtype, device)
+
+    cache = [t(4, 2, 16, 64, dtype=torch.uint8) for _ in range(2)] + [t(4, 2, dtype=torch.float32) for _ in range(2)]
+    cache += [t(1, 2, dtype=torch.int32), t(2, dtype=torch.int32), t(1, dtype=torch.int32)]
+    q, ws = t(1, 2, 64, dtype=torch.bfloat16), t(1 << 20, dtype=torch.uint8)
+    return [lambda **kw: moe.moe_kv_append(q, q, *cache, **kw),
+            lambda **kw: moe.moe_kv_attention(q, *cache, q, ws, 1.0, **kw),
+            lambda **kw: moe.make_kv_attention_desc(q, *cache, q, 1.0, **kw)]
+
+
+class Library:
+    """In the library's place: counts the calls that get through."""
+
+    def __init__(self):
+        self.through = 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.through += 1
+            return 0
+        return call
+
+
+def test_tensors_of_another_gpu_than_the_current_one_are_refused(moe, monkeypatch):  # noqa: F811
+    """The library launches on the current GPU: with the handle of another one's stream (0 for
+    every GPU's default stream) it would use foreign pointers there."""
+    library = Library()
+    monkeypatch.setattr(moe, "_lib", library)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    for call in calls(moe, 1):
+        with pytest.raises(ValueError, match="GPU 1, but GPU 0 is current"):
+            call()
+    append_call, attention_call, describe = calls(moe, 0)
+    other, own = (types.SimpleNamespace(device_index=d, cuda_stream=77) for d in (1, 0))
+    for call in (append_call, attention_call):
+        with pytest.raises(ValueError, match="stream: on GPU 1"):
+            call(stream=other)
+    assert library.through == 0
+    append_call()
+    append_call(stream=own)
+    attention_call()
+    attention_call(stream=own)
+    describe()
+    assert library.through == 4
