@@ -607,8 +607,8 @@ def moe_kv_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, 
     c, rest = _kv_attention_fields(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, kv_len, out, sm_scale, max_q, window,
                                    softcap, flags, lse, err)
     device = q.get_device()
-    if workspace.get_device() != device:
-        raise ValueError("workspace: not on the cache's GPU")
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on the cache's GPU")
     rc = _lib.moe_kv_attention(_kv_attention_pack(*c, *rest), workspace.data_ptr(), workspace.nbytes, _stream_of(device, stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_kv_attention")

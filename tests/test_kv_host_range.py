@@ -37,13 +37,13 @@ class OnGpu:
         return getattr(self.meta, name)
 
 
-def calls(moe, device):  # noqa: F811
+def calls(moe, device, workspace=None):  # noqa: F811
     def t(*shape, dtype):
         return OnGpu(shape, dtype, device)
 
     cache = [t(4, 2, 16, 64, dtype=torch.uint8) for _ in range(2)] + [t(4, 2, dtype=torch.float32) for _ in range(2)]
     cache += [t(1, 2, dtype=torch.int32), t(2, dtype=torch.int32), t(1, dtype=torch.int32)]
-    q, ws = t(1, 2, 64, dtype=torch.bfloat16), t(1 << 20, dtype=torch.uint8)
+    q, ws = t(1, 2, 64, dtype=torch.bfloat16), workspace or t(1 << 20, dtype=torch.uint8)
     return [lambda **kw: moe.moe_kv_append(q, q, *cache, **kw),
             lambda **kw: moe.moe_kv_attention(q, *cache, q, ws, 1.0, **kw),
             lambda **kw: moe.make_kv_attention_desc(q, *cache, q, 1.0, **kw)]
@@ -84,3 +84,17 @@ def test_tensors_of_another_gpu_than_the_current_one_are_refused(moe, monkeypatc
     attention_call(stream=own)
     describe()
     assert library.through == 4
+
+
+def test_a_workspace_that_only_looks_large_is_refused(moe, monkeypatch):  # noqa: F811
+    """An expanded tensor counts bytes that it does not have."""
+    library = Library()
+    monkeypatch.setattr(moe, "_lib", library)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    one = OnGpu((1,), torch.uint8, 0)
+    one.meta = one.meta.expand(1 << 20)
+    assert one.nbytes == 1 << 20
+    with pytest.raises(ValueError, match="workspace"):
+        calls(moe, 0, one)[1]()
+    assert library.through == 0
