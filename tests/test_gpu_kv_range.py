@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_kv import Cache, angles, check_attention, plain_attention, rotated
+from tests.test_gpu_kv import Cache, angles, check_append, check_attention, plain_attention, rotated
 
 pytestmark = pytest.mark.gpu
 
@@ -105,6 +105,36 @@ def test_attention_scales_of_neighbouring_pages(lib, new):
     check_attention(lib, [new + 500], [new], 2, 4, 128, 16, q_gain=0.5, cache=c)
 
 
+@pytest.mark.parametrize("heads,q_heads,new", [(1, 64, 1), (1, 128, 2), (1, 64, 9), (2, 96, 7), (1, 20, 13), (1, 17, 1)])
+def test_attention_wide_groups(lib, heads, q_heads, new):
+    # units and groups of rows that end inside a token
+    check_attention(lib, [new + 300, 77], [new, min(new, 3)], heads, q_heads, 128, 32)
+    check_attention(lib, [new + 300, 77], [new, min(new, 3)], heads, q_heads, 64, 64, "f16", window=40)
+
+
+def test_sliced_page_table(lib):
+    c = Cache([200, 90, 33], [5, 40, 1], 2, 64, 16)
+    wide = torch.full((3, 40), -5, dtype=torch.int32, device="cuda")
+    wide[:, 7:7 + c.table.shape[1]] = c.table
+    c.table = wide[:, 7:7 + c.table.shape[1]]
+    x = torch.randn((46, 2, 64), generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    err = lib.new_error_word()
+    lib.moe_kv_append(x, x, *c.args(), err=err)
+    assert lib.moe_read_device_status(err) == (lib.MOE_OK, 0)
+    check_attention(lib, c.total, c.new, 2, 4, 64, 16, cache=c)
+
+
+@pytest.mark.parametrize("new,window", [(1, 1), (1, 50), (3, 17), (9, 64)])
+def test_attention_many_sequences_under_a_window(lib, new, window):
+    total = [new + (37 * i) % 191 for i in range(150)]
+    check_attention(lib, total, [new if i % 7 else 0 for i in range(150)], 2, 8, 64, 16, window=window)
+
+
+def test_append_wide_groups(lib):
+    check_append(lib, [300, 40], [40, 3], 1, 33, 128, 32, 128, False, "bf16")
+    check_append(lib, [300, 40, 9], [1, 1, 1], 1, 64, 64, 16, 64, True, "f16")
+
+
 # ---------------------------------------------------------------- sequences that are skipped
 def appended(lib, c, cs, q_heads=2, seed=3):
     """One append; what was there before, the rows, the queries' output and the status bits."""
@@ -166,3 +196,34 @@ def test_offsets_that_decrease_are_told(lib, cu):
         ws = lib.alloc_kv_workspace(lib.make_kv_attention_desc(x, *c.args(), out, 0.125))
         lib.moe_kv_attention(x, *c.args(), out, ws, 0.125, err=err)
         assert lib.moe_read_device_status(err)[1] & 4
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("what,bit", [("long", 1), ("short", 4), ("max_q", 1)])
+def test_attention_skips_a_bad_sequence_alone(lib, new, what, bit):
+    total, news = [90, 45 + new, 300], [new, new + 2, new]
+    c = Cache(total, news, 2, 64, 16)
+    max_q = new + 2
+    if what == "long":
+        c.table[1] = -1
+        c.kv_len[1] = 16 * c.table.shape[1] + 1
+    elif what == "short":
+        c.kv_len[1] = new + 1
+    else:
+        max_q = new + 1
+    T = sum(news)
+    q = torch.randn((T, 4, 64), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((T, 4), 7.0, device="cuda")
+    err = lib.new_error_word()
+    ws = lib.alloc_kv_workspace(lib.make_kv_attention_desc(q, *c.args(), out, 0.125, max_q))
+    lib.moe_kv_attention(q, *c.args(), out, ws, 0.125, max_q=max_q, lse=lse, err=err)
+    assert lib.moe_read_device_status(err)[1] == bit
+    mine = torch.zeros(T, dtype=torch.bool, device="cuda")
+    mine[new:2 * new + 2] = True
+    assert (out[mine] == 7).all() and (lse[mine] == 7).all()
+    good = Cache(total, news, 2, 64, 16)               # the same codes, as they were
+    good.total, good.new = [total[0], 0, total[2]], [new, 0, new]
+    ref, mag, _ = plain_attention(good, q, 0.125, 0, 0.0, False)
+    ok = (out.double() - ref).abs() <= U * (mag + ref.abs()) + 2.0 ** -8 * ref.abs() + 1e-7
+    assert ok[~mine].all()
