@@ -37,8 +37,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // to multiples of 2^-32 of it, so that keys by the thousand under a dominant one still
 // count.  (With the reference at the maximum those were 2^-14 and 2^-24.)
 constexpr float kHead = 8.0f, kLazy = 15.5f;
-// A V scale this small counts as this: weights carry the scale as its logarithm.
-constexpr float kMinScale = 7.888609e-31f;   // 2^-100
+// A V scale this small counts as this: weights carry the scale as its logarithm, and the
+// sum of weights over scales, up to 2^kLazy times 2^31 keys over this, has to stay in fp32.
+constexpr float kMinScale = 8.2718061e-25f;   // 2^-80
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -565,7 +565,7 @@ int moe_kv_append(const moe_kv_append_desc *desc, void *stream);
  * of the row's largest (2^-12 within the first 4096 keys) to multiples of 2^-28 (2^-22)
  * of that.  V scales may lie up to 2^60 apart without taking part in this, but for pages
  * of 16 and 32 tokens under more than 32 rows: of these, weight times scale counts
- * within each 64 keys.  Scales must be positive and finite (below 2^-100 a V scale
+ * within each 64 keys.  Scales must be positive and finite (below 2^-80 a V scale
  * counts as that).  Results repeat bit for bit.
  * q, out: device rows as in moe_kv_append; lse: device fp32 [T, q_heads] or NULL.
  * max_q: no sequence has more new tokens than this (0 = T): a hint that picks

@@ -105,6 +105,26 @@ def test_attention_scales_of_neighbouring_pages(lib, new):
     check_attention(lib, [new + 500], [new], 2, 4, 128, 16, q_gain=0.5, cache=c)
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_smallest_scales_over_many_keys(lib, new):
+    # a million keys of equal weight under V scales below the smallest that count: the sum of
+    # weights over scales stays in range
+    t, page, dim = 1 << 20, 128, 64
+    pages = t // page
+    k = torch.zeros((pages, 1, page, dim), dtype=torch.uint8, device="cuda")
+    v = torch.randint(0x30, 0x40, k.shape, dtype=torch.uint8, device="cuda")
+    ks, vs = torch.ones((pages, 1), device="cuda"), torch.full((pages, 1), 2.0 ** -100, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    cu, kv_len = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, new], [t]))
+    q = torch.ones((new, 2, dim), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(q)
+    args = (q, k, v, ks, vs, table, cu, kv_len, out)
+    ws = lib.alloc_kv_workspace(lib.make_kv_attention_desc(*args, 0.125, new))
+    lib.moe_kv_attention(*args, ws, 0.125, max_q=new, flags=lib.MOE_KV_FULL)
+    ref = v.view(torch.float8_e4m3fn).float().mean((0, 1, 2)).double() * 2.0 ** -80
+    assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref).all()
+
+
 @pytest.mark.parametrize("heads,q_heads,new", [(1, 64, 1), (1, 128, 2), (1, 64, 9), (2, 96, 7), (1, 20, 13), (1, 17, 1)])
 def test_attention_wide_groups(lib, heads, q_heads, new):
     # units and groups of rows that end inside a token
