@@ -244,9 +244,15 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
 }
 
 // A unit: up to 256 rows of a sequence.  Units of sequence b start at cu[b] * G / 256 +
-// b: enough for its rows whatever cu is, and nothing has to be summed.  Its keys are
-// cut into `splits` runs of `chunk` steps (an even number: whole blocks), fewer than
-// asked for where they would be short.
+// min(b, cu[b] * G / 33): enough for its rows whatever cu is if it has more than 32, as
+// both terms of the minimum then grow by one at least, and nothing has to be summed; those
+// with fewer, or none, add next to no units.  A unit's keys are cut into `splits` runs of
+// `chunk` steps (an even number: whole blocks), fewer than asked for where they would be
+// short.
+__host__ __device__ __forceinline__ uint32_t units_before(uint32_t b, uint32_t rows) {
+  const uint32_t many = rows / (kDecodeRows + 1);
+  return rows / (2 * kTileRows) + (many < b ? many : b);
+}
 struct Unit {
   int b, rows, row0, row_end, splits, chunk;
   Seq s;
@@ -256,7 +262,7 @@ constexpr int kMinChunk = 8;             // steps
 __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int unit, int splits) {
   const moe_kv_cache& kc = a.d.cache;
   const auto unit0 = [&](int b) {
-    return static_cast<int>(static_cast<int64_t>(__ldg(kc.cu_new + b)) * a.G / (2 * kTileRows)) + b;
+    return static_cast<int>(units_before(b, static_cast<uint32_t>(__ldg(kc.cu_new + b)) * a.G));   // at most 2^30 rows
   };
   Unit u;
   u.splits = 0;
@@ -915,9 +921,10 @@ int launch(const AttnArgs& a, cudaStream_t st) {
     MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem));
     __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
   }
-  const int64_t units = (a.d.T * a.G / (2 * kTileRows) + a.d.cache.batch) * a.d.cache.kv_heads;
+  const int64_t units = static_cast<int64_t>(units_before(a.d.cache.batch, static_cast<uint32_t>(a.d.T * a.G))) * a.d.cache.kv_heads;
+  if (units == 0) return MOE_OK;           // max_q allows more rows than there are
   const int splits = prefill_splits(a, units);
-  if (units * splits * (2 * kTileRows / kJoinRows) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  // (some 2^25 by the limits of the descriptor; with splits at most one for each SM)
   const dim3 grid(static_cast<unsigned>(units * splits));
   if (int rc = launch_pdl(kernel, grid, dim3(kThreads), Cfg<D>::kSmem, st, a, splits)) return rc;
   if (splits == 1) return MOE_OK;

@@ -3,6 +3,7 @@
 The tolerance of attention is that of test_gpu_kv (a softmax weight off by at most 2^-11
 + 2^-14, the output's rounding, 1e-7)."""
 import math
+import random
 
 import pytest
 import torch
@@ -148,6 +149,39 @@ def test_sliced_page_table(lib):
 def test_attention_many_sequences_under_a_window(lib, new, window):
     total = [new + (37 * i) % 191 for i in range(150)]
     check_attention(lib, total, [new if i % 7 else 0 for i in range(150)], 2, 8, 64, 16, window=window)
+
+
+def test_attention_as_many_sequences_as_the_limits_allow(lib):
+    # 2^20 sequences of 64 kv heads, nearly all without new tokens
+    batch, heads, dim, page = 1 << 20, 64, 64, 16
+    n, t = 34, 40
+    c = Cache([t], [n], heads, dim, page)
+    at = batch - 7                                       # the one that has some
+    table = torch.full((batch, 3), -1, dtype=torch.int32, device="cuda")
+    table[at] = c.table[0, :3]
+    cu, kv_len = torch.zeros(batch + 1, dtype=torch.int32, device="cuda"), torch.zeros(batch, dtype=torch.int32, device="cuda")
+    cu[at + 1:], kv_len[at] = n, t
+    q = torch.randn((n, heads, dim), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    out = torch.full_like(q, 7.0)
+    args = (q, c.k, c.v, c.ks, c.vs, table, cu, kv_len, out)
+    err = lib.new_error_word()
+    lib.moe_kv_attention(*args, lib.alloc_kv_workspace(lib.make_kv_attention_desc(*args, 0.125)), 0.125, err=err)
+    assert lib.moe_read_device_status(err) == (lib.MOE_OK, 0)
+    ref, mag, _ = plain_attention(c, q, 0.125, 0, 0.0, False)
+    assert ((out.double() - ref).abs() <= U * (mag + ref.abs()) + 2.0 ** -8 * ref.abs() + 1e-7).all()
+
+
+@pytest.mark.parametrize("heads,q_heads", [(1, 1), (2, 10), (1, 16)])
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_attention_mixed_batches(lib, heads, q_heads, seed):
+    # steps, drafts, chunks and idle sequences in any order: every sequence's rows are found
+    r = random.Random(seed)
+    new = [r.choice([0, 1, 1, 1, 2, 5, r.randint(6, 40), r.randint(30, 300)]) for _ in range(r.choice([3, 40, 90]))]
+    check_attention(lib, [n + r.randint(0, 90) for n in new], new, heads, q_heads, 64, 16, max_q=r.choice([0, None, 5000]))
+
+
+def test_attention_max_q_far_above_the_rows(lib):
+    check_attention(lib, [50, 7, 3], [1, 1, 0], 1, 4, 64, 16, max_q=1000)
 
 
 def test_append_wide_groups(lib):
