@@ -18,7 +18,7 @@
 // Measured: 256 single tokens with 32 query and 8 kv heads 5.4 us on the GPU; 32768
 // prompt tokens with 64 and 8 heads 210 us, 6.1 TB/s (91% of a copy's rate), of which
 // the queries 154 at the copy's rate and the pages 56; ragged chunks of 64-dimension
-// heads, f16, token-major pages 44 us, 3.7 TB/s (4 KB a head and CTA, a barrier each).
+// heads, f16, token-major pages 44 us by graph replay, 3.7 TB/s (4 KB a head and CTA, a barrier each).
 //
 // Query rows need no maximum: further CTAs of the tokens kernel's launch rotate them,
 // and for prompts a kernel of its own, with the registers that suit it.

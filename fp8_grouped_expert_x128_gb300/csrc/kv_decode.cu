@@ -18,11 +18,12 @@
 // the weight: w = exp2(s + log2 s_V - m), the sum takes w / s_V; m follows the largest
 // score, and the size of s_V both ways.
 //
-// A step is some 300 instructions with little parallelism inside a warp, so three or
-// four CTAs share an SM (two: 253 us where three take 191).  Measured: 64 sequences of
-// 2000 to 16400 tokens, 8 kv heads, 4 rows each, 191 us, 6.2 TB/s (92% of a copy's);
-// four of 131072 tokens, 167 us (95%); one of 1010 tokens, 11 us: four dependent loads,
-// the join's release and acquire, and its loads, about a microsecond each.
+// A step is some 420 instructions (560 with two groups of rows) with little parallelism
+// inside a warp, so three or four CTAs share an SM (two: 253 us where three took 191).
+// Measured by graph replay: 64 sequences of 2000 to 16400 tokens, 8 kv heads, 4 rows
+// each, 193 us, 6.2 TB/s (92% of a copy's); four of 131072 tokens, 166 us (96%); one of
+// 1010 tokens, 11 us: four dependent loads, the join's release and acquire, and its
+// loads, about a microsecond each.
 #include "kv_attention.cuh"
 
 namespace moe {

@@ -15,10 +15,11 @@
 // as in the decode kernel.  Where there are fewer 256-row units than SMs, the keys are
 // split as well, and kv_prefill_join_kernel adds the parts.
 //
-// Measured: an 8192-token prompt with 64 / 8 heads of 128 in 0.96 ms, 1.15 PFLOP/s,
-// 58% of the bf16 rate that a large matrix product has; 1.50 ms under a cap.  No single
-// role binds: with one taken out (widening, softmax, MMAs) it is 10 to 20% less, with all
-// three 320 us; 60% of the issue slots, 22% of the exponentials' rate.
+// Measured by graph replay: an 8192-token prompt with 64 / 8 heads of 128 in 0.965 ms,
+// 1.14 PFLOP/s, 58% of the bf16 rate that a large matrix product has; 1.50 ms under a
+// cap, 3.1 under one past 64.  The MMAs alone take 0.82 ms as they are issued; with one
+// role taken out (widening, softmax, MMAs) the whole is 10 to 20% less, with all three
+// 0.32 ms; 62% of the issue slots, 23% of the exponentials' rate.
 // 128-key steps with one S buffer take the same (their MMAs are quicker, N = 64 takes
 // as long as N = 128, but a softmax waits for its S), and so do four warpgroups of
 // softmax; one that takes weights before the maximum of the block is known, 20% more.
@@ -40,7 +41,7 @@ constexpr uint32_t kTmemCols = 512;
 // from where it seldom has to move, and is put kHead below after kSettle steps, when a
 // maximum seldom rises by much; until then there are 4096 keys at most, whose rounding to
 // multiples of 2^-26 of the largest weight amounts to 2^-15.  (kHead from the start: 1006
-// us for an 8192-token prompt instead of 972; never, which is not right for long contexts
+// us for an 8192-token prompt instead of 968; never, which is not right for long contexts
 // under a dominant key: 959.)
 constexpr float kFirstHead = 2.0f;
 constexpr int kSettle = 64;
