@@ -98,3 +98,32 @@ def test_a_workspace_that_only_looks_large_is_refused(moe, monkeypatch):  # noqa
     with pytest.raises(ValueError, match="workspace"):
         calls(moe, 0, one)[1]()
     assert library.through == 0
+
+
+def test_kernels_for_large_caps_keep_the_register_split(moe, tmp_path):  # noqa: F811
+    """They hand registers between warpgroups like those without: 96 a thread at launch (the
+    launch refuses anything else), next to no spills."""
+    import os
+    import re
+    import shutil
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    src = os.path.join(root, "fp8_grouped_expert_x128_gb300", "csrc", "kv_prefill.cu")
+    r = subprocess.run([nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
+                        "-I", os.path.join(root, "include"), "-Xptxas", "-v", "-c", src, "-o", str(tmp_path / "p.o")],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    current, seen = "", 0
+    for line in r.stderr.splitlines():
+        m = re.search(r"Compiling entry function '(\S+)'", line)
+        current = m.group(1) if m else current
+        if "kv_prefill_bend_kernel" not in current:
+            continue
+        m = re.search(r"(\d+) bytes spill stores", line)
+        assert m is None or int(m.group(1)) <= 64, line
+        m = re.search(r"Used (\d+) registers", line)
+        if m:
+            assert int(m.group(1)) == 96, current
+            seen += 1
+    assert seen == 4            # two types x two dimensions
