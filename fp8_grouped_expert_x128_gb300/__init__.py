@@ -47,9 +47,12 @@ MOE_GEMM_EARLY_WEIGHTS = 0x20
 MOE_GEMM_DEBUG_STALL = 0x100
 MOE_QUANT_UE8M0 = 0x1
 MOE_COMBINE_ACCUMULATE = 0x1
-MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1
+MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32 = 0, 1, 2
 MOE_KV_INTERLEAVED = 0x1
 MOE_KV_FULL = 0x1
+MOE_ROUTE_SOFTMAX = 0x1
+MOE_ROUTE_RENORM = 0x2
+MOE_ROUTE_GROUP_PAIR = 0x4
 
 EXPORTED = [
     "moe_status_string", "moe_version", "moe_read_device_status", "moe_quant_fp8",
@@ -59,6 +62,7 @@ EXPORTED = [
     "moe_ue8m0_scale", "moe_quant_weight_fp8_ue8m0", "moe_ue8m0_act_words", "moe_ue8m0_weight_words",
     "moe_pack_ue8m0_act", "moe_pack_ue8m0_weight", "moe_gemm_fp8_contig_ue8m0", "moe_gemm_fp8_masked_ue8m0",
     "moe_kv_append", "moe_kv_attention", "moe_kv_attention_workspace_size",
+    "moe_gate", "moe_route", "moe_kv_pages", "moe_verify_drafts",
 ]
 
 _P = ctypes.c_void_p
@@ -99,6 +103,37 @@ class moe_kv_attention_desc(ctypes.Structure):
         ("q_token_ld", _I64), ("q_head_ld", _I64), ("o_token_ld", _I64), ("o_head_ld", _I64),
         ("sm_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("q_heads", _I32), ("max_q", _I32), ("window", _I32),
         ("flags", _I32),
+    ]
+
+
+class moe_gate_desc(ctypes.Structure):
+    _fields_ = [
+        ("x", _P), ("w", _P), ("logits", _P), ("err", _P), ("T", _I64), ("x_ld", _I64), ("w_ld", _I64), ("logits_ld", _I64),
+        ("E", _I32), ("H", _I32), ("dtype", _I32), ("flags", _I32),
+    ]
+
+
+class moe_route_desc(ctypes.Structure):
+    _fields_ = [
+        ("logits", _P), ("bias", _P), ("n_tokens", _P), ("topk_ids", _P), ("topk_w", _P), ("T", _I64), ("logits_ld", _I64),
+        ("ids_ld", _I64), ("w_ld", _I64), ("scale", ctypes.c_float), ("E", _I32), ("k", _I32), ("n_group", _I32),
+        ("topk_group", _I32), ("dtype", _I32), ("flags", _I32),
+    ]
+
+
+class moe_kv_pages_desc(ctypes.Structure):
+    _fields_ = [
+        ("kv_old", _P), ("kv_keep", _P), ("n_new", _P), ("page_table", _P), ("free_list", _P), ("free_count", _P), ("kv_len", _P),
+        ("cu_new", _P), ("free_count_out", _P), ("seqs", _P), ("positions", _P), ("slots", _P), ("err", _P), ("table_ld", _I64),
+        ("free_capacity", _I64), ("rows", _I64), ("batch", _I32), ("max_pages", _I32), ("page_size", _I32), ("flags", _I32),
+    ]
+
+
+class moe_verify_desc(ctypes.Structure):
+    _fields_ = [
+        ("probs", _P), ("draft_probs", _P), ("tokens", _P), ("cu_new", _P), ("n_draft", _P), ("u_accept", _P), ("u_sample", _P),
+        ("kv_len", _P), ("accepted", _P), ("out_tokens", _P), ("kv_keep", _P), ("err", _P), ("T", _I64), ("vocab", _I64),
+        ("p_ld", _I64), ("q_ld", _I64), ("out_ld", _I64), ("batch", _I32), ("max_out", _I32), ("dtype", _I32), ("flags", _I32),
     ]
 
 
@@ -145,6 +180,8 @@ _sig("moe_ffn_noalloc_capacity", ctypes.c_size_t, [])
 _sig("moe_kv_append", ctypes.c_int, [_P, _P])
 _sig("moe_kv_attention_workspace_size", ctypes.c_size_t, [ctypes.POINTER(moe_kv_attention_desc)])
 _sig("moe_kv_attention", ctypes.c_int, [_P, _P, ctypes.c_size_t, _P])
+for _name in ("moe_gate", "moe_route", "moe_kv_pages", "moe_verify_drafts"):
+    _sig(_name, ctypes.c_int, [_P, _P])
 
 
 class MoeError(RuntimeError):
@@ -620,3 +657,146 @@ def alloc_kv_workspace(desc: moe_kv_attention_desc, device=None) -> torch.Tensor
     if n == 0:
         raise MoeError(MOE_ERR_INVALID_ARG, "moe_kv_attention_workspace_size")
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+# ---------------------------------------------------------------- what a serving step decides
+_STEP_TYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
+_gate_pack = struct.Struct("@4Q4q4i").pack
+_route_pack = struct.Struct("@5Q4qf6i4x").pack
+_kv_pages_pack = struct.Struct("@13Q3q4i").pack
+_verify_pack = struct.Struct("@12Q5q4i").pack
+
+
+def _here(device, name):
+    """The library launches on the current GPU, so that is where a call's tensors have to be."""
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if torch.cuda.current_device() != device:
+        raise ValueError(f"{name}: on GPU {device}, but GPU {torch.cuda.current_device()} is current (torch.cuda.set_device)")
+
+
+def _rows2d(t, name, shape, dtype, device):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    ld, one = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or (one != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: expected {dtype} {list(shape)} on GPU {device} with contiguous rows, got {t.dtype} "
+                         f"{list(t.shape)}, strides {list(t.stride())}, GPU {t.get_device()}")
+    return ld if shape[0] > 1 else shape[1]              # one row's stride is never used, and may be anything
+
+
+def _flat(t, name, n, dtype, device):
+    """Address of a contiguous 1-D tensor of n elements, 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} [{n}] on GPU {device}, got {t.dtype} {list(t.shape)}, strides "
+                         f"{list(t.stride())}, GPU {t.get_device()}")
+    return t.data_ptr()
+
+
+def _step_err(err, device):
+    return 0 if err is None else _flat(err, "err", 1, torch.int32, device)
+
+
+def moe_gate(x, w, logits, err=None, stream=None):
+    """Router logits: x [T, H] and w [E, H] (both bf16 or both f16, contiguous rows) ->
+    logits fp32 [T, E], summed in fp32.  See moe_fp8.h for the limits."""
+    device, dtype = x.get_device(), x.dtype
+    _here(device, "x")
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"x: expected bfloat16 or float16, got {dtype}")
+    T, H = x.shape
+    E = w.shape[0]
+    d = _gate_pack(x.data_ptr(), w.data_ptr(), logits.data_ptr(), _step_err(err, device), T, _rows2d(x, "x", (T, H), dtype, device),
+                   _rows2d(w, "w", (E, H), dtype, device), _rows2d(logits, "logits", (T, E), torch.float32, device), E, H,
+                   _STEP_TYPES[dtype], 0)
+    rc = _lib.moe_gate(d, _stream_of(device, stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_gate")
+    return logits
+
+
+def moe_route(logits, topk_ids, topk_w, bias=None, n_group=1, topk_group=1, scale=1.0, flags=0, n_tokens=None, stream=None):
+    """Routing to experts: logits [T, E] (bf16, f16 or fp32) -> topk_ids int32 [T, k] and
+    topk_w fp32 [T, k], as moe_permute and moe_ffn take them; see moe_fp8.h for the rule.
+    bias: fp32 [E] added to the scores for the ranking alone; n_tokens: int32 [1], rows at
+    and past it get id -1; flags: MOE_ROUTE_SOFTMAX (else sigmoid scores),
+    MOE_ROUTE_RENORM, MOE_ROUTE_GROUP_PAIR."""
+    device, dtype = logits.get_device(), logits.dtype
+    _here(device, "logits")
+    if dtype not in _STEP_TYPES:
+        raise ValueError(f"logits: expected bfloat16, float16 or float32, got {dtype}")
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    d = _route_pack(logits.data_ptr(), _flat(bias, "bias", E, torch.float32, device), _flat(n_tokens, "n_tokens", 1, torch.int32, device),
+                    topk_ids.data_ptr(), topk_w.data_ptr(), T, _rows2d(logits, "logits", (T, E), dtype, device),
+                    _rows2d(topk_ids, "topk_ids", (T, k), torch.int32, device), _rows2d(topk_w, "topk_w", (T, k), torch.float32, device),
+                    scale, E, k, n_group, topk_group, _STEP_TYPES[dtype], flags)
+    rc = _lib.moe_route(d, _stream_of(device, stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_route")
+    return topk_ids, topk_w
+
+
+def moe_kv_pages(kv_old, n_new, page_table, free_list, free_count, page_size, kv_len, cu_new, free_count_out, kv_keep=None, seqs=None,
+                 positions=None, slots=None, err=None, stream=None):
+    """The paged cache's bookkeeping for a step; see moe_fp8.h for the rule.  Sequence b
+    had kv_old[b] tokens, keeps kv_keep[b] of them (None: all) and gains n_new[b]: writes
+    kv_len [batch], cu_new [batch + 1], page_table [batch, max_pages], the free list (a
+    stack of free_count[0] pages, of free_count_out[0] afterwards) and, where given, each
+    new row's sequence, position (int32 [rows]) and slot page * page_size + offset (int64
+    [rows]).  kv_len and kv_old, and the two counts, are different tensors."""
+    device = kv_old.get_device()
+    _here(device, "kv_old")
+    i32 = torch.int32
+    batch, max_pages = page_table.shape
+    rows = 0
+    for t in (seqs, positions, slots):
+        if t is not None:
+            rows = t.shape[0]
+            break
+    else:
+        rows = 1 << 30                     # no row tensors: nothing limits the rows
+    d = _kv_pages_pack(_flat(kv_old, "kv_old", batch, i32, device), _flat(kv_keep, "kv_keep", batch, i32, device),
+                       _flat(n_new, "n_new", batch, i32, device), page_table.data_ptr(),
+                       _flat(free_list, "free_list", free_list.shape[0], i32, device), _flat(free_count, "free_count", 1, i32, device),
+                       _flat(kv_len, "kv_len", batch, i32, device), _flat(cu_new, "cu_new", batch + 1, i32, device),
+                       _flat(free_count_out, "free_count_out", 1, i32, device), _flat(seqs, "seqs", rows, i32, device),
+                       _flat(positions, "positions", rows, i32, device), _flat(slots, "slots", rows, torch.int64, device),
+                       _step_err(err, device), _rows2d(page_table, "page_table", (batch, max_pages), i32, device), free_list.shape[0],
+                       rows, batch, max_pages, page_size, 0)
+    rc = _lib.moe_kv_pages(d, _stream_of(device, stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_kv_pages")
+
+
+def moe_verify_drafts(probs, tokens, cu_new, u_accept, u_sample, accepted, out_tokens, draft_probs=None, n_draft=None, kv_len=None,
+                      kv_keep=None, err=None, stream=None):
+    """Drafted tokens against the target's probabilities, from given random numbers; see
+    moe_fp8.h for the rule.  probs, draft_probs [T, vocab] (bf16, f16 or fp32, one type),
+    tokens int32 [T] and u_accept fp32 [T] by the step's rows (cu_new [batch + 1]),
+    u_sample fp32 [batch] -> accepted int32 [batch], out_tokens int32 [batch, max_out]
+    (the taken drafts, the token behind them, -1) and kv_keep int32 [batch] =
+    kv_len - rejected drafts.  n_draft int32 [batch]: drafts among a sequence's rows
+    (None: all but the first)."""
+    device, dtype = probs.get_device(), probs.dtype
+    _here(device, "probs")
+    if dtype not in _STEP_TYPES:
+        raise ValueError(f"probs: expected bfloat16, float16 or float32, got {dtype}")
+    i32, f32 = torch.int32, torch.float32
+    T, vocab = probs.shape
+    batch, max_out = out_tokens.shape
+    q_ptr = q_ld = 0
+    if draft_probs is not None:
+        q_ptr, q_ld = draft_probs.data_ptr(), _rows2d(draft_probs, "draft_probs", (T, vocab), dtype, device)
+    d = _verify_pack(probs.data_ptr(), q_ptr, _flat(tokens, "tokens", T, i32, device), _flat(cu_new, "cu_new", batch + 1, i32, device),
+                     _flat(n_draft, "n_draft", batch, i32, device), _flat(u_accept, "u_accept", T, f32, device),
+                     _flat(u_sample, "u_sample", batch, f32, device), _flat(kv_len, "kv_len", batch, i32, device),
+                     _flat(accepted, "accepted", batch, i32, device), out_tokens.data_ptr(),
+                     _flat(kv_keep, "kv_keep", batch, i32, device), _step_err(err, device), T, vocab,
+                     _rows2d(probs, "probs", (T, vocab), dtype, device), q_ld,
+                     _rows2d(out_tokens, "out_tokens", (batch, max_out), i32, device), batch, max_out, _STEP_TYPES[dtype], 0)
+    rc = _lib.moe_verify_drafts(d, _stream_of(device, stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_verify_drafts")
+    return accepted, out_tokens

@@ -1,0 +1,282 @@
+// The paged cache's bookkeeping for a step: lengths, page tables, the free list
+// and the rows' positions and slots from what sequences keep and gain
+// (moe_kv_pages).
+//
+// Every CTA scans the sequences (at most 8192) by itself, so one launch does it
+// all, and then serves its share of the rows and of the pages that move.  No CTA
+// reads what another writes: pages that are taken come from entries of the list
+// below its old length, or straight from the table of a sequence that shrinks;
+// what is written are table entries of sequences that grow and list entries past
+// the old length.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kPagesThreads = 512;
+constexpr int kPagesMaxBatch = 8192;
+
+struct PagesArgs {
+  moe_kv_pages_desc d;
+  int32_t shift;   // log2 page_size
+};
+
+struct Sums {      // over sequences: new tokens, pages taken, pages given back
+  int64_t n, take, back;
+  __device__ __forceinline__ Sums operator+(const Sums& o) const { return {n + o.n, take + o.take, back + o.back}; }
+};
+
+// Exclusive sums over the block's threads; `total` gets the sum of all.
+__device__ Sums block_scan(Sums v, Sums* part, Sums& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Sums x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sums y{__shfl_up_sync(0xffffffffu, x.n, o), __shfl_up_sync(0xffffffffu, x.take, o), __shfl_up_sync(0xffffffffu, x.back, o)};
+    if (lane >= o) x = x + y;
+  }
+  __syncthreads();            // `part` of an earlier call has been read
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  Sums before{0, 0, 0};
+  total = Sums{0, 0, 0};
+  for (int w = 0; w < kPagesThreads / 32; ++w) {
+    const Sums y = part[w];
+    if (w < warp) before = before + y;
+    total = total + y;
+  }
+  return {before.n + x.n - v.n, before.take + x.take - v.take, before.back + x.back - v.back};
+}
+
+// The last b in [0, n) with first[b] <= x (first is not decreasing, first[0] <= x).
+__device__ __forceinline__ int find_last(const int32_t* first, int n, int32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const __grid_constant__ PagesArgs a) {
+  extern __shared__ int32_t pages_smem[];
+  __shared__ Sums part[kPagesThreads / 32];
+  const moe_kv_pages_desc& d = a.d;
+  const int B = d.batch;
+  // by sequence: first row, first page taken, first page given back (a prefix sum each,
+  // one entry more than sequences), tokens kept, pages held and pages in the end
+  int32_t* row0 = pages_smem;
+  int32_t* take0 = row0 + B + 1;
+  int32_t* back0 = take0 + B + 1;
+  int32_t* keep_of = back0 + B + 1;
+  int32_t* held_of = keep_of + B;
+  int32_t* need_of = held_of + B;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  const int per = (B + kPagesThreads - 1) / kPagesThreads;
+  const int b0 = min(static_cast<int>(threadIdx.x) * per, B), b1 = min(b0 + per, B);
+  const int64_t most = static_cast<int64_t>(d.max_pages) << a.shift;
+  const int32_t f = *d.free_count;
+  const bool list_ok = f >= 0 && f <= d.free_capacity;
+  auto pages = [&](int64_t tokens) { return static_cast<int32_t>((tokens + d.page_size - 1) >> a.shift); };
+
+  struct Seq {
+    int32_t old, keep, n, held;
+    int64_t want;
+    bool bad, wide;
+  };
+  auto load = [&](int b) {
+    Seq s;
+    s.old = d.kv_old[b];
+    s.keep = d.kv_keep ? d.kv_keep[b] : s.old;
+    s.n = d.n_new[b];
+    s.bad = !list_ok || s.old < 0 || s.n < 0 || s.old > most || s.keep < 0 || s.keep > s.old;
+    s.held = s.bad ? 0 : pages(s.old);
+    s.want = static_cast<int64_t>(s.keep) + s.n;
+    s.wide = !s.bad && s.want > most;
+    return s;
+  };
+  // what a sequence asks for
+  auto asked = [&](const Seq& s) {
+    Sums v{0, 0, 0};
+    if (s.bad || s.wide) return v;
+    const int32_t need = pages(s.want);
+    v.n = s.n;
+    v.take = max(0, need - s.held);
+    v.back = max(0, s.held - need);
+    return v;
+  };
+  int32_t bits = 0;
+  Sums mine{0, 0, 0}, total;
+  bool refused = false;
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = load(b);
+    mine = mine + asked(s);
+    refused |= s.wide;
+    if (s.bad) bits |= MOE_DEV_BAD_INDEX;
+    if (s.wide) bits |= MOE_DEV_OVERFLOW;
+  }
+  Sums before = block_scan(mine, part, total);
+  const int64_t room = f + total.back;
+  const bool all = !__syncthreads_or(refused) && total.n <= d.rows && total.take <= room;
+  // which sequences get what they ask for (bit i: the thread's i-th; at most 16 of them)
+  uint32_t grants = 0xffffffffu;
+  if (!all) {
+    // by rows first, then by pages among those that pass
+    int64_t n = before.n;
+    uint32_t fits = 0;
+    Sums asks{0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load(b);
+      const Sums v = asked(s);
+      n += v.n;
+      if (s.bad || s.wide || (v.n > 0 && n > d.rows)) continue;
+      fits |= 1u << (b - b0);
+      asks.take += v.take;
+    }
+    Sums sum;
+    int64_t take = block_scan(asks, part, sum).take;
+    grants = 0;
+    mine = Sums{0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load(b);
+      Sums v = asked(s);
+      bool ok = (fits >> (b - b0)) & 1;
+      if (ok) {
+        take += v.take;
+        ok = v.take == 0 || take <= room;
+      }
+      if (ok) {
+        grants |= 1u << (b - b0);
+      } else if (!s.bad) {
+        bits |= MOE_DEV_OVERFLOW;
+        v = Sums{0, 0, s.held - pages(s.keep)};
+      }
+      mine = mine + v;
+    }
+    before = block_scan(mine, part, total);
+  }
+  // a list that would not hold what comes back: nothing moves
+  const bool whole = list_ok && f + total.back <= d.free_capacity;
+  if (!whole) {
+    bits |= MOE_DEV_BAD_INDEX;
+    before = total = Sums{0, 0, 0};
+  }
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = load(b);
+    const bool stays = s.bad || !whole, ok = !stays && ((grants >> (b - b0)) & 1);
+    const int32_t len = stays ? s.old : ok ? static_cast<int32_t>(s.want) : s.keep;
+    const int32_t held = stays ? 0 : s.held, need = stays ? 0 : pages(len);
+    row0[b] = static_cast<int32_t>(before.n);
+    take0[b] = static_cast<int32_t>(before.take);
+    back0[b] = static_cast<int32_t>(before.back);
+    keep_of[b] = s.keep;
+    held_of[b] = held;
+    need_of[b] = need;
+    if (blockIdx.x == 0) {
+      d.cu_new[b] = row0[b];
+      d.kv_len[b] = len;
+    }
+    before.n += ok ? s.n : 0;
+    before.take += max(0, need - held);
+    before.back += max(0, held - need);
+  }
+  const int32_t rows = static_cast<int32_t>(total.n), taken = static_cast<int32_t>(total.take), back = static_cast<int32_t>(total.back);
+  const int32_t left = f + back - taken;
+  if (threadIdx.x == 0) {
+    row0[B] = rows;
+    take0[B] = taken;
+    back0[B] = back;
+    if (blockIdx.x == 0) {
+      d.cu_new[B] = rows;
+      *d.free_count_out = whole ? left : f;
+    }
+  }
+  if (blockIdx.x == 0 && bits) set_err(d.err, bits);
+  __syncthreads();
+
+  const int32_t step = static_cast<int32_t>(gridDim.x) * kPagesThreads;
+  const int32_t first = static_cast<int32_t>(blockIdx.x) * kPagesThreads + threadIdx.x;
+  auto entry = [&](int b, int32_t j) { return d.page_table + b * d.table_ld + j; };
+  // the i-th page given back, and the i-th page taken
+  auto given = [&](int32_t i) {
+    const int b = find_last(back0, B, i);
+    return *entry(b, need_of[b] + i - back0[b]);
+  };
+  auto source = [&](int32_t i) {
+    const int32_t at = f + back - 1 - i;
+    return at < f ? d.free_list[at] : given(at - f);
+  };
+  for (int64_t i = first; i < taken; i += step) {
+    const int b = find_last(take0, B, static_cast<int32_t>(i));
+    *entry(b, held_of[b] + static_cast<int32_t>(i) - take0[b]) = source(static_cast<int32_t>(i));
+  }
+  for (int64_t i = first; i < static_cast<int64_t>(left) - f; i += step) d.free_list[f + i] = given(static_cast<int32_t>(i));
+  if (d.seqs == nullptr && d.positions == nullptr && d.slots == nullptr) return;
+  for (int64_t r = first; r < d.rows; r += step) {
+    int32_t b = -1, pos = -1;
+    int64_t slot = -1;
+    if (r < rows) {
+      b = find_last(row0, B, static_cast<int32_t>(r));
+      pos = keep_of[b] + static_cast<int32_t>(r) - row0[b];
+      if (d.slots) {
+        const int32_t j = pos >> a.shift;
+        const int32_t page = j < held_of[b] ? *entry(b, j) : source(take0[b] + j - held_of[b]);
+        slot = (static_cast<int64_t>(page) << a.shift) + (pos & (d.page_size - 1));
+      }
+    }
+    if (d.seqs) d.seqs[r] = b;
+    if (d.positions) d.positions[r] = pos;
+    if (d.slots) d.slots[r] = slot;
+  }
+}
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+inline bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_kv_pages(const moe_kv_pages_desc* d, void* stream) {
+  MOE_CHECK_ARG(d != nullptr && d->flags == 0);
+  MOE_CHECK_ARG(d->batch >= 0 && d->max_pages >= 0 && d->rows >= 0 && d->free_capacity >= 0 && d->table_ld >= d->max_pages);
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128) return MOE_ERR_UNSUPPORTED;
+  if (d->batch > kPagesMaxBatch || d->max_pages > (INT32_MAX - 65535) / d->page_size || d->rows > (1 << 30) ||
+      d->free_capacity > (1 << 30) || d->table_ld > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
+  MOE_CHECK_ARG(d->free_count && d->free_count_out && d->cu_new && (d->free_list || d->free_capacity == 0));
+  MOE_CHECK_ARG(d->batch == 0 || (d->kv_old && d->n_new && d->kv_len && (d->page_table || d->max_pages == 0)));
+  const int64_t b4 = 4ll * d->batch;
+  const Range in[4] = {{d->kv_old, b4}, {d->kv_keep, b4}, {d->n_new, b4}, {d->free_count, 4}};
+  const Range out[8] = {{d->kv_len, b4}, {d->cu_new, b4 + 4}, {d->free_count_out, 4},
+                        {d->page_table, d->batch ? 4 * ((d->batch - 1) * d->table_ld + d->max_pages) : 0},
+                        {d->free_list, 4 * d->free_capacity}, {d->seqs, 4 * d->rows}, {d->positions, 4 * d->rows}, {d->slots, 8 * d->rows}};
+  for (int i = 0; i < 8; ++i) {
+    const uintptr_t unit = i == 7 ? 7 : 3;
+    MOE_CHECK_ARG((reinterpret_cast<uintptr_t>(out[i].p) & unit) == 0);
+    for (const Range& r : in) MOE_CHECK_ARG(!overlap(out[i], r) && (reinterpret_cast<uintptr_t>(r.p) & 3) == 0);
+    for (int j = 0; j < i; ++j) MOE_CHECK_ARG(!overlap(out[i], out[j]));
+  }
+  if (int rc = check_device()) return rc;
+  PagesArgs a{*d, 0};
+  while ((1 << a.shift) < d->page_size) ++a.shift;
+  // a CTA for 4096 rows, and for 16 sequences, whose pages may all go back
+  const int64_t told = d->seqs || d->positions || d->slots ? d->rows : 0;
+  int64_t ctas = std::max<int64_t>((told + 4095) / 4096, (d->batch + 15) / 16);
+  ctas = std::min<int64_t>(std::max<int64_t>(ctas, 1), num_sms());
+  const size_t smem = sizeof(int32_t) * (6 * static_cast<size_t>(d->batch) + 3);
+  if (smem > 48 * 1024)
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kv_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (6 * kPagesMaxBatch + 3)));
+  return launch_pdl(kv_pages_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPagesThreads), smem, as_stream(stream), a);
+}

@@ -593,6 +593,203 @@ typedef struct moe_kv_attention_desc {
 size_t moe_kv_attention_workspace_size(const moe_kv_attention_desc *desc);
 int moe_kv_attention(const moe_kv_attention_desc *desc, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * What a serving step decides before and between its products: which experts a
+ * token goes to, which pages a sequence owns, which drafted tokens stand.  Each is
+ * one kernel on `stream` that reads lengths and counts on the device only, so a
+ * captured step runs without the host.
+ *
+ * moe_gate -- the router's logits.
+ *   logits[t, e] = sum_h x[t, h] * w[e, h]          (fp32)
+ * x: device [T, H], w: device [E, H], both of one type (MOE_DTYPE_BF16 or
+ * MOE_DTYPE_F16); row strides in elements, multiples of 8, at least H, below 2^31;
+ * logits: device fp32 [T, E], row stride at least E.  Products are exact; they are summed on the tensor cores over 128 columns at
+ * a time, and these sums in fp32, rounded to nearest.  Results repeat bit for bit.
+ * Limits: H a multiple of 8, up to 2^20; E up to 1024; T up to 2^24.  T may be 0
+ * (nothing is launched).  logits must not overlap x or w.
+ */
+#define MOE_DTYPE_F32 2
+
+typedef struct moe_gate_desc {
+  const void *x;
+  const void *w;
+  float *logits;
+  int32_t *err;               /* device error word (may be NULL)            */
+  int64_t T, x_ld, w_ld, logits_ld;                              /* elements */
+  int32_t E, H, dtype;
+  int32_t flags;              /* 0                                          */
+} moe_gate_desc;
+
+int moe_gate(const moe_gate_desc *desc, void *stream);
+
+/*
+ * moe_route -- logits to experts and their weights, as moe_ffn takes them.
+ * For a token with logits z_e (bf16, f16 or fp32), e = 0 .. E - 1:
+ *   open     experts whose logit is not NaN or -inf (+inf counts as the largest fp32)
+ *   score_e  1 / (1 + exp(-z_e)), or with MOE_ROUTE_SOFTMAX exp(z_e) / sum exp(z) over
+ *            the open experts
+ *   value_e  score_e + bias_e; without a bias the experts are ranked by z_e itself.
+ *            An expert whose bias is NaN or -inf is not open.
+ *   groups   with n_group > 1, experts e in [g * E / n_group, (g + 1) * E / n_group)
+ *            form group g; it counts as its largest open value, or with
+ *            MOE_ROUTE_GROUP_PAIR as the sum of its two largest (of scores where there
+ *            is no bias; of one, if only one is open).  The topk_group largest groups
+ *            stay open; one without open experts comes last.
+ *   topk_ids[t, 0..k)  the open experts of largest value, falling
+ *   topk_w[t, j]       scale * score of topk_ids[t, j], with MOE_ROUTE_RENORM divided
+ *                      by the sum of the k scores first
+ * Among equal values (and groups) the lowest number comes first.  Values are compared
+ * as 64-bit arithmetic has them: what fp32 cannot tell apart is computed again.
+ * Where fewer than k experts are open, the remaining entries get id -1 and weight 0
+ * (moe_permute and moe_ffn skip these), and so do all entries of rows at and past
+ * n_tokens[0], the rows behind a padded batch (n_tokens may be NULL; a negative
+ * number counts as 0).
+ * logits: device [T, E] (type dtype: MOE_DTYPE_BF16, _F16 or _F32); bias: device fp32
+ * [E] or NULL; topk_ids: device int32, topk_w: device fp32 [T, k]; row strides in
+ * elements, at least E and k.  scale finite.
+ * Limits: E and k as moe_permute (1024 and 32; k up to topk_group * E / n_group),
+ * n_group up to 32, a divisor of E; T up to 2^24, 0 launches nothing.  logits aligned
+ * to its elements.
+ */
+#define MOE_ROUTE_SOFTMAX 0x1
+#define MOE_ROUTE_RENORM 0x2
+#define MOE_ROUTE_GROUP_PAIR 0x4
+
+typedef struct moe_route_desc {
+  const void *logits;
+  const float *bias;          /* or NULL                                    */
+  const int32_t *n_tokens;    /* device int32 [1] or NULL                   */
+  int32_t *topk_ids;
+  float *topk_w;
+  int64_t T, logits_ld, ids_ld, w_ld;                            /* elements */
+  float scale;
+  int32_t E, k, n_group, topk_group, dtype, flags;
+} moe_route_desc;
+
+int moe_route(const moe_route_desc *desc, void *stream);
+
+/*
+ * moe_kv_pages -- the paged cache's bookkeeping for a step: sequences lose tokens
+ * (rejected drafts, ended requests), gain this step's, and the pages follow.
+ * Sequence b had kv_old[b] tokens, keeps the first kv_keep[b] of them (all of them
+ * where kv_keep is NULL) and gains n_new[b]:
+ *   want = kv_keep[b] + n_new[b],  held = ceil(kv_old[b] / page_size),
+ *   need = ceil(want / page_size)
+ *   kv_len[b] = want; cu_new[b + 1] - cu_new[b] = n_new[b], cu_new[0] = 0
+ *   need < held: pages page_table[b, need .. held) go back to the free list
+ *   need > held: page_table[b, held .. need) are set to pages from its end
+ * The free list holds free_count[0] pages.  All pages that go back are put behind its
+ * last one, in the order of (sequence, page); then the pages that are needed are
+ * taken from the end one after another in the same order (one that goes back may be
+ * taken again at once), and what is left is free_count_out[0] long.  Entries of the
+ * list past that, and of the table past a sequence's pages, have no meaning.
+ * For row r of the step's token tensors (r < rows), where given:
+ *   seqs[r] = b, positions[r] = kv_keep[b] + r - cu_new[b],
+ *   slots[r] = page_table[b, p / page_size] * page_size + p % page_size, p = positions[r]
+ * for cu_new[b] <= r < cu_new[b + 1], and -1 behind the last sequence's.
+ * So kv_len, cu_new and page_table are what moe_kv_append and moe_kv_attention take,
+ * cu_new + batch is moe_route's n_tokens, and moe_verify_drafts' kv_keep is the next
+ * step's, whose kv_old is this step's kv_len.
+ *
+ * A sequence that cannot grow gains nothing (n_new counts as 0, it keeps kv_keep[b]
+ * tokens, the pages past these go back), and MOE_DEV_OVERFLOW is set:
+ *  - want needs more than max_pages pages;
+ *  - the n_new[b] > 0 of the sequences up to and with b, but for those above, come to
+ *    more than `rows`;
+ *  - it needs pages (need > held) and those that the sequences up to and with it need,
+ *    but for the ones above, are more than free_count[0] and the pages of sequences
+ *    with need < held (all of them) together.
+ * A sequence with kv_old[b] or n_new[b] negative, kv_old[b] of more than max_pages
+ * pages, or kv_keep[b] outside [0, kv_old[b]] is left as it is (kv_len[b] = kv_old[b],
+ * no new tokens, its pages stay): MOE_DEV_BAD_INDEX.  Where free_count[0] is outside
+ * [0, free_capacity], or is more than free_capacity together with the pages that go
+ * back, that holds for every sequence, and free_count_out[0] = free_count[0].
+ * All arrays are device int32 but slots (int64); page ids are copied, never followed.
+ * No output may overlap an input or another output, but page_table and free_list are
+ * both (kv_len and kv_old, free_count and free_count_out: two buffers that change
+ * places from step to step).
+ * Limits: batch up to 8192, page_size 16, 32, 64 or 128, max_pages * page_size up to
+ * 2^31 - 2^16, rows and free_capacity up to 2^30.  batch may be 0 (the counts and the
+ * rows are written all the same).  page_table row stride table_ld >= max_pages.
+ */
+typedef struct moe_kv_pages_desc {
+  const int32_t *kv_old;      /* [batch]                                    */
+  const int32_t *kv_keep;     /* [batch] or NULL                            */
+  const int32_t *n_new;       /* [batch]                                    */
+  int32_t *page_table;        /* [batch, max_pages]                         */
+  int32_t *free_list;         /* [free_capacity]                            */
+  const int32_t *free_count;  /* [1]                                        */
+  int32_t *kv_len;            /* [batch]                                    */
+  int32_t *cu_new;            /* [batch + 1]                                */
+  int32_t *free_count_out;    /* [1]                                        */
+  int32_t *seqs;              /* [rows] or NULL                             */
+  int32_t *positions;         /* [rows] or NULL                             */
+  int64_t *slots;             /* [rows] or NULL                             */
+  int32_t *err;               /* device error word (may be NULL)            */
+  int64_t table_ld, free_capacity, rows;
+  int32_t batch, max_pages, page_size;
+  int32_t flags;              /* 0                                          */
+} moe_kv_pages_desc;
+
+int moe_kv_pages(const moe_kv_pages_desc *desc, void *stream);
+
+/*
+ * moe_verify_drafts -- which of a step's drafted tokens the target model takes, and the
+ * token that follows them.
+ * Row r of probs is the target's distribution of the token after row r's.  Sequence b's
+ * rows are cu_new[b] .. cu_new[b + 1] - 1; its last n_draft[b] rows (all but the first
+ * where n_draft is NULL) hold drafted tokens, the row in front of these, s, the last
+ * token that stands.  Draft i (i = 1 .. n) is d_i = tokens[s + i]; it was drawn from row
+ * s + i - 1 of draft_probs, or, where draft_probs is NULL, from no distribution (a
+ * lookup's: all of it on d_i).  With p = probs[s + i - 1], q = draft_probs[s + i - 1]:
+ *   d_i is taken while all before it are and u_accept[s + i - 1] * q[d_i] < p[d_i]
+ *   (q[d_i] = 1 without draft_probs; a d_i outside [0, vocab) is not taken, and
+ *   MOE_DEV_BAD_INDEX is set)
+ *   accepted[b] = a, the number taken
+ *   next token: the first j whose sum w_0 + .. + w_j is above u_sample[b] times the sum
+ *   of all w (the last j with w_j > 0 where u_sample[b] is too large for one), with, in
+ *   row s + a,
+ *     w = p                                                  if all are taken
+ *     w = max(p - q, 0), p without d_(a + 1) if there is no q;  else
+ *     w = p                                                  where that is all zero
+ *   An entry of w that is not a positive finite number counts as 0, so NaNs in p and q
+ *   do; if all are 0 the token is -1, with MOE_DEV_BAD_INDEX.  A u that is NaN or
+ *   negative counts as 0.
+ *   out_tokens[b, 0 .. a) = the taken drafts, [a] = the next token, -1 up to max_out
+ *   kv_keep[b] = kv_len[b] - (n - a): the tokens that stay in the cache (both or neither
+ *   may be NULL); moe_kv_pages' kv_keep
+ * A sequence without rows gets accepted 0, tokens -1 and kv_keep = kv_len.  One whose
+ * n_draft is negative or takes all its rows, or whose rows leave [0, T), gets that with
+ * MOE_DEV_BAD_INDEX, one with more than max_out - 1 drafts with MOE_DEV_OVERFLOW.
+ * The products of the test are exact, and the sums of w are those of 64-bit arithmetic
+ * (to some 2^-44 of the total); results repeat bit for bit.
+ * probs, draft_probs: device [T, vocab] of one type (MOE_DTYPE_BF16, _F16 or _F32),
+ * row strides in elements, at least vocab, aligned to their elements; tokens, cu_new
+ * [batch + 1], n_draft, accepted, kv_len, kv_keep [batch], out_tokens [batch, max_out]
+ * (row stride out_ld): device int32; u_accept [T], u_sample [batch]: device fp32.
+ * kv_keep may be kv_len.  Limits: vocab 1 .. 2^24, batch up to 2^20, T up to 2^24,
+ * max_out 1 .. 1024.  batch = 0 launches nothing.
+ */
+typedef struct moe_verify_desc {
+  const void *probs;
+  const void *draft_probs;    /* or NULL                                    */
+  const int32_t *tokens;      /* [T]                                        */
+  const int32_t *cu_new;      /* [batch + 1]                                */
+  const int32_t *n_draft;     /* [batch] or NULL                            */
+  const float *u_accept;      /* [T]                                        */
+  const float *u_sample;      /* [batch]                                    */
+  const int32_t *kv_len;      /* [batch] or NULL                            */
+  int32_t *accepted;          /* [batch]                                    */
+  int32_t *out_tokens;        /* [batch, max_out]                           */
+  int32_t *kv_keep;           /* [batch] or NULL                            */
+  int32_t *err;               /* device error word (may be NULL)            */
+  int64_t T, vocab, p_ld, q_ld, out_ld;                          /* elements */
+  int32_t batch, max_out, dtype;
+  int32_t flags;              /* 0                                          */
+} moe_verify_desc;
+
+int moe_verify_drafts(const moe_verify_desc *desc, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
