@@ -115,6 +115,10 @@ int gemm_ue8m0_combine1(const uint8_t* A, const uint32_t* sfA, const uint8_t* B,
 // global [rows, cols] (row stride ld bytes), box [box_rows, 128 bytes].
 int make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                        uint64_t ld_bytes, uint32_t box_rows);
+// The same for a matrix of 16-bit elements: global [rows, cols] (row stride ld
+// bytes), box [box_rows, 64 elements].
+int make_tmap_b16_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                        uint64_t ld_bytes, uint32_t box_rows);
 // 2-D map over a row-major bf16 (16-bit) matrix for TMA stores of 32 x 32
 // boxes from shared memory in the 64-byte swizzle (a 64-byte row's 16-byte
 // chunk c sits at c ^ ((row >> 1) & 3)).  Same rules and codes as above.
