@@ -27,7 +27,8 @@ def bound(x, w):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("T,E,H", [(1, 1, 8), (1, 256, 7168), (2, 16, 64), (3, 17, 72), (31, 60, 2040), (64, 256, 512), (128, 128, 128),
                                    (129, 257, 136), (130, 1024, 264), (200, 300, 1000), (257, 8, 4096), (333, 60, 2040), (1000, 512, 192),
-                                   (5000, 64, 256), (4097, 255, 520), (7, 31, 8200), (20000, 33, 128)])
+                                   (5000, 64, 256), (4097, 255, 520), (7, 31, 8200), (20000, 33, 128), (16461, 256, 264),
+                                   (3000, 512, 7168), (8193, 200, 2048), (900, 129, 1032)])
 def test_logits(lib, T, E, H, dtype):
     x, w = made(T, E, H, dtype, seed=T + E)
     out = Guarded((T, E), torch.float32, f32_bits(SENTINEL_F32))
