@@ -23,6 +23,7 @@
 #include <algorithm>
 
 #include "gemm_common.cuh"
+#include "kv_common.cuh"
 
 
 namespace moe {
@@ -33,12 +34,14 @@ constexpr int kCols = 64;                      // columns of a stage: 128 bytes,
 constexpr uint32_t kXBytes = kTile * kCols * 2;
 
 constexpr int kMaxStages = 16;
+constexpr int kRun = 4;                        // blocks of 128 columns that one accumulator sums
 
 // BN experts a tile; kPair: two CTAs share the tile's gate rows and 256 tokens.
 template <int BN, bool kPair>
 struct Gate {
   static constexpr int kWRows = kPair ? BN / 2 : BN;         // gate rows that a CTA loads
-  static constexpr uint32_t kWBytes = kWRows * kCols * 2;
+  static constexpr int kSub = BN <= 128 ? 2 : 1;             // boxes of 64 columns in a stage
+  static constexpr uint32_t kWBytes = kWRows * kCols * 2;    // of one box
   static constexpr int kEpi = BN > 64 ? BN / 16 : 4;         // epilogue warps
   static constexpr int kPer = BN > 64 ? 64 : BN;             // experts of a warp
   static constexpr int kLoad = BN >= 256 || BN < 32 ? 16 : 32;   // columns of one read of an accumulator (18 warps: 96 registers)
@@ -81,6 +84,20 @@ __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uin
   }
 }
 
+// Every thread of every CTA of the cluster arrives and waits; orders no memory.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// A copy into this CTA whose barrier may be the even CTA's of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
@@ -89,21 +106,22 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 
 // A CTA's place: `rank` in its cluster of splits (x 2 in pairs) CTAs; in a pair the even
 // CTA issues the MMAs of both (M = 256: its own 128 tokens and the odd one's), with half of
-// the gate's rows in each one's shared memory.  The odd CTA's warp 1 tells the even one of
-// its full stages; commits arrive in both, the epilogue warps of both at the even one.
+// the gate's rows in each one's shared memory.  The copies of both complete on the even
+// one's barrier; commits arrive in both, the epilogue warps of both at the even one.
 template <int BN, bool kPair, bool F16>
 __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
     gate_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const GateArgs p) {
   using G = Gate<BN, kPair>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars[3 * kMaxStages + 4];
+  __shared__ uint64_t bars[2 * kMaxStages + 4];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   volatile int* abort = &abort_flag;
-  const uint32_t S = p.stages, x_bytes = static_cast<uint32_t>(p.box_rows) * kCols * 2, stage_bytes = x_bytes + G::kWBytes;
-  const uint32_t tiles = smem_u32(smem), full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages, pfull0 = empty0 + 8 * kMaxStages;
-  const uint32_t tfull0 = pfull0 + 8 * kMaxStages, tempty0 = tfull0 + 16;
+  const uint32_t S = p.stages, x_bytes = static_cast<uint32_t>(p.box_rows) * kCols * 2, box_bytes = x_bytes + G::kWBytes;
+  const uint32_t stage_bytes = G::kSub * box_bytes;
+  const uint32_t tiles = smem_u32(smem), full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages;
+  const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   constexpr int kCtas = kPair ? 2 : 1;
@@ -120,7 +138,6 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
-      mbar_init(pfull0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
@@ -147,17 +164,44 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
   const uint32_t tmem = tmem_slot;
   grid_dependency_wait();
   grid_launch_dependents();
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return kPair ? mbar_wait_bounded_cluster(bar, parity, abort, p.err, p.wait_limit_ns)
+                 : mbar_wait_bounded(bar, parity, abort, p.err, p.wait_limit_ns);
+  };
+  const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(kTile), p.T - t0))), cols = min(BN, p.E - e0);
+  const bool wide = p.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0;
+  // four logits of the tile's row r, from column c on
+  auto put = [&](int r, int c, float4 v) {
+    float* out = p.logits + (t0 + r) * p.ld + e0 + c;
+    if (wide && c + 4 <= cols) {
+      *reinterpret_cast<float4*>(out) = v;
+    } else {
+      if (c < cols) out[0] = v.x;
+      if (c + 1 < cols) out[1] = v.y;
+      if (c + 2 < cols) out[2] = v.z;
+      if (c + 3 < cols) out[3] = v.w;
+    }
+  };
 
   if (warp == 0) {
     if (lane == 0) {
-      const uint32_t n = 2 * (kb1 - kb0);
+      const uint32_t n = 2 / G::kSub * (kb1 - kb0), full_even = kPair ? cluster_map_shared(full0, rank - side) : full0;
       uint32_t it = 0, s = 0, ph = 1;
       for (; it < n; ++it) {
-        if (!mbar_wait_bounded(empty0 + 8 * s, ph, abort, p.err, p.wait_limit_ns)) break;
-        mbar_arrive_expect_tx(full0 + 8 * s, stage_bytes);
-        const int32_t col = (2 * kb0 + static_cast<int32_t>(it)) * kCols;
-        tma_load_2d(tiles + s * stage_bytes, &tmX, full0 + 8 * s, col, static_cast<int32_t>(t0));
-        tma_load_2d(tiles + s * stage_bytes + x_bytes, &tmW, full0 + 8 * s, col, e0 + side * G::kWRows);
+        if (!wait(empty0 + 8 * s, ph)) break;
+        if (side == 0) mbar_arrive_expect_tx(full0 + 8 * s, kCtas * stage_bytes);
+#pragma unroll
+        for (int i = 0; i < G::kSub; ++i) {
+          const int32_t col = (2 * kb0 + static_cast<int32_t>(it) * G::kSub + i) * kCols;
+          const uint32_t to = tiles + s * stage_bytes + i * box_bytes;
+          if constexpr (kPair) {
+            tma_load_2d_pair(to, &tmX, full_even + 8 * s, col, static_cast<int32_t>(t0));
+            tma_load_2d_pair(to + x_bytes, &tmW, full_even + 8 * s, col, e0 + side * G::kWRows);
+          } else {
+            tma_load_2d(to, &tmX, full0 + 8 * s, col, static_cast<int32_t>(t0));
+            tma_load_2d(to + x_bytes, &tmW, full0 + 8 * s, col, e0);
+          }
+        }
         if (++s == S) {
           s = 0;
           ph ^= 1;
@@ -175,19 +219,22 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
       const uint16_t both = static_cast<uint16_t>(3u << rank);
       uint32_t s = 0, ph = 0, done = 0;
       bool ok = true;
-      for (int kb = kb0; ok && kb < kb1; ++kb, ++done) {
+      for (int kb = kb0; ok && kb < kb1; kb += kRun, ++done) {
         const uint32_t b = done & 1;
-        ok = kPair ? mbar_wait_bounded_cluster(tempty0 + 8 * b, ((done >> 1) & 1) ^ 1, abort, p.err, p.wait_limit_ns)
-                   : mbar_wait_bounded(tempty0 + 8 * b, ((done >> 1) & 1) ^ 1, abort, p.err, p.wait_limit_ns);
-        for (int half = 0; ok && half < 2; ++half) {
-          ok = mbar_wait_bounded(full0 + 8 * s, ph, abort, p.err, p.wait_limit_ns) &&
-               (!kPair || mbar_wait_bounded_cluster(pfull0 + 8 * s, ph, abort, p.err, p.wait_limit_ns));
+        ok = wait(tempty0 + 8 * b, ((done >> 1) & 1) ^ 1);
+        const int n = 2 / G::kSub * min(kRun, kb1 - kb);
+        for (int i = 0; ok && i < n; ++i) {
+          ok = wait(full0 + 8 * s, ph);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t ad = sdesc_kmajor_sw128(tiles + s * stage_bytes), bd = sdesc_kmajor_sw128(tiles + s * stage_bytes + x_bytes);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)      // 16 columns, 32 bytes, an MMA: +2 in the 16-byte address field
-            umma_f16<kPair>(tmem + b * BN, ad + 2 * k, bd + 2 * k, idesc, half | k ? 1u : 0u);
+          for (int j = 0; j < G::kSub; ++j) {
+            const uint32_t at = tiles + s * stage_bytes + j * box_bytes;
+            const uint64_t ad = sdesc_kmajor_sw128(at), bd = sdesc_kmajor_sw128(at + x_bytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)      // 16 columns, 32 bytes, an MMA: +2 in the 16-byte address field
+              umma_f16<kPair>(tmem + b * BN, ad + 2 * k, bd + 2 * k, idesc, i | j | k ? 1u : 0u);
+          }
           if constexpr (kPair) umma_commit_pair(empty0 + 8 * s, both); else umma_commit(empty0 + 8 * s);
           if (++s == S) {
             s = 0;
@@ -203,17 +250,6 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
         const uint32_t j = s == 0 ? S - 1 : s - 1;
         mbar_wait_bounded(empty0 + 8 * j, s == 0 ? ph ^ 1 : ph, &dummy, nullptr, p.wait_limit_ns / 10);
       }
-    } else if (kPair && lane == 0) {
-      const uint32_t to = cluster_map_shared(pfull0, rank - 1);
-      uint32_t s = 0, ph = 0;
-      for (int it = 2 * kb0; it < 2 * kb1; ++it) {
-        if (!mbar_wait_bounded(full0 + 8 * s, ph, abort, p.err, p.wait_limit_ns)) break;
-        mbar_arrive_cluster(to + 8 * s);
-        if (++s == S) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
     }
   } else {
     const int q = warp & 3, g = (warp - 2) >> 2;
@@ -223,10 +259,11 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
     const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16) + g * 64;
     const uint32_t tempty = kPair ? cluster_map_shared(tempty0, rank - side) : tempty0;
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const uint32_t done = kb - kb0, b = done & 1;
+    uint32_t done = 0;
+    for (int kb = kb0; kb < kb1; kb += kRun, ++done) {
+      const uint32_t b = done & 1;
       int got = 1;
-      if (lane == 0) got = mbar_wait_bounded(tfull0 + 8 * b, (done >> 1) & 1, abort, p.err, p.wait_limit_ns);
+      if (lane == 0) got = wait(tfull0 + 8 * b, (done >> 1) & 1);
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) {
         ok = false;
@@ -253,34 +290,40 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
     }
     // The part goes to shared memory, over the ring: with the last accumulator full every
     // copy has landed and every MMA has read its stage.
-    if (ok && q * 32 + lane < p.box_rows) {
-      float* row = reinterpret_cast<float*>(smem) + (q * 32 + lane) * G::kLd + g * 64;
+    if (ok) {
+      float* part = reinterpret_cast<float*>(smem);
+      if (q * 32 + lane < p.box_rows) {
+        float* row = part + (q * 32 + lane) * G::kLd + g * 64;
 #pragma unroll
-      for (int i = 0; i < G::kPer / 4; ++i)
-        *reinterpret_cast<float4*>(row + 4 * i) = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+        for (int i = 0; i < G::kPer / 4; ++i)
+          *reinterpret_cast<float4*>(row + 4 * i) = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+      }
+      __syncwarp();
+      if (p.splits == 1) {     // each warp stores what it has, whole rows of it at a time
+        constexpr int n = G::kPer / 4;
+#pragma unroll 4
+        for (int i = lane; i < 32 * n; i += 32) {
+          const int r = q * 32 + i / n, c = g * 64 + i % n * 4;
+          if (r < rows) put(r, c, *reinterpret_cast<const float4*>(part + r * G::kLd + c));
+        }
+      }
     }
   }
   __syncwarp();
-  if (p.splits > 1) cluster_sync_all(); else __syncthreads();
-  // each split adds its share of the tile, the parts in the order of the splits
-  const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(kTile), p.T - t0))), cols = min(BN, p.E - e0);
-  const int items = rows * (BN / 4);
-  const int i0 = static_cast<int>(static_cast<int64_t>(items) * split / p.splits);
-  const int i1 = static_cast<int>(static_cast<int64_t>(items) * (split + 1) / p.splits);
-  const bool wide = p.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0;
-  for (int i = i0 + threadIdx.x; i < i1; i += G::kThreadCount) {
-    const int r = i / (BN / 4), c = i % (BN / 4) * 4;
-    if (c >= cols) continue;
-    const uint32_t at = tiles + (r * G::kLd + c) * 4;
-    float4 v;
-    if (p.splits == 1) {
-      v = *reinterpret_cast<const float4*>(smem + (r * G::kLd + c) * 4);
-    } else {
+  if (p.splits > 1) {
+    cluster_sync_all();
+    // each split adds its share of the tile, the parts in the order of the splits
+    const int items = rows * (BN / 4);
+    const int i0 = static_cast<int>(static_cast<int64_t>(items) * split / p.splits);
+    const int i1 = static_cast<int>(static_cast<int64_t>(items) * (split + 1) / p.splits);
+    for (int i = i0 + threadIdx.x; i < i1; i += G::kThreadCount) {
+      const int r = i / (BN / 4), c = i % (BN / 4) * 4;
+      const uint32_t at = tiles + (r * G::kLd + c) * 4;
       float4 part[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k < p.splits) part[k] = ld_cluster_f32x4(cluster_map_shared(at, k * kCtas + side));
-      v = part[0];
+      float4 v = part[0];
 #pragma unroll
       for (int k = 1; k < 8; ++k)
         if (k < p.splits) {
@@ -289,23 +332,89 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
           v.z += part[k].z;
           v.w += part[k].w;
         }
+      put(r, c, v);
     }
-    float* out = p.logits + (t0 + r) * p.ld + e0 + c;
-    if (wide && c + 4 <= cols) {
-      *reinterpret_cast<float4*>(out) = v;
-    } else {
-      out[0] = v.x;
-      if (c + 1 < cols) out[1] = v.y;
-      if (c + 2 < cols) out[2] = v.z;
-      if (c + 3 < cols) out[3] = v.w;
-    }
+    __syncwarp();
   }
   tc_fence_before();
-  if (kPair || p.splits > 1) cluster_sync_all(); else __syncthreads();   // parts are read, and barriers arrived at, by others
+  // Parts are read, and barriers arrived at, by other CTAs: none leaves before the others are
+  // done with it.  What they read has been stored by now, so no order of memory is asked for,
+  // which would have each CTA wait for its stores.
+  if (kPair || p.splits > 1) cluster_sync_relaxed();
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     if constexpr (kPair) tmem_dealloc_pair(tmem, G::kTmem); else tmem_dealloc(tmem, G::kTmem);
   }
+}
+
+// Up to 8 tokens: a tile would be idle, and what counts is how soon the gate's rows are
+// here.  A CTA takes EB experts whole, its threads 8 columns at a time.
+constexpr int kFewThreads = 256;
+constexpr int kFewTokens = 8;
+
+template <int TT, int EB, bool F16>
+__global__ void __launch_bounds__(kFewThreads) gate_few_kernel(const __grid_constant__ moe_gate_desc d) {
+  __shared__ float sums[kFewThreads / 32][TT * EB];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e0 = blockIdx.x * EB;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  float2 acc[TT][EB];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int e = 0; e < EB; ++e) acc[t][e] = make_float2(0.0f, 0.0f);
+  const uint16_t* x = static_cast<const uint16_t*>(d.x);
+  const uint16_t* w = static_cast<const uint16_t*>(d.w);
+  const int T = static_cast<int>(d.T);
+#pragma unroll TT * EB <= 4 ? 4 : 2
+  for (int h = 8 * threadIdx.x; h < d.H; h += 8 * kFewThreads) {
+    uint4 wv[EB], xv[TT];
+#pragma unroll
+    for (int e = 0; e < EB; ++e) wv[e] = __ldg(reinterpret_cast<const uint4*>(w + min(e0 + e, d.E - 1) * d.w_ld + h));
+#pragma unroll
+    for (int t = 0; t < TT; ++t) xv[t] = __ldg(reinterpret_cast<const uint4*>(x + min(t, T - 1) * d.x_ld + h));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      auto word = [&](const uint4& v) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+      float2 wf[EB];
+#pragma unroll
+      for (int e = 0; e < EB; ++e) wf[e] = pair_to_float<F16>(word(wv[e]));
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const float2 xf = pair_to_float<F16>(word(xv[t]));
+#pragma unroll
+        for (int e = 0; e < EB; ++e) acc[t][e] = __ffma2_rn(xf, wf[e], acc[t][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int e = 0; e < EB; ++e) {
+      float v = acc[t][e].x + acc[t][e].y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) sums[warp][t * EB + e] = v;
+    }
+  __syncthreads();
+  if (threadIdx.x < TT * EB) {
+    float v = sums[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kFewThreads / 32; ++i) v += sums[i][threadIdx.x];
+    const int t = threadIdx.x / EB, e = e0 + threadIdx.x % EB;
+    if (t < T && e < d.E) d.logits[t * d.logits_ld + e] = v;
+  }
+}
+
+template <int TT, bool F16>
+int launch_few(const moe_gate_desc& d, cudaStream_t st) {
+  // a CTA for every SM, and no more than two of them
+  const int sms = num_sms();
+  if (d.E <= sms) return launch_pdl(gate_few_kernel<TT, 1, F16>, dim3(d.E), dim3(kFewThreads), 0, st, d);
+  if (d.E <= 2 * sms) return launch_pdl(gate_few_kernel<TT, 2, F16>, dim3((d.E + 1) / 2), dim3(kFewThreads), 0, st, d);
+  return launch_pdl(gate_few_kernel<TT, 4, F16>, dim3((d.E + 3) / 4), dim3(kFewThreads), 0, st, d);
 }
 
 // A choice of tile and split, and what it takes.
@@ -319,8 +428,8 @@ struct GatePlan {
 size_t gate_smem(int bn, bool pair, int box_rows, int stages) {
   // the MMA reads 128 rows of tokens whether the copy brought them or not: behind the last
   // stage there is room for them; and the parts fit over the ring
-  const size_t stage = static_cast<size_t>(box_rows + (pair ? bn / 2 : bn)) * kCols * 2;
-  const size_t ring = stages * stage + (stage < kXBytes ? kXBytes - stage : 0);
+  const size_t box = static_cast<size_t>(box_rows + (pair ? bn / 2 : bn)) * kCols * 2;
+  const size_t ring = stages * (bn <= 128 ? 2 : 1) * box + (box < kXBytes ? kXBytes - box : 0);
   return 1024 + std::max(ring, static_cast<size_t>(box_rows) * (bn + 4) * 4);
 }
 
@@ -337,17 +446,18 @@ GatePlan plan_gate(int64_t T, int E, int H, int box_rows, int sms) {
         if (cluster > 8 || (pair && (bn != 256 || T <= kTile)) || (bn > 16 && bn / 2 >= E)) continue;
         const int64_t n_tiles = (E + bn - 1) / bn, m_tiles = (T + (kTile << pair) - 1) / (kTile << pair);
         const int64_t ctas = m_tiles * n_tiles * cluster;
-        const double stage = (box_rows + (pair ? bn / 2 : bn)) * 128.0;
-        const int n = 2 * ((blocks + splits - 1) / splits);
+        const int sub = bn <= 128 ? 2 : 1;
+        const double stage = sub * (box_rows + (pair ? bn / 2 : bn)) * 128.0;
+        const int n = 2 / sub * ((blocks + splits - 1) / splits);
         int stages = std::min(kMaxStages, static_cast<int>((bn >= 128 ? 196608.0 : 98304.0) / stage));
-        stages = std::max(2, std::min(stages, n));
+        stages = std::max(1, std::min(stages, n));
         const size_t smem = gate_smem(bn, pair, box_rows, stages);
         const int on_sm = smem <= 110 * 1024 ? 2 : 1;
         // clusters that an even share of a GPC's SMs does not hold leave SMs idle
         const int64_t room = cluster <= 2 ? sms : cluster == 4 ? sms - sms / 19 : sms - sms / 19 * 4;
         const int64_t waves = (ctas + room * on_sm - 1) / (room * on_sm);
         const double shared = ctas > room && on_sm == 2 ? 2.0 : 1.0;
-        const double step = std::max({shared * stage / 56.0, shared * 2.0 * bn, 200.0});
+        const double step = std::max({shared * stage / 56.0, shared * 2.0 * bn * sub, 300.0 * sub});
         const double rows = std::min<int64_t>(kTile, T);
         const double end = 3000.0 + (cluster > 1 ? 1000.0 : 0.0) + rows * bn * 4.0 / (splits > 1 ? 20.0 : 40.0);
         const double cycles = waves * (end + n * step);
@@ -381,6 +491,10 @@ int launch_gate(const moe_gate_desc& d, const GatePlan& plan, const CUtensorMap&
 
 template <bool F16>
 int run_gate(const moe_gate_desc& d, cudaStream_t st) {
+  if (d.T == 1) return launch_few<1, F16>(d, st);
+  if (d.T == 2) return launch_few<2, F16>(d, st);
+  if (d.T <= 4) return launch_few<4, F16>(d, st);
+  if (d.T <= kFewTokens) return launch_few<8, F16>(d, st);
   const int box_rows = static_cast<int>(std::min<int64_t>(kTile, (d.T + 7) / 8 * 8));
   const GatePlan plan = plan_gate(d.T, d.E, d.H, box_rows, num_sms());
   if (plan.ctas > INT32_MAX) return MOE_ERR_UNSUPPORTED;

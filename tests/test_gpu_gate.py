@@ -17,11 +17,11 @@ def made(T, E, H, dtype, seed=0, x_ld=None, w_ld=None, gain=1.0):
 
 
 def bound(x, w):
-    """Products are exact in fp32's range; sums of 128 columns on the tensor cores lose at most
-    a bit of 2^-23 of the running magnitude at each of their 8 steps of 16 (and within a step),
+    """Products are exact in fp32's range; sums of 512 columns on the tensor cores lose at most
+    a bit of 2^-23 of the running magnitude at each of their 32 steps of 16 (and within a step),
     the fp32 sums of these at most 2^-24 each of theirs.  All of it relative to sum |x w|."""
-    n = -(-x.shape[1] // 128)
-    return ((16 * 2.0 ** -23) + n * 2.0 ** -24) * (x.double().abs() @ w.double().abs().T) + 1e-37
+    n = -(-x.shape[1] // 512) + 8
+    return ((64 * 2.0 ** -23) + n * 2.0 ** -24) * (x.double().abs() @ w.double().abs().T) + 1e-37
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
