@@ -627,7 +627,7 @@ int moe_gate(const moe_gate_desc *desc, void *stream);
  * For a token with logits z_e (bf16, f16 or fp32), e = 0 .. E - 1:
  *   open     experts whose logit is not NaN or -inf (+inf counts as the largest fp32)
  *   score_e  1 / (1 + exp(-z_e)), or with MOE_ROUTE_SOFTMAX exp(z_e) / sum exp(z) over
- *            the open experts
+ *            these
  *   value_e  score_e + bias_e; without a bias the experts are ranked by z_e itself.
  *            An expert whose bias is NaN or -inf is not open.
  *   groups   with n_group > 1, experts e in [g * E / n_group, (g + 1) * E / n_group)
