@@ -254,6 +254,40 @@ __device__ __noinline__ int rank_exactly(const void* row, const float* bias, int
   return rank;
 }
 
+// Which groups stay, as a mask, by their sigmoids and biases in 64 bits.  Lane l < count has
+// expert e; among these are the experts that any group counts.
+template <int DT>
+__device__ __noinline__ uint32_t groups_exactly(const moe_route_desc& d, const void* row, int e, int count) {
+  const int lane = threadIdx.x & 31, size = d.E / d.n_group;
+  uint64_t key = 0, a = 0, b = 0;
+  if (lane < count) key = key_of(1.0 / (1.0 + exp(-static_cast<double>(load_logit<DT>(row, e)))) + __ldg(d.bias + e));
+  const int g = lane < count ? e / size : -1;
+  for (int j = 0; j < count; ++j) {
+    const uint64_t k = __shfl_sync(kAll, key, j);
+    if (__shfl_sync(kAll, g, j) == lane) {
+      b = max(b, min(a, k));
+      a = max(a, k);
+    }
+  }
+  if ((d.flags & MOE_ROUTE_GROUP_PAIR) && b != 0) a = key_of(value_of(a) + value_of(b));
+  int rank = 0;
+  for (int i = 0; i < d.n_group; ++i) rank += __shfl_sync(kAll, a, i) + (i < lane) > a;
+  return __ballot_sync(kAll, lane < d.n_group && rank < d.topk_group);
+}
+
+// How many of the earlier lanes' things there are, and of all.
+__device__ __forceinline__ int lanes_before(int have, int& all) {
+  const int lane = threadIdx.x & 31;
+  int upto = have;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, upto, o);
+    upto += lane >= o ? y : 0;
+  }
+  all = __shfl_sync(kAll, upto, 31);
+  return upto - have;
+}
+
 // A warp routes one token after another, in fp32 as far as that decides.  What bounds it is
 // the number of instructions (256 experts: 40 instructions' time of loads, some 450 of
 // arithmetic and exchange a token), so values become sortable keys once, and selection works
@@ -263,7 +297,7 @@ __device__ __noinline__ int rank_exactly(const void* row, const float* bias, int
 // the last group that stays and the first that does not, lie too near, the token is decided
 // in 64 bits.
 template <int DT, int VPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ uint64_t route_smem[];
   const moe_route_desc& d = a.d;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * VPL;
@@ -398,6 +432,24 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       } else if (biased || pair) {
         unsure = out && !(value_of(low) - value_of(out) > 4.0f * near_of(value_of(low), softmax));
       }
+      if (unsure && whole && biased && !softmax) {
+        // the experts that a group may count, up to a lane each, settle it in 64 bits
+        const float v = value_of(pair && second ? second : best);
+        const uint32_t from = best ? key_of(v - 4.0f * near_of(v, false)) : 0xffffffffu;
+        int have = 0, count;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) have += key[i] >= from;
+        int at = lanes_before(have, count);
+        if (count <= 32) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (key[i] >= from) sorted[at++] = e0 + i;
+          __syncwarp();
+          kept = real && ((groups_exactly<DT>(d, row, lane < count ? sorted[lane] : 0, count) >> mine) & 1);
+          unsure = false;
+          __syncwarp();
+        }
+      }
       if (whole) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) key[i] = kept ? key[i] : 0u;
@@ -430,17 +482,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     int have = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) have += key[i] >= least;
-    int upto = have;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, upto, o);
-      upto += lane >= o ? y : 0;
-    }
-    int count = __shfl_sync(kAll, upto, 31), rank = lane;
+    int count, rank = lane;
+    const int first = lanes_before(have, count);
     const bool few = count <= 32;
     uint2 me = make_uint2(0u, 0u);
     if (few) {
-      uint2* at = list + (upto - have);
+      uint2* at = list + first;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
         if (key[i] >= least) *at++ = make_uint2(key[i], e0 + i);
@@ -526,7 +573,7 @@ int launch_route(RouteArgs& a, cudaStream_t st) {
   a.group_lanes = 1;
   while (2 * a.group_lanes * a.d.n_group <= 32) a.group_lanes *= 2;
   // a few tokens a warp, so that a row is on its way while another is routed
-  const int64_t ctas = std::min<int64_t>((a.d.T + kRouteWarps - 1) / kRouteWarps, 8ll * num_sms());
+  const int64_t ctas = std::min<int64_t>((a.d.T + kRouteWarps - 1) / kRouteWarps, 32ll * num_sms());
   return launch_pdl(route_kernel<DT, VPL>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kRouteWarps),
                     sizeof(uint64_t) * kRouteWarps * a.slot, st, a);
 }
