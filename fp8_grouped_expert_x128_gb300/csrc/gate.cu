@@ -84,11 +84,6 @@ __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uin
   }
 }
 
-// Every thread of every CTA of the cluster arrives and waits; orders no memory.
-__device__ __forceinline__ void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
 // A copy into this CTA whose barrier may be the even CTA's of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t bar, int32_t x, int32_t y) {
   asm volatile(

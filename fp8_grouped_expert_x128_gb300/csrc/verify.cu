@@ -5,12 +5,13 @@
 // takes time is the one row of the target's distribution (and of the draft's, where
 // a draft is turned down) that the next token is drawn from.  It is read once: every
 // warp sums a run of the vocabulary, the cluster exchanges the warps' sums, and the
-// warp whose run holds the border reads its run again, from the L2.
+// warp whose run holds the border looks for it in its run, a 32nd at a time, from the
+// L2.
 //
 // Exactness: a token's borders may lie 1e-9 of the total apart, so sums are those of
-// 64-bit arithmetic.  GB300 has few 64-bit units, so a lane sums in pairs of fp32
-// (D. E. Knuth's two-sum, TAOCP vol. 2, 4.2.2: sum and rounding error of two numbers
-// as two numbers), and only its totals are taken to fp64.
+// 64-bit arithmetic.  GB300 has few 64-bit units (a dependent addition takes 61 cycles),
+// so a lane sums in pairs of fp32 (D. E. Knuth's two-sum, TAOCP vol. 2, 4.2.2: sum and
+// rounding error of two numbers as two numbers), and only warps' totals are taken to fp64.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -22,7 +23,7 @@ namespace {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyMaxCluster = 8;
+constexpr int kAhead = 4;              // 16-byte loads of a row that a lane has under way
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct VerifyArgs {
@@ -36,24 +37,16 @@ __device__ __forceinline__ float prob_at(const void* row, int64_t j) {
   return DT == MOE_DTYPE_F16 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_float(b);
 }
 
+// A sum and what its rounding lost.
 struct Pair {
   float hi = 0.0f, lo = 0.0f;
   // adds s + e, e small beside s
   __device__ __forceinline__ void add(float s, float e) {
-    const float t = hi + s, u = t - hi;
-    lo += ((hi - (t - u)) + (s - u)) + e;
+    const float t = __fadd_rn(hi, s), u = __fsub_rn(t, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(t, u)), __fsub_rn(s, u)), e));
     hi = t;
   }
 };
-
-// w of an entry as a sum of two fp32 numbers: p - q exactly, 0 where that is not a
-// positive finite number.
-__device__ __forceinline__ void weight_of(float p, float q, float& s, float& e) {
-  s = p - q;
-  const float u = s - p;
-  e = (p - (s - u)) - (q + u);
-  if (!(s > 0.0f && s <= FLT_MAX)) s = e = 0.0f;
-}
 
 __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
   double v;
@@ -61,17 +54,151 @@ __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
   return v;
 }
 
-// The distribution that the next token is drawn from.
+// The distribution that the next token is drawn from: weights p, or max(p - q, 0), in
+// vectors of 16 bytes that start where p's addresses are multiples of 16.
 template <int DT>
 struct Weights {
-  const void* p;
-  const void* q;     // or NULL
-  int64_t without;   // an entry that counts as 0, or -1
-  __device__ __forceinline__ void at(int64_t j, float& s, float& e) const {
-    weight_of(prob_at<DT>(p, j), q ? prob_at<DT>(q, j) : 0.0f, s, e);
-    if (j == without) s = e = 0.0f;
+  static constexpr int kVec = DT == MOE_DTYPE_F32 ? 4 : 8, kSize = 16 / kVec;
+  const char* p;
+  const char* q;      // or NULL
+  int64_t vocab;
+  int64_t without;    // an entry that counts as 0, or -1
+  int shift;          // entries of vector 0 in front of the row
+  bool q_wide;        // q's vectors lie like p's
+  bool careful;       // infinities are looked for (else they show as a sum that is not finite)
+
+  __device__ __forceinline__ void set(const char* p_row, const char* q_row, int64_t v, int64_t wo) {
+    p = p_row;
+    q = q_row;
+    vocab = v;
+    without = wo;
+    shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / kSize;
+    q_wide = ((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15) == 0;
+    careful = false;
+  }
+  __device__ __forceinline__ int64_t vectors() const { return (shift + vocab + kVec - 1) / kVec; }
+  // vectors [k, k + n) inside the row
+  __device__ __forceinline__ bool inside(int64_t k, int64_t n) const {
+    return k * kVec >= shift && (k + n) * kVec <= shift + vocab;
+  }
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kVec]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == MOE_DTYPE_F32) {
+        f[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 v = pair_to_float<DT == MOE_DTYPE_F16>(w[i]);
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ uint4 load(const char* row, int64_t k, int shift) {
+    return __ldcs(reinterpret_cast<const uint4*>(row - shift * kSize) + k);
+  }
+  // p - q as the sum of two numbers, 0 where that is not positive (or NaN)
+  __device__ __forceinline__ void weight(float x, float y, float& s, float& e) const {
+    const float d = __fsub_rn(x, y), u = __fsub_rn(d, x);
+    e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, u)), __fadd_rn(y, u));
+    e = d > 0.0f ? e : 0.0f;
+    s = fmaxf(d, 0.0f);
+    if (careful && !(s <= FLT_MAX)) s = e = 0.0f;
+  }
+  __device__ __forceinline__ void weight(float x, float& s) const {
+    s = fmaxf(x, 0.0f);
+    if (careful && !(s <= FLT_MAX)) s = 0.0f;
+  }
+  // vector k's weights, whatever of it is in the row
+  __device__ __forceinline__ void get(int64_t k, float (&s)[kVec], float (&e)[kVec]) const {
+    float x[kVec], y[kVec];
+    const int64_t j0 = k * kVec - shift;
+    if (inside(k, 1)) {
+      unpack(load(p, k, shift), x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[i] = j0 + i >= 0 && j0 + i < vocab ? prob_at<DT>(p, j0 + i) : 0.0f;
+    }
+    if (q != nullptr && inside(k, 1) && q_wide) {
+      unpack(load(q, k, shift), y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) y[i] = q != nullptr && j0 + i >= 0 && j0 + i < vocab ? prob_at<DT>(q, j0 + i) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      weight(x[i], y[i], s[i], e[i]);
+      if (j0 + i == without) s[i] = e[i] = 0.0f;
+    }
+  }
+  // the sum of vectors from, from + by, .. below to
+  __device__ __forceinline__ double sum(int64_t from, int64_t to, int by) const {
+    Pair acc[4];
+    const bool wide = q == nullptr || q_wide;
+    int64_t k = from;
+    for (; k + (kAhead - 1) * by < to; k += kAhead * by) {
+      const int64_t j0 = k * kVec - shift, j1 = (k + (kAhead - 1) * by + 1) * kVec - shift;
+      if (wide && inside(k, (kAhead - 1) * by + 1) && !(without >= j0 && without < j1)) {
+        uint4 a[kAhead], b[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) a[i] = load(p, k + i * by, shift);
+        if (q != nullptr) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) b[i] = load(q, k + i * by, shift);
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            float x[kVec], y[kVec];
+            unpack(a[i], x);
+            unpack(b[i], y);
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+              float s, e;
+              weight(x[c], y[c], s, e);
+              acc[c & 3].add(s, e);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            float x[kVec];
+            unpack(a[i], x);
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+              float s;
+              weight(x[c], s);
+              acc[c & 3].add(s, 0.0f);
+            }
+          }
+        }
+      } else {
+        for (int i = 0; i < kAhead; ++i) add_one(k + i * by, acc);
+      }
+    }
+    for (; k < to; k += by) add_one(k, acc);
+    acc[0].add(acc[1].hi, acc[1].lo);
+    acc[2].add(acc[3].hi, acc[3].lo);
+    acc[0].add(acc[2].hi, acc[2].lo);
+    return static_cast<double>(acc[0].hi) + static_cast<double>(acc[0].lo);
+  }
+
+ private:
+  __device__ __forceinline__ void add_one(int64_t k, Pair (&acc)[4]) const {
+    float s[kVec], e[kVec];
+    get(k, s, e);
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) acc[c & 3].add(s[c], e[c]);
   }
 };
+
+__device__ __forceinline__ double warp_prefix(double x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(kAll, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
 
 template <int DT>
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
@@ -85,11 +212,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
   const int64_t r0 = d.cu_new[b], r1 = d.cu_new[b + 1];
   const int64_t n = d.n_draft ? d.n_draft[b] : r1 - r0 - 1;
   const int32_t len = d.kv_len ? d.kv_len[b] : 0;
+  const float u_sample = d.u_sample[b];
   const bool none = r1 == r0 && r0 >= 0 && r1 <= d.T;
   const bool bad = !none && (r0 < 0 || r1 < r0 || r1 > d.T || n < 0 || n >= r1 - r0), wide = !none && !bad && n >= d.max_out;
+  int32_t* out = d.out_tokens + b * d.out_ld;
   if (none || bad || wide) {           // the same for all threads of the cluster
     if (rank == 0) {
-      for (int i = threadIdx.x; i < d.max_out; i += kVerifyThreads) d.out_tokens[b * d.out_ld + i] = -1;
+      for (int i = threadIdx.x; i < d.max_out; i += kVerifyThreads) out[i] = -1;
       if (threadIdx.x == 0) {
         d.accepted[b] = 0;
         if (d.kv_keep) d.kv_keep[b] = len;
@@ -98,10 +227,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     }
     return;
   }
-  constexpr int kSize = DT == MOE_DTYPE_F32 ? 4 : 2;
+  using W = Weights<DT>;
   const int64_t s0 = r1 - 1 - n;       // the last token that stands
-  auto p_row = [&](int64_t r) { return static_cast<const char*>(d.probs) + r * d.p_ld * kSize; };
-  auto q_row = [&](int64_t r) { return static_cast<const char*>(d.draft_probs) + r * d.q_ld * kSize; };
+  auto p_row = [&](int64_t r) { return static_cast<const char*>(d.probs) + r * d.p_ld * W::kSize; };
+  auto q_row = [&](int64_t r) { return static_cast<const char*>(d.draft_probs) + r * d.q_ld * W::kSize; };
   // every warp tests all drafts, 32 at a time, up to the first that is not taken
   int taken = 0;
   for (; taken < n; taken += 32) {
@@ -109,11 +238,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     if (taken + lane < n) {
       const int64_t r = s0 + taken + lane;
       const int32_t t = d.tokens[r + 1];
+      const float u = d.u_accept[r];
       ok = t >= 0 && t < d.vocab;
       if (ok) {
         const double p = prob_at<DT>(p_row(r), t), q = d.draft_probs ? prob_at<DT>(q_row(r), t) : 1.0;
-        const float u = d.u_accept[r];
-        ok = (u > 0.0f ? static_cast<double>(u) : 0.0) * q < p;
+        ok = (u > 0.0f ? static_cast<double>(u) : 0.0) * q < p;      // exact: 24 bits by 24
       }
     }
     const uint32_t no = __ballot_sync(kAll, !ok);
@@ -126,96 +255,121 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
   const bool refused = taken < n;
   const int64_t row = s0 + taken;
   const int32_t wrong = refused ? d.tokens[row + 1] : -1;
+
+  // this warp's run of the vocabulary
+  W w;
+  w.set(p_row(row), refused && d.draft_probs ? q_row(row) : nullptr, d.vocab, refused && !d.draft_probs ? wrong : -1);
+  const int warps = ctas * kVerifyWarps, me = rank * kVerifyWarps + warp;
+  const int64_t run = ((w.vectors() + warps - 1) / warps + 31) / 32 * 32;
+  int64_t k0 = min(me * run, w.vectors()), k1 = min(k0 + run, w.vectors());
+  const double u = u_sample > 0.0f ? static_cast<double>(u_sample) : 0.0;
+  const int per = (warps + 31) / 32;            // warps' sums of a lane, at most 4
+  double before = 0.0, target = 0.0;
+  int owner = -1;
+  bool any = false;
+  for (int pass = 0; pass < 4; ++pass) {
+    double sum = w.sum(k0 + lane, k1, 32);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (lane == 0) sums[pass & 1][warp] = sum;
+    __syncwarp();
+    cluster_sync_all();
+    // every warp: all warps' sums, in the vocabulary's order
+    double x[4], mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = lane * per + i;
+      x[i] = i < per && at < warps ? ld_cluster_f64(cluster_map_shared(smem_u32(&sums[pass & 1][at % kVerifyWarps]), at / kVerifyWarps)) : 0.0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < per) mine += x[i];
+    const double upto = warp_prefix(mine);
+    const double total = __shfl_sync(kAll, upto, 31);
+    if (!isfinite(total) && !w.careful) {       // infinities among the entries: without them
+      w.careful = true;
+      continue;
+    }
+    any = total > 0.0;
+    if (!any && refused && (w.q != nullptr || w.without >= 0)) {
+      w.set(p_row(row), nullptr, d.vocab, -1);    // nothing is left of the target's distribution: all of it
+      // (its vectors are the same ones)
+      continue;
+    }
+    target = u * total;
+    // the first warp whose sums pass the target, or the last that has some
+    int first = -1, last = -1;
+    double at = upto - mine, from = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < per) {
+        const double next = i + 1 == per ? upto : at + x[i];
+        if (first < 0 && next > target) {
+          first = lane * per + i;
+          from = at;
+        }
+        if (x[i] > 0.0) last = lane * per + i;
+        at = next;
+      }
+    const uint32_t over = __ballot_sync(kAll, first >= 0), some = __ballot_sync(kAll, last >= 0);
+    if (over) {
+      owner = __shfl_sync(kAll, first, __ffs(over) - 1);
+      before = __shfl_sync(kAll, from, __ffs(over) - 1);
+    } else if (some) {
+      owner = __shfl_sync(kAll, last, 31 - __clz(some));
+      target = INFINITY;
+    }
+    break;
+  }
+  __syncwarp();
+  cluster_sync_relaxed();                       // the others have read this CTA's sums
   if (rank == 0) {
     for (int i = threadIdx.x; i < d.max_out; i += kVerifyThreads)
-      if (i != taken) d.out_tokens[b * d.out_ld + i] = i < taken ? d.tokens[s0 + 1 + i] : -1;
+      if (i != taken) out[i] = i < taken ? d.tokens[s0 + 1 + i] : -1;
     if (threadIdx.x == 0) {
       d.accepted[b] = taken;
       if (d.kv_keep) d.kv_keep[b] = len - static_cast<int32_t>(n - taken);
-      if (wrong < 0 ? refused : wrong >= d.vocab) set_err(d.err, MOE_DEV_BAD_INDEX);
+      if (!any) out[taken] = -1;
+      if (!any || (refused && (wrong < 0 || wrong >= d.vocab))) set_err(d.err, MOE_DEV_BAD_INDEX);
     }
   }
-
-  // this warp's run of the vocabulary
-  const int64_t V = d.vocab, warps = static_cast<int64_t>(ctas) * kVerifyWarps;
-  const int64_t len_run = (V + warps - 1) / warps, me = static_cast<int64_t>(rank) * kVerifyWarps + warp;
-  const int64_t v0 = min(me * len_run, V), v1 = min(v0 + len_run, V);
-  Weights<DT> w{p_row(row), nullptr, -1};
-  if (refused) {
-    if (d.draft_probs) w.q = q_row(row);
-    else w.without = wrong;
+  if (!any || owner != me) return;
+  // the vector in the run, a 32nd at a time
+  for (;;) {
+    const int64_t piece = (k1 - k0 + 31) / 32, f = min(k0 + lane * piece, k1), t = min(f + piece, k1);
+    const double x = w.sum(f, t, 1), upto = warp_prefix(x);
+    const uint32_t over = __ballot_sync(kAll, x > 0.0 && before + upto > target), some = __ballot_sync(kAll, x > 0.0);
+    // rounding may leave the border just behind the run: then its last entry
+    const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
+    if (!over) target = INFINITY;
+    before += __shfl_sync(kAll, upto - x, at);
+    k0 = __shfl_sync(kAll, f, at);
+    k1 = __shfl_sync(kAll, t, at);
+    if (piece <= 1) break;
   }
-  double total = 0.0, before = 0.0, run = 0.0;
-  int owner = -1, last = -1;
-  for (int pass = 0; pass < 2; ++pass) {
-    Pair acc;
-    for (int64_t j = v0 + lane; j < v1; j += 32) {
-      float s, e;
-      w.at(j, s, e);
-      acc.add(s, e);
-    }
-    double sum = static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
+  if (lane == 0) {
+    float s[W::kVec], e[W::kVec];
+    w.get(k0, s, e);
+    int found = -1, last = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) sums[pass][warp] = sum;
-    cluster_sync_all();
-    // every warp: all warps' sums, in the vocabulary's order
-    total = before = 0.0;
-    owner = last = -1;
-    const double u = d.u_sample[b] > 0.0f ? static_cast<double>(d.u_sample[b]) : 0.0;
-    auto sum_of = [&](int i) {
-      return ld_cluster_f64(cluster_map_shared(smem_u32(&sums[pass][i % kVerifyWarps]), i / kVerifyWarps));
-    };
-    for (int i = 0; i < warps; ++i) total += sum_of(i);
-    const double target = u * total;
-    double at = 0.0;
-    for (int i = 0; i < warps; ++i) {
-      const double x = sum_of(i);
-      if (owner < 0 && at + x > target) {
-        owner = i;
-        before = at;
-        run = target;
+    for (int i = 0; i < W::kVec; ++i) {
+      before += static_cast<double>(s[i]) + static_cast<double>(e[i]);
+      if (s[i] > 0.0f) {
+        last = i;
+        if (found < 0 && before > target) found = i;
       }
-      if (x > 0.0) last = i;
-      at += x;
     }
-    if (total > 0.0 || !refused) break;
-    w.q = nullptr;                     // nothing is left of the target's distribution: all of it
-    w.without = -1;
+    out[taken] = static_cast<int32_t>(k0 * W::kVec - w.shift + (found >= 0 ? found : last));
   }
-  const bool beyond = owner < 0;       // u of 1 or more
-  if ((beyond ? last : owner) == me) {
-    // the first entry of the run whose sum passes the target, or the last that counts
-    int64_t found = -1, counts = -1;
-    for (int64_t j0 = v0; j0 < v1 && found < 0; j0 += 32) {
-      const int64_t j = j0 + lane;
-      float s = 0.0f, e = 0.0f;
-      if (j < v1) w.at(j, s, e);
-      double x = static_cast<double>(s) + static_cast<double>(e);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(kAll, x, o);
-        if (lane >= o) x += y;
-      }
-      const uint32_t some = __ballot_sync(kAll, s > 0.0f);
-      const uint32_t over = __ballot_sync(kAll, !beyond && s > 0.0f && before + x > run);
-      if (over) found = j0 + __ffs(over) - 1;
-      if (some) counts = j0 + 31 - __clz(some);
-      before += __shfl_sync(kAll, x, 31);
-    }
-    if (lane == 0) d.out_tokens[b * d.out_ld + taken] = static_cast<int32_t>(found >= 0 ? found : counts);
-  } else if (last < 0 && rank == 0 && threadIdx.x == 0) {   // no entry counts
-    d.out_tokens[b * d.out_ld + taken] = -1;
-    set_err(d.err, MOE_DEV_BAD_INDEX);
-  }
-  cluster_sync_all();                  // the others may still read this CTA's sums
 }
 
 template <int DT>
 int launch_verify(const VerifyArgs& a, cudaStream_t st) {
-  // as many CTAs a sequence as fill the GPU, up to a portable cluster
-  int ctas = kVerifyMaxCluster;
-  while (ctas > 1 && static_cast<int64_t>(a.d.batch) * ctas > 4 * num_sms()) ctas /= 2;
+  // As many CTAs a sequence as fill the GPU (8 on an SM), but no more than have 32 vectors a
+  // warp.  Sixteen to a cluster only where these find room at once (7 clusters).
+  const int64_t vectors = a.d.vocab / Weights<DT>::kVec + 2, B = a.d.batch;
+  int ctas = 16 * B <= 112 ? 16 : 8;
+  while (ctas > 1 && (B * ctas > 8 * num_sms() || (ctas / 2) * kVerifyWarps * 32 >= vectors)) ctas /= 2;
   for (int32_t b0 = 0; b0 < a.d.batch; b0 += 65535) {      // a grid's second dimension
     VerifyArgs part = a;
     part.d.batch = std::min(a.d.batch - b0, 65535);
@@ -238,6 +392,7 @@ int launch_verify(const VerifyArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    if (ctas > 8) MOE_CUDA_TRY(cudaFuncSetAttribute(verify_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     if (cudaLaunchKernelEx(&cfg, verify_kernel<DT>, part) != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
