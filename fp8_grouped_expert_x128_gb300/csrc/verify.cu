@@ -9,9 +9,9 @@
 // L2.
 //
 // Exactness: a token's borders may lie 1e-9 of the total apart, so sums are those of
-// 64-bit arithmetic.  GB300 has few 64-bit units (a dependent addition takes 61 cycles),
-// so a lane sums in pairs of fp32 (D. E. Knuth's two-sum, TAOCP vol. 2, 4.2.2: sum and
-// rounding error of two numbers as two numbers), and only warps' totals are taken to fp64.
+// 64-bit arithmetic.  GB300 has few 64-bit units (a dependent addition takes 61 cycles,
+// and a warp's holds up the SM's other warps), so sums are pairs of fp32 (D. E. Knuth's
+// two-sum, TAOCP vol. 2, 4.2.2: sum and rounding error of two numbers as two numbers).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyMaxCluster = 16;
 constexpr int kAhead = 4;              // 16-byte loads of a row that a lane has under way
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -46,41 +47,84 @@ struct Pair {
     lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(t, u)), __fsub_rn(s, u)), e));
     hi = t;
   }
+  __device__ __forceinline__ void add(const Pair& o) { add(o.hi, o.lo); }
+  // lo below half a unit of hi: then pairs compare by hi first
+  __device__ __forceinline__ Pair tidy() const {
+    const float t = __fadd_rn(hi, lo);
+    return {t, __fadd_rn(__fsub_rn(hi, t), lo)};
+  }
+  __device__ __forceinline__ bool above(const Pair& o) const {
+    const Pair a = tidy(), b = o.tidy();
+    return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+  }
 };
 
-__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ Pair plus(Pair a, const Pair& b) {
+  a.add(b);
+  return a;
 }
+__device__ __forceinline__ Pair shfl(const Pair& v, int lane) { return {__shfl_sync(kAll, v.hi, lane), __shfl_sync(kAll, v.lo, lane)}; }
+
+// The sum over the lanes up to and with this one, and of those before it.
+__device__ __forceinline__ Pair warp_prefix(Pair x, Pair& before) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair y{__shfl_up_sync(kAll, x.hi, o), __shfl_up_sync(kAll, x.lo, o)};
+    if (lane >= o) x = plus(y, x);
+  }
+  before = {__shfl_up_sync(kAll, x.hi, 1), __shfl_up_sync(kAll, x.lo, 1)};
+  if (lane == 0) before = Pair{};
+  return x;
+}
+
+__device__ __forceinline__ void st_cluster_pair(uint32_t addr, const Pair& v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.hi), "f"(v.lo) : "memory");
+}
+
+// Two sums at a time, in the packed arithmetic of sm_100 and later.
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.0f, -1.0f), a); }
+struct Pairs {
+  float2 hi = {0.0f, 0.0f}, lo = {0.0f, 0.0f};
+  __device__ __forceinline__ void add(float2 s, float2 e) {
+    const float2 t = __fadd2_rn(hi, s), u = sub2(t, hi);
+    lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(sub2(hi, sub2(t, u)), sub2(s, u)), e));
+    hi = t;
+  }
+  __device__ __forceinline__ void add(float2 s) {
+    const float2 t = __fadd2_rn(hi, s), u = sub2(t, hi);
+    lo = __fadd2_rn(lo, __fadd2_rn(sub2(hi, sub2(t, u)), sub2(s, u)));
+    hi = t;
+  }
+  __device__ __forceinline__ Pair sum() const { return plus(Pair{hi.x, lo.x}, Pair{hi.y, lo.y}); }
+};
 
 // The distribution that the next token is drawn from: weights p, or max(p - q, 0), in
 // vectors of 16 bytes that start where p's addresses are multiples of 16.
 template <int DT>
 struct Weights {
   static constexpr int kVec = DT == MOE_DTYPE_F32 ? 4 : 8, kSize = 16 / kVec;
-  const char* p;
-  const char* q;      // or NULL
-  int64_t vocab;
-  int64_t without;    // an entry that counts as 0, or -1
+  const char* p;      // the row, and q's or NULL
+  const char* q;
+  int vocab;
+  int without;        // an entry that counts as 0, or -1
   int shift;          // entries of vector 0 in front of the row
+  int whole0, whole1; // vectors that lie in the row whole
   bool q_wide;        // q's vectors lie like p's
-  bool careful;       // infinities are looked for (else they show as a sum that is not finite)
+  bool careful;       // entries that are not finite are looked for (else they show as a sum that is not)
 
-  __device__ __forceinline__ void set(const char* p_row, const char* q_row, int64_t v, int64_t wo) {
+  __device__ __forceinline__ void set(const char* p_row, const char* q_row, int v, int wo) {
     p = p_row;
     q = q_row;
     vocab = v;
     without = wo;
     shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / kSize;
+    whole0 = shift > 0;
+    whole1 = (shift + vocab) / kVec;
     q_wide = ((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15) == 0;
     careful = false;
   }
-  __device__ __forceinline__ int64_t vectors() const { return (shift + vocab + kVec - 1) / kVec; }
-  // vectors [k, k + n) inside the row
-  __device__ __forceinline__ bool inside(int64_t k, int64_t n) const {
-    return k * kVec >= shift && (k + n) * kVec <= shift + vocab;
-  }
+  __device__ __forceinline__ int vectors() const { return (shift + vocab + kVec - 1) / kVec; }
   static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kVec]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -94,115 +138,96 @@ struct Weights {
       }
     }
   }
-  static __device__ __forceinline__ uint4 load(const char* row, int64_t k, int shift) {
+  __device__ __forceinline__ uint4 load(const char* row, int k) const {
     return __ldcs(reinterpret_cast<const uint4*>(row - shift * kSize) + k);
   }
-  // p - q as the sum of two numbers, 0 where that is not positive (or NaN)
-  __device__ __forceinline__ void weight(float x, float y, float& s, float& e) const {
-    const float d = __fsub_rn(x, y), u = __fsub_rn(d, x);
-    e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, u)), __fadd_rn(y, u));
-    e = d > 0.0f ? e : 0.0f;
-    s = fmaxf(d, 0.0f);
-    if (careful && !(s <= FLT_MAX)) s = e = 0.0f;
-  }
-  __device__ __forceinline__ void weight(float x, float& s) const {
-    s = fmaxf(x, 0.0f);
-    if (careful && !(s <= FLT_MAX)) s = 0.0f;
-  }
-  // vector k's weights, whatever of it is in the row
-  __device__ __forceinline__ void get(int64_t k, float (&s)[kVec], float (&e)[kVec]) const {
-    float x[kVec], y[kVec];
-    const int64_t j0 = k * kVec - shift;
-    if (inside(k, 1)) {
-      unpack(load(p, k, shift), x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = j0 + i >= 0 && j0 + i < vocab ? prob_at<DT>(p, j0 + i) : 0.0f;
-    }
-    if (q != nullptr && inside(k, 1) && q_wide) {
-      unpack(load(q, k, shift), y);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) y[i] = q != nullptr && j0 + i >= 0 && j0 + i < vocab ? prob_at<DT>(q, j0 + i) : 0.0f;
-    }
-#pragma unroll
+  // vector k of a row that does not lie in it whole, or not at multiples of 16 bytes: zeros outside
+  __device__ __noinline__ uint4 piece(const char* row, int k) const {
+    uint32_t w[4] = {0, 0, 0, 0};
     for (int i = 0; i < kVec; ++i) {
-      weight(x[i], y[i], s[i], e[i]);
-      if (j0 + i == without) s[i] = e[i] = 0.0f;
+      const int j = k * kVec - shift + i;
+      if (j < 0 || j >= vocab) continue;
+      if constexpr (DT == MOE_DTYPE_F32) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row) + j);
+      else w[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(row) + j)) << (16 * (i & 1));
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // the sum of vectors from, from + by, .. below to
-  __device__ __forceinline__ double sum(int64_t from, int64_t to, int by) const {
-    Pair acc[4];
-    const bool wide = q == nullptr || q_wide;
-    int64_t k = from;
-    for (; k + (kAhead - 1) * by < to; k += kAhead * by) {
-      const int64_t j0 = k * kVec - shift, j1 = (k + (kAhead - 1) * by + 1) * kVec - shift;
-      if (wide && inside(k, (kAhead - 1) * by + 1) && !(without >= j0 && without < j1)) {
-        uint4 a[kAhead], b[kAhead];
+  // one entry's weight as the sum of two numbers, 0 where that is not positive and finite
+  __device__ __forceinline__ Pair weight(float x, float y) const {
+    const float d = __fsub_rn(x, y), u = __fsub_rn(d, x), e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, u)), __fadd_rn(y, u));
+    return d > 0.0f && d <= FLT_MAX ? Pair{d, e} : Pair{};
+  }
+  __device__ __forceinline__ Pair entry(int j) const {
+    if (j < 0 || j >= vocab || j == without) return Pair{};
+    return weight(prob_at<DT>(p, j), q ? prob_at<DT>(q, j) : 0.0f);
+  }
+  // The sum of vectors from, from + by, .. below to.  q counts as min(q, p): no comparison is
+  // left, and what is not finite shows in the sum.
+  __device__ __forceinline__ Pair sum(int from, int to, int by) const {
+    if (careful) return sum_carefully(from, to, by);
+    Pairs acc[2];
+    for (int k = from; k < to; k += kAhead * by) {
+      uint4 a[kAhead], b[kAhead];
+      const int last = k + (kAhead - 1) * by;
+      if (k >= whole0 && last < min(whole1, to) && q_wide) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) a[i] = load(p, k + i * by, shift);
-        if (q != nullptr) {
+        for (int i = 0; i < kAhead; ++i) a[i] = load(p, k + i * by);
+        if (q != nullptr)
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) b[i] = load(q, k + i * by, shift);
+          for (int i = 0; i < kAhead; ++i) b[i] = load(q, k + i * by);
+      } else {
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            float x[kVec], y[kVec];
-            unpack(a[i], x);
-            unpack(b[i], y);
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-              float s, e;
-              weight(x[c], y[c], s, e);
-              acc[c & 3].add(s, e);
-            }
+        for (int i = 0; i < kAhead; ++i) {
+          const int at = k + i * by;
+          const bool inside = at >= whole0 && at < whole1;
+          a[i] = b[i] = make_uint4(0, 0, 0, 0);
+          if (at < to) {
+            a[i] = inside ? load(p, at) : piece(p, at);
+            if (q != nullptr) b[i] = inside && q_wide ? load(q, at) : piece(q, at);
           }
-        } else {
+        }
+      }
+      if (q != nullptr) {
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            float x[kVec];
-            unpack(a[i], x);
+        for (int i = 0; i < kAhead; ++i) {
+          float x[kVec], y[kVec];
+          unpack(a[i], x);
+          unpack(b[i], y);
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-              float s;
-              weight(x[c], s);
-              acc[c & 3].add(s, 0.0f);
-            }
+          for (int c = 0; c < kVec; c += 2) {
+            const float2 m = make_float2(fminf(y[c], x[c]), fminf(y[c + 1], x[c + 1])), v = make_float2(x[c], x[c + 1]);
+            const float2 d = sub2(v, m), u = sub2(d, v);
+            acc[c / 2 & 1].add(d, sub2(sub2(v, sub2(d, u)), __fadd2_rn(m, u)));
           }
         }
       } else {
-        for (int i = 0; i < kAhead; ++i) add_one(k + i * by, acc);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          float x[kVec];
+          unpack(a[i], x);
+          const int out = without - ((k + i * by) * kVec - shift);
+          if (without >= 0 && out >= 0 && out < kVec) {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) x[c] = c == out ? 0.0f : x[c];
+          }
+#pragma unroll
+          for (int c = 0; c < kVec; c += 2) acc[c / 2 & 1].add(make_float2(fmaxf(x[c], 0.0f), fmaxf(x[c + 1], 0.0f)));
+        }
       }
     }
-    for (; k < to; k += by) add_one(k, acc);
-    acc[0].add(acc[1].hi, acc[1].lo);
-    acc[2].add(acc[3].hi, acc[3].lo);
-    acc[0].add(acc[2].hi, acc[2].lo);
-    return static_cast<double>(acc[0].hi) + static_cast<double>(acc[0].lo);
+    return plus(acc[0].sum(), acc[1].sum());
   }
-
- private:
-  __device__ __forceinline__ void add_one(int64_t k, Pair (&acc)[4]) const {
-    float s[kVec], e[kVec];
-    get(k, s, e);
-#pragma unroll
-    for (int c = 0; c < kVec; ++c) acc[c & 3].add(s[c], e[c]);
+  __device__ __noinline__ Pair sum_carefully(int from, int to, int by) const {
+    Pair acc;
+    for (int k = from; k < to; k += by)
+      for (int i = 0; i < kVec; ++i) acc.add(entry(k * kVec - shift + i));
+    return acc;
   }
 };
 
-__device__ __forceinline__ double warp_prefix(double x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(kAll, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-
 template <int DT>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ double sums[2][kVerifyWarps];
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ Pair sums[2][kVerifyWarps * kVerifyMaxCluster];      // of all warps of the cluster
   const moe_verify_desc& d = a.d;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y, ctas = gridDim.x, rank = blockIdx.x;
@@ -227,6 +252,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     }
     return;
   }
+  cluster_arrive_relaxed();            // this CTA runs: the others may write to its shared memory
   using W = Weights<DT>;
   const int64_t s0 = r1 - 1 - n;       // the last token that stands
   auto p_row = [&](int64_t r) { return static_cast<const char*>(d.probs) + r * d.p_ld * W::kSize; };
@@ -258,71 +284,71 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
 
   // this warp's run of the vocabulary
   W w;
-  w.set(p_row(row), refused && d.draft_probs ? q_row(row) : nullptr, d.vocab, refused && !d.draft_probs ? wrong : -1);
+  w.set(p_row(row), refused && d.draft_probs ? q_row(row) : nullptr, static_cast<int>(d.vocab), refused && !d.draft_probs ? wrong : -1);
   const int warps = ctas * kVerifyWarps, me = rank * kVerifyWarps + warp;
-  const int64_t run = ((w.vectors() + warps - 1) / warps + 31) / 32 * 32;
-  int64_t k0 = min(me * run, w.vectors()), k1 = min(k0 + run, w.vectors());
-  const double u = u_sample > 0.0f ? static_cast<double>(u_sample) : 0.0;
+  const int run = ((w.vectors() + warps - 1) / warps + 31) / 32 * 32;
+  int k0 = min(me * run, w.vectors()), k1 = min(k0 + run, w.vectors());
+  const float u = u_sample > 0.0f ? u_sample : 0.0f;
   const int per = (warps + 31) / 32;            // warps' sums of a lane, at most 4
-  double before = 0.0, target = 0.0;
+  Pair before, target;
   int owner = -1;
-  bool any = false;
+  bool any = false, beyond = false;
   for (int pass = 0; pass < 4; ++pass) {
-    double sum = w.sum(k0 + lane, k1, 32);
+    Pair sum = w.sum(k0 + lane, k1, 32);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) sums[pass & 1][warp] = sum;
+    for (int o = 16; o > 0; o >>= 1) sum.add(Pair{__shfl_xor_sync(kAll, sum.hi, o), __shfl_xor_sync(kAll, sum.lo, o)});
+    // to every CTA of the cluster
+    if (pass == 0) cluster_wait();
+    if (lane < ctas) st_cluster_pair(cluster_map_shared(smem_u32(&sums[pass & 1][me]), lane), sum);
     __syncwarp();
     cluster_sync_all();
     // every warp: all warps' sums, in the vocabulary's order
-    double x[4], mine = 0.0;
+    Pair x[4], mine;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int at = lane * per + i;
-      x[i] = i < per && at < warps ? ld_cluster_f64(cluster_map_shared(smem_u32(&sums[pass & 1][at % kVerifyWarps]), at / kVerifyWarps)) : 0.0;
+      if (i < per && at < warps) x[i] = sums[pass & 1][at];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < per) mine += x[i];
-    const double upto = warp_prefix(mine);
-    const double total = __shfl_sync(kAll, upto, 31);
-    if (!isfinite(total) && !w.careful) {       // infinities among the entries: without them
+      if (i < per) mine.add(x[i]);
+    Pair at, upto = warp_prefix(mine, at);
+    const Pair total = shfl(upto, 31);
+    if (!(fabsf(total.hi) <= FLT_MAX) && !w.careful) {       // infinities among the entries: without them
       w.careful = true;
       continue;
     }
-    any = total > 0.0;
+    any = total.hi > 0.0f;
     if (!any && refused && (w.q != nullptr || w.without >= 0)) {
-      w.set(p_row(row), nullptr, d.vocab, -1);    // nothing is left of the target's distribution: all of it
-      // (its vectors are the same ones)
+      w.set(p_row(row), nullptr, static_cast<int>(d.vocab), -1);    // nothing is left of the target's distribution: all of it
       continue;
     }
-    target = u * total;
+    target.hi = __fmul_rn(u, total.hi);
+    target.lo = __fmaf_rn(u, total.lo, __fmaf_rn(u, total.hi, -target.hi));
     // the first warp whose sums pass the target, or the last that has some
     int first = -1, last = -1;
-    double at = upto - mine, from = 0.0;
+    Pair from;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < per) {
-        const double next = i + 1 == per ? upto : at + x[i];
-        if (first < 0 && next > target) {
+        const Pair next = i + 1 == per ? upto : plus(at, x[i]);
+        if (first < 0 && next.above(target)) {
           first = lane * per + i;
           from = at;
         }
-        if (x[i] > 0.0) last = lane * per + i;
+        if (x[i].hi > 0.0f) last = lane * per + i;
         at = next;
       }
     const uint32_t over = __ballot_sync(kAll, first >= 0), some = __ballot_sync(kAll, last >= 0);
     if (over) {
       owner = __shfl_sync(kAll, first, __ffs(over) - 1);
-      before = __shfl_sync(kAll, from, __ffs(over) - 1);
+      before = shfl(from, __ffs(over) - 1);
     } else if (some) {
       owner = __shfl_sync(kAll, last, 31 - __clz(some));
-      target = INFINITY;
+      beyond = true;                              // u of 1 or more
     }
     break;
   }
-  __syncwarp();
-  cluster_sync_relaxed();                       // the others have read this CTA's sums
   if (rank == 0) {
     for (int i = threadIdx.x; i < d.max_out; i += kVerifyThreads)
       if (i != taken) out[i] = i < taken ? d.tokens[s0 + 1 + i] : -1;
@@ -333,33 +359,29 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
       if (!any || (refused && (wrong < 0 || wrong >= d.vocab))) set_err(d.err, MOE_DEV_BAD_INDEX);
     }
   }
-  if (!any || owner != me) return;
-  // the vector in the run, a 32nd at a time
-  for (;;) {
-    const int64_t piece = (k1 - k0 + 31) / 32, f = min(k0 + lane * piece, k1), t = min(f + piece, k1);
-    const double x = w.sum(f, t, 1), upto = warp_prefix(x);
-    const uint32_t over = __ballot_sync(kAll, x > 0.0 && before + upto > target), some = __ballot_sync(kAll, x > 0.0);
-    // rounding may leave the border just behind the run: then its last entry
-    const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
-    if (!over) target = INFINITY;
-    before += __shfl_sync(kAll, upto - x, at);
-    k0 = __shfl_sync(kAll, f, at);
-    k1 = __shfl_sync(kAll, t, at);
-    if (piece <= 1) break;
-  }
-  if (lane == 0) {
-    float s[W::kVec], e[W::kVec];
-    w.get(k0, s, e);
-    int found = -1, last = 0;
-#pragma unroll
-    for (int i = 0; i < W::kVec; ++i) {
-      before += static_cast<double>(s[i]) + static_cast<double>(e[i]);
-      if (s[i] > 0.0f) {
-        last = i;
-        if (found < 0 && before > target) found = i;
-      }
+  if (any && owner == me) {
+    // the entry in the run, a 32nd of it at a time and then an entry a lane
+    while ((k1 - k0) * W::kVec > 32) {
+      const int piece = (k1 - k0 + 31) / 32, f = min(k0 + lane * piece, k1), t = min(f + piece, k1);
+      const Pair x = w.sum(f, t, 1);
+      Pair ahead;
+      const Pair upto = warp_prefix(x, ahead);
+      const uint32_t over = __ballot_sync(kAll, !beyond && x.hi > 0.0f && plus(before, upto).above(target));
+      const uint32_t some = __ballot_sync(kAll, x.hi > 0.0f);
+      // rounding may leave the border just behind the run: then its last entry
+      const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
+      beyond |= over == 0;
+      before.add(shfl(ahead, at));
+      k0 = __shfl_sync(kAll, f, at);
+      k1 = __shfl_sync(kAll, t, at);
     }
-    out[taken] = static_cast<int32_t>(k0 * W::kVec - w.shift + (found >= 0 ? found : last));
+    const int j = k0 * W::kVec - w.shift + lane;
+    Pair x, ahead;
+    if (lane < (k1 - k0) * W::kVec) x = w.entry(j);
+    const bool some_of_it = x.hi > 0.0f;
+    const Pair upto = warp_prefix(x, ahead);
+    const uint32_t over = __ballot_sync(kAll, !beyond && some_of_it && plus(before, upto).above(target)), some = __ballot_sync(kAll, some_of_it);
+    if (lane == (over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0)) out[taken] = j;
   }
 }
 
