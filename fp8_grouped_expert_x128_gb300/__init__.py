@@ -667,49 +667,76 @@ _kv_pages_pack = struct.Struct("@13Q3q4i").pack
 _verify_pack = struct.Struct("@12Q5q4i").pack
 
 
-def _here(device, name):
+_current_device = torch._C._cuda_getDevice
+
+
+# The checks of these calls pass quickly and leave the telling of what is wrong to
+# functions that run only then.
+def _here(t, name):
     """The library launches on the current GPU, so that is where a call's tensors have to be."""
+    device = t.get_device()
     if device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
+        return ValueError(f"{name} must be a CUDA tensor")
     if torch.cuda.current_device() != device:
-        raise ValueError(f"{name}: on GPU {device}, but GPU {torch.cuda.current_device()} is current (torch.cuda.set_device)")
+        return ValueError(f"{name}: on GPU {device}, but GPU {torch.cuda.current_device()} is current (torch.cuda.set_device)")
+    return None
 
 
-def _rows2d(t, name, shape, dtype, device):
-    """Row stride of a 2-D tensor whose rows are contiguous."""
-    ld, one = t.stride() if t.dim() == 2 else (0, 0)
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or (one != 1 and shape[1] > 1):
-        raise ValueError(f"{name}: expected {dtype} {list(shape)} on GPU {device} with contiguous rows, got {t.dtype} "
-                         f"{list(t.shape)}, strides {list(t.stride())}, GPU {t.get_device()}")
-    return ld if shape[0] > 1 else shape[1]              # one row's stride is never used, and may be anything
+def _is_rows(t, rows, cols, dtype, device):
+    """A [rows, cols] tensor of contiguous rows."""
+    shape = t.shape
+    return (len(shape) == 2 and shape[0] == rows and shape[1] == cols and (cols == 1 or t.stride(1) == 1) and t.dtype is dtype
+            and t.get_device() == device)
 
 
-def _flat(t, name, n, dtype, device):
-    """Address of a contiguous 1-D tensor of n elements, 0 for None."""
-    if t is None:
-        return 0
-    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} [{n}] on GPU {device}, got {t.dtype} {list(t.shape)}, strides "
-                         f"{list(t.stride())}, GPU {t.get_device()}")
-    return t.data_ptr()
+def _is_flat(t, n, dtype, device):
+    """A contiguous tensor of n elements."""
+    return t.numel() == n and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+
+
+def _not_as_wanted(where, *wanted):
+    """What is wrong among (tensor, name, shape, dtype); the first one is where the call runs."""
+    first = wanted[0][0]
+    wrong = _here(first, wanted[0][1])
+    if wrong:
+        return wrong
+    for t, name, shape, dtype in wanted:
+        if t is None:
+            continue
+        ok = _is_rows(t, *shape, dtype, first.get_device()) if len(shape) == 2 else _is_flat(t, *shape, dtype, first.get_device())
+        if not ok:
+            return ValueError(f"{name}: expected {dtype} {list(shape)} with contiguous rows on GPU {first.get_device()}, got {t.dtype} "
+                              f"{list(t.shape)}, strides {list(t.stride())}, GPU {t.get_device()}")
+    return ValueError(f"{where}: tensors not as moe_fp8.h has them")
 
 
 def _step_err(err, device):
-    return 0 if err is None else _flat(err, "err", 1, torch.int32, device)
+    if err is None:
+        return 0
+    if not _is_flat(err, 1, torch.int32, device):
+        raise ValueError("err: expected an int32 word on the call's GPU (new_error_word)")
+    return err.data_ptr()
 
 
 def moe_gate(x, w, logits, err=None, stream=None):
     """Router logits: x [T, H] and w [E, H] (both bf16 or both f16, contiguous rows) ->
     logits fp32 [T, E], summed in fp32.  See moe_fp8.h for the limits."""
-    device, dtype = x.get_device(), x.dtype
-    _here(device, "x")
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise ValueError(f"x: expected bfloat16 or float16, got {dtype}")
     T, H = x.shape
     E = w.shape[0]
-    d = _gate_pack(x.data_ptr(), w.data_ptr(), logits.data_ptr(), _step_err(err, device), T, _rows2d(x, "x", (T, H), dtype, device),
-                   _rows2d(w, "w", (E, H), dtype, device), _rows2d(logits, "logits", (T, E), torch.float32, device), E, H,
-                   _STEP_TYPES[dtype], 0)
+    dtype, device = x.dtype, x.get_device()
+    xt, x1 = x.stride()
+    wt, w1 = w.stride()
+    lt, l1 = logits.stride()
+    if not (device >= 0 and _current_device() == device and (dtype is torch.bfloat16 or dtype is torch.float16) and w.dtype is dtype
+            and x1 == 1 == w1 and (l1 == 1 or E == 1) and w.shape[1] == H and logits.shape == (T, E) and logits.dtype is torch.float32
+            and w.get_device() == device == logits.get_device()):
+        if dtype is not torch.bfloat16 and dtype is not torch.float16:
+            raise _here(x, "x") or ValueError(f"x: expected bfloat16 or float16, got {dtype}")
+        raise _not_as_wanted("moe_gate", (x, "x", (T, H), dtype), (w, "w", (E, H), dtype), (logits, "logits", (T, E), torch.float32))
+    if T == 1:                              # the stride of a single row is never used, and may be anything
+        xt, lt = H, E
+    d = _gate_pack(x.data_ptr(), w.data_ptr(), logits.data_ptr(), 0 if err is None else _step_err(err, device), T, xt, wt if E > 1 else H, lt,
+                   E, H, _STEP_TYPES[dtype], 0)
     rc = _lib.moe_gate(d, _stream_of(device, stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_gate")
@@ -722,16 +749,27 @@ def moe_route(logits, topk_ids, topk_w, bias=None, n_group=1, topk_group=1, scal
     bias: fp32 [E] added to the scores for the ranking alone; n_tokens: int32 [1], rows at
     and past it get id -1; flags: MOE_ROUTE_SOFTMAX (else sigmoid scores),
     MOE_ROUTE_RENORM, MOE_ROUTE_GROUP_PAIR."""
-    device, dtype = logits.get_device(), logits.dtype
-    _here(device, "logits")
-    if dtype not in _STEP_TYPES:
-        raise ValueError(f"logits: expected bfloat16, float16 or float32, got {dtype}")
     T, E = logits.shape
     k = topk_ids.shape[1]
-    d = _route_pack(logits.data_ptr(), _flat(bias, "bias", E, torch.float32, device), _flat(n_tokens, "n_tokens", 1, torch.int32, device),
-                    topk_ids.data_ptr(), topk_w.data_ptr(), T, _rows2d(logits, "logits", (T, E), dtype, device),
-                    _rows2d(topk_ids, "topk_ids", (T, k), torch.int32, device), _rows2d(topk_w, "topk_w", (T, k), torch.float32, device),
-                    scale, E, k, n_group, topk_group, _STEP_TYPES[dtype], flags)
+    dtype, device = logits.dtype, logits.get_device()
+    i32, f32 = torch.int32, torch.float32
+    lt, l1 = logits.stride()
+    it, i1 = topk_ids.stride()
+    wt, w1 = topk_w.stride()
+    rows = (T, k)
+    if not (device >= 0 and _current_device() == device and dtype in _STEP_TYPES and topk_ids.shape == rows == topk_w.shape
+            and (l1 == 1 or E == 1) and (i1 == 1 == w1 or k == 1) and topk_ids.dtype is i32 and topk_w.dtype is f32
+            and topk_ids.get_device() == device == topk_w.get_device()
+            and (bias is None or bias.dtype is f32 and bias.numel() == E and bias.get_device() == device and bias.is_contiguous())
+            and (n_tokens is None or n_tokens.dtype is i32 and n_tokens.numel() == 1 and n_tokens.get_device() == device and n_tokens.is_contiguous())):
+        if dtype not in _STEP_TYPES:
+            raise _here(logits, "logits") or ValueError(f"logits: expected bfloat16, float16 or float32, got {dtype}")
+        raise _not_as_wanted("moe_route", (logits, "logits", (T, E), dtype), (topk_ids, "topk_ids", (T, k), i32), (topk_w, "topk_w", (T, k), f32),
+                             (bias, "bias", (E,), f32), (n_tokens, "n_tokens", (1,), i32))
+    if T == 1:                              # the stride of a single row is never used, and may be anything
+        lt, it, wt = E, k, k
+    d = _route_pack(logits.data_ptr(), 0 if bias is None else bias.data_ptr(), 0 if n_tokens is None else n_tokens.data_ptr(),
+                    topk_ids.data_ptr(), topk_w.data_ptr(), T, lt, it, wt, scale, E, k, n_group, topk_group, _STEP_TYPES[dtype], flags)
     rc = _lib.moe_route(d, _stream_of(device, stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_route")
@@ -746,24 +784,35 @@ def moe_kv_pages(kv_old, n_new, page_table, free_list, free_count, page_size, kv
     stack of free_count[0] pages, of free_count_out[0] afterwards) and, where given, each
     new row's sequence, position (int32 [rows]) and slot page * page_size + offset (int64
     [rows]).  kv_len and kv_old, and the two counts, are different tensors."""
-    device = kv_old.get_device()
-    _here(device, "kv_old")
-    i32 = torch.int32
     batch, max_pages = page_table.shape
-    rows = 0
-    for t in (seqs, positions, slots):
-        if t is not None:
-            rows = t.shape[0]
-            break
-    else:
-        rows = 1 << 30                     # no row tensors: nothing limits the rows
-    d = _kv_pages_pack(_flat(kv_old, "kv_old", batch, i32, device), _flat(kv_keep, "kv_keep", batch, i32, device),
-                       _flat(n_new, "n_new", batch, i32, device), page_table.data_ptr(),
-                       _flat(free_list, "free_list", free_list.shape[0], i32, device), _flat(free_count, "free_count", 1, i32, device),
-                       _flat(kv_len, "kv_len", batch, i32, device), _flat(cu_new, "cu_new", batch + 1, i32, device),
-                       _flat(free_count_out, "free_count_out", 1, i32, device), _flat(seqs, "seqs", rows, i32, device),
-                       _flat(positions, "positions", rows, i32, device), _flat(slots, "slots", rows, torch.int64, device),
-                       _step_err(err, device), _rows2d(page_table, "page_table", (batch, max_pages), i32, device), free_list.shape[0],
+    device = kv_old.get_device()
+    i32 = torch.int32
+    given = seqs if seqs is not None else positions if positions is not None else slots
+    rows = given.numel() if given is not None else 1 << 30          # no row tensors: nothing limits the rows
+    pool = free_list.numel()
+    table_ld, table_1 = page_table.stride()
+    if not (device >= 0 and _current_device() == device and (table_1 == 1 or max_pages <= 1) and page_table.dtype is i32
+            and page_table.get_device() == device
+            and kv_old.dtype is i32 and kv_old.numel() == batch and kv_old.get_device() == device and kv_old.is_contiguous()
+            and n_new.dtype is i32 and n_new.numel() == batch and n_new.get_device() == device and n_new.is_contiguous()
+            and kv_len.dtype is i32 and kv_len.numel() == batch and kv_len.get_device() == device and kv_len.is_contiguous()
+            and cu_new.dtype is i32 and cu_new.numel() == batch + 1 and cu_new.get_device() == device and cu_new.is_contiguous()
+            and free_list.dtype is i32 and free_list.numel() == pool and free_list.get_device() == device and free_list.is_contiguous()
+            and free_count.dtype is i32 and free_count.numel() == 1 and free_count.get_device() == device and free_count.is_contiguous()
+            and free_count_out.dtype is i32 and free_count_out.numel() == 1 and free_count_out.get_device() == device and free_count_out.is_contiguous()
+            and (kv_keep is None or kv_keep.dtype is i32 and kv_keep.numel() == batch and kv_keep.get_device() == device and kv_keep.is_contiguous())
+            and (seqs is None or seqs.dtype is i32 and seqs.numel() == rows and seqs.get_device() == device and seqs.is_contiguous())
+            and (positions is None or positions.dtype is i32 and positions.numel() == rows and positions.get_device() == device and positions.is_contiguous())
+            and (slots is None or slots.dtype is torch.int64 and slots.numel() == rows and slots.get_device() == device and slots.is_contiguous())):
+        raise _not_as_wanted("moe_kv_pages", (kv_old, "kv_old", (batch,), i32), (n_new, "n_new", (batch,), i32), (kv_len, "kv_len", (batch,), i32),
+                             (cu_new, "cu_new", (batch + 1,), i32), (page_table, "page_table", (batch, max_pages), i32),
+                             (free_list, "free_list", (pool,), i32), (free_count, "free_count", (1,), i32),
+                             (free_count_out, "free_count_out", (1,), i32), (kv_keep, "kv_keep", (batch,), i32), (seqs, "seqs", (rows,), i32),
+                             (positions, "positions", (rows,), i32), (slots, "slots", (rows,), torch.int64))
+    d = _kv_pages_pack(kv_old.data_ptr(), 0 if kv_keep is None else kv_keep.data_ptr(), n_new.data_ptr(), page_table.data_ptr(),
+                       free_list.data_ptr(), free_count.data_ptr(), kv_len.data_ptr(), cu_new.data_ptr(), free_count_out.data_ptr(),
+                       0 if seqs is None else seqs.data_ptr(), 0 if positions is None else positions.data_ptr(),
+                       0 if slots is None else slots.data_ptr(), 0 if err is None else _step_err(err, device), table_ld if batch > 1 else max_pages, pool,
                        rows, batch, max_pages, page_size, 0)
     rc = _lib.moe_kv_pages(d, _stream_of(device, stream))
     if rc != MOE_OK:
@@ -779,23 +828,41 @@ def moe_verify_drafts(probs, tokens, cu_new, u_accept, u_sample, accepted, out_t
     (the taken drafts, the token behind them, -1) and kv_keep int32 [batch] =
     kv_len - rejected drafts.  n_draft int32 [batch]: drafts among a sequence's rows
     (None: all but the first)."""
-    device, dtype = probs.get_device(), probs.dtype
-    _here(device, "probs")
-    if dtype not in _STEP_TYPES:
-        raise ValueError(f"probs: expected bfloat16, float16 or float32, got {dtype}")
-    i32, f32 = torch.int32, torch.float32
     T, vocab = probs.shape
     batch, max_out = out_tokens.shape
+    dtype, device = probs.dtype, probs.get_device()
+    i32, f32 = torch.int32, torch.float32
+    p_ld, p1 = probs.stride()
+    o_ld, o1 = out_tokens.stride()
     q_ptr = q_ld = 0
+    q_ok = True
     if draft_probs is not None:
-        q_ptr, q_ld = draft_probs.data_ptr(), _rows2d(draft_probs, "draft_probs", (T, vocab), dtype, device)
-    d = _verify_pack(probs.data_ptr(), q_ptr, _flat(tokens, "tokens", T, i32, device), _flat(cu_new, "cu_new", batch + 1, i32, device),
-                     _flat(n_draft, "n_draft", batch, i32, device), _flat(u_accept, "u_accept", T, f32, device),
-                     _flat(u_sample, "u_sample", batch, f32, device), _flat(kv_len, "kv_len", batch, i32, device),
-                     _flat(accepted, "accepted", batch, i32, device), out_tokens.data_ptr(),
-                     _flat(kv_keep, "kv_keep", batch, i32, device), _step_err(err, device), T, vocab,
-                     _rows2d(probs, "probs", (T, vocab), dtype, device), q_ld,
-                     _rows2d(out_tokens, "out_tokens", (batch, max_out), i32, device), batch, max_out, _STEP_TYPES[dtype], 0)
+        q_ptr = draft_probs.data_ptr()
+        q_ld, q1 = draft_probs.stride()
+        q_ok = ((q1 == 1 or vocab == 1) and draft_probs.dtype is dtype and draft_probs.shape == probs.shape
+                and draft_probs.get_device() == device)
+    if not (device >= 0 and _current_device() == device and dtype in _STEP_TYPES and q_ok and (p1 == 1 or vocab == 1)
+            and (o1 == 1 or max_out == 1) and out_tokens.dtype is i32 and out_tokens.get_device() == device
+            and tokens.dtype is i32 and tokens.numel() == T and tokens.get_device() == device and tokens.is_contiguous()
+            and u_accept.dtype is f32 and u_accept.numel() == T and u_accept.get_device() == device and u_accept.is_contiguous()
+            and cu_new.dtype is i32 and cu_new.numel() == batch + 1 and cu_new.get_device() == device and cu_new.is_contiguous()
+            and u_sample.dtype is f32 and u_sample.numel() == batch and u_sample.get_device() == device and u_sample.is_contiguous()
+            and accepted.dtype is i32 and accepted.numel() == batch and accepted.get_device() == device and accepted.is_contiguous()
+            and (n_draft is None or n_draft.dtype is i32 and n_draft.numel() == batch and n_draft.get_device() == device and n_draft.is_contiguous())
+            and (kv_len is None or kv_len.dtype is i32 and kv_len.numel() == batch and kv_len.get_device() == device and kv_len.is_contiguous())
+            and (kv_keep is None or kv_keep.dtype is i32 and kv_keep.numel() == batch and kv_keep.get_device() == device and kv_keep.is_contiguous())):
+        if dtype not in _STEP_TYPES:
+            raise _here(probs, "probs") or ValueError(f"probs: expected bfloat16, float16 or float32, got {dtype}")
+        raise _not_as_wanted("moe_verify_drafts", (probs, "probs", (T, vocab), dtype), (draft_probs, "draft_probs", (T, vocab), dtype),
+                             (out_tokens, "out_tokens", (batch, max_out), i32), (tokens, "tokens", (T,), i32), (u_accept, "u_accept", (T,), f32),
+                             (cu_new, "cu_new", (batch + 1,), i32), (u_sample, "u_sample", (batch,), f32), (accepted, "accepted", (batch,), i32),
+                             (n_draft, "n_draft", (batch,), i32), (kv_len, "kv_len", (batch,), i32), (kv_keep, "kv_keep", (batch,), i32))
+    if T <= 1:                              # the stride of a single row is never used, and may be anything
+        p_ld = q_ld = vocab
+    d = _verify_pack(probs.data_ptr(), q_ptr, tokens.data_ptr(), cu_new.data_ptr(), 0 if n_draft is None else n_draft.data_ptr(),
+                     u_accept.data_ptr(), u_sample.data_ptr(), 0 if kv_len is None else kv_len.data_ptr(), accepted.data_ptr(),
+                     out_tokens.data_ptr(), 0 if kv_keep is None else kv_keep.data_ptr(), 0 if err is None else _step_err(err, device), T, vocab,
+                     p_ld, q_ld, o_ld if batch > 1 else max_out, batch, max_out, _STEP_TYPES[dtype], 0)
     rc = _lib.moe_verify_drafts(d, _stream_of(device, stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_verify_drafts")

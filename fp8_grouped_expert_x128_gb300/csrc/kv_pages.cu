@@ -28,25 +28,33 @@ struct Sums {      // over sequences: new tokens, pages taken, pages given back
   __device__ __forceinline__ Sums operator+(const Sums& o) const { return {n + o.n, take + o.take, back + o.back}; }
 };
 
+__device__ __forceinline__ Sums shfl_up(const Sums& v, int o) {
+  return {__shfl_up_sync(0xffffffffu, v.n, o), __shfl_up_sync(0xffffffffu, v.take, o), __shfl_up_sync(0xffffffffu, v.back, o)};
+}
+__device__ __forceinline__ Sums shfl(const Sums& v, int lane) {
+  return {__shfl_sync(0xffffffffu, v.n, lane), __shfl_sync(0xffffffffu, v.take, lane), __shfl_sync(0xffffffffu, v.back, lane)};
+}
+
 // Exclusive sums over the block's threads; `total` gets the sum of all.
 __device__ Sums block_scan(Sums v, Sums* part, Sums& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Sums x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Sums y{__shfl_up_sync(0xffffffffu, x.n, o), __shfl_up_sync(0xffffffffu, x.take, o), __shfl_up_sync(0xffffffffu, x.back, o)};
+    const Sums y = shfl_up(x, o);
     if (lane >= o) x = x + y;
   }
   __syncthreads();            // `part` of an earlier call has been read
   if (lane == 31) part[warp] = x;
   __syncthreads();
-  Sums before{0, 0, 0};
-  total = Sums{0, 0, 0};
-  for (int w = 0; w < kPagesThreads / 32; ++w) {
-    const Sums y = part[w];
-    if (w < warp) before = before + y;
-    total = total + y;
+  Sums w = lane < kPagesThreads / 32 ? part[lane] : Sums{0, 0, 0};
+#pragma unroll
+  for (int o = 1; o < kPagesThreads / 32; o <<= 1) {
+    const Sums y = shfl_up(w, o);
+    if (lane >= o) w = w + y;
   }
+  total = shfl(w, kPagesThreads / 32 - 1);
+  const Sums before = warp ? shfl(w, warp - 1) : Sums{0, 0, 0};
   return {before.n + x.n - v.n, before.take + x.take - v.take, before.back + x.back - v.back};
 }
 
@@ -90,9 +98,9 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const __grid_co
   };
   auto load = [&](int b) {
     Seq s;
-    s.old = d.kv_old[b];
-    s.keep = d.kv_keep ? d.kv_keep[b] : s.old;
-    s.n = d.n_new[b];
+    s.old = __ldg(d.kv_old + b);
+    s.n = __ldg(d.n_new + b);
+    s.keep = d.kv_keep ? __ldg(d.kv_keep + b) : s.old;
     s.bad = !list_ok || s.old < 0 || s.n < 0 || s.old > most || s.keep < 0 || s.keep > s.old;
     s.held = s.bad ? 0 : pages(s.old);
     s.want = static_cast<int64_t>(s.keep) + s.n;
@@ -204,35 +212,86 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const __grid_co
   // the i-th page given back, and the i-th page taken
   auto given = [&](int32_t i) {
     const int b = find_last(back0, B, i);
-    return *entry(b, need_of[b] + i - back0[b]);
+    return __ldg(entry(b, need_of[b] + i - back0[b]));
   };
   auto source = [&](int32_t i) {
     const int32_t at = f + back - 1 - i;
-    return at < f ? d.free_list[at] : given(at - f);
+    return at < f ? __ldg(d.free_list + at) : given(at - f);
   };
+  // page j of sequence b
+  auto lookup = [&](int b, int32_t j) { return j < held_of[b] ? __ldg(entry(b, j)) : source(take0[b] + j - held_of[b]); };
   for (int64_t i = first; i < taken; i += step) {
     const int b = find_last(take0, B, static_cast<int32_t>(i));
     *entry(b, held_of[b] + static_cast<int32_t>(i) - take0[b]) = source(static_cast<int32_t>(i));
   }
   for (int64_t i = first; i < static_cast<int64_t>(left) - f; i += step) d.free_list[f + i] = given(static_cast<int32_t>(i));
   if (d.seqs == nullptr && d.positions == nullptr && d.slots == nullptr) return;
-  for (int64_t r = first; r < d.rows; r += step) {
-    int32_t b = -1, pos = -1;
+  auto one_row = [&](int r, int b) {        // b: its sequence, -1 behind the last
+    int32_t pos = -1;
     int64_t slot = -1;
-    if (r < rows) {
-      b = find_last(row0, B, static_cast<int32_t>(r));
-      pos = keep_of[b] + static_cast<int32_t>(r) - row0[b];
-      if (d.slots) {
-        const int32_t j = pos >> a.shift;
-        const int32_t page = j < held_of[b] ? *entry(b, j) : source(take0[b] + j - held_of[b]);
-        slot = (static_cast<int64_t>(page) << a.shift) + (pos & (d.page_size - 1));
-      }
+    if (b >= 0) {
+      pos = keep_of[b] + r - row0[b];
+      if (d.slots) slot = (static_cast<int64_t>(lookup(b, pos >> a.shift)) << a.shift) + (pos & (d.page_size - 1));
     }
     if (d.seqs) d.seqs[r] = b;
     if (d.positions) d.positions[r] = pos;
     if (d.slots) d.slots[r] = slot;
+  };
+  if (d.rows <= step) {                  // few rows, mostly a sequence each
+    if (first < d.rows) one_row(first, first < rows ? find_last(row0, B, first) : -1);
+    return;
+  }
+  // four rows a thread: the search for their sequence, and mostly the page, are shared
+  const bool wide = ((reinterpret_cast<uintptr_t>(d.seqs) | reinterpret_cast<uintptr_t>(d.positions) | reinterpret_cast<uintptr_t>(d.slots)) & 15) == 0;
+  const int all_rows = static_cast<int>(d.rows), in_page = d.page_size - 1;
+  for (int64_t r64 = 4ll * first; r64 < all_rows; r64 += 4ll * step) {
+    const int r0 = static_cast<int>(r64);
+    int seq[4], pos[4];
+    int64_t slot[4];
+    int b = r0 < rows ? find_last(row0, B, r0) : 0, end = row0[b + 1], from = keep_of[b] - row0[b], page_of = -1, page = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + i;
+      seq[i] = pos[i] = -1;
+      slot[i] = -1;
+      if (r < rows) {
+        while (r >= end) {
+          end = row0[++b + 1];
+          from = keep_of[b] - row0[b];
+          page_of = -1;
+        }
+        seq[i] = b;
+        pos[i] = from + r;
+        const int j = pos[i] >> a.shift;
+        if (d.slots != nullptr && j != page_of) {
+          page = lookup(b, j);
+          page_of = j;
+        }
+        slot[i] = (static_cast<int64_t>(page) << a.shift) + (pos[i] & in_page);
+      }
+    }
+    if (wide && r0 + 4 <= all_rows) {
+      if (d.seqs) *reinterpret_cast<int4*>(d.seqs + r0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+      if (d.positions) *reinterpret_cast<int4*>(d.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      if (d.slots) {
+        *reinterpret_cast<longlong2*>(d.slots + r0) = make_longlong2(slot[0], slot[1]);
+        *reinterpret_cast<longlong2*>(d.slots + r0 + 2) = make_longlong2(slot[2], slot[3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r0 + i < all_rows) {
+          if (d.seqs) d.seqs[r0 + i] = seq[i];
+          if (d.positions) d.positions[r0 + i] = pos[i];
+          if (d.slots) d.slots[r0 + i] = slot[i];
+        }
+    }
   }
 }
+
+// Six arrays of a sequence each, three of them with an entry more, and room for one more
+// sequence, which is looked at (and not used) where there is none.
+inline size_t pages_smem_bytes(int batch) { return sizeof(int32_t) * (6 * (static_cast<size_t>(batch) + 1) + 3); }
 
 struct Range {
   const void* p;
@@ -271,12 +330,13 @@ extern "C" int moe_kv_pages(const moe_kv_pages_desc* d, void* stream) {
   if (int rc = check_device()) return rc;
   PagesArgs a{*d, 0};
   while ((1 << a.shift) < d->page_size) ++a.shift;
-  // a CTA for 4096 rows, and for 16 sequences, whose pages may all go back
+  // a CTA for every 512 rows, and for 16 sequences, whose pages may all go back
   const int64_t told = d->seqs || d->positions || d->slots ? d->rows : 0;
-  int64_t ctas = std::max<int64_t>((told + 4095) / 4096, (d->batch + 15) / 16);
-  ctas = std::min<int64_t>(std::max<int64_t>(ctas, 1), num_sms());
-  const size_t smem = sizeof(int32_t) * (6 * static_cast<size_t>(d->batch) + 3);
+  const int64_t ctas = std::min<int64_t>(std::max<int64_t>({(told + kPagesThreads - 1) / kPagesThreads, (d->batch + 15) / 16, 1}),
+                                         (d->batch <= kPagesMaxBatch / 2 ? 2 : 1) * num_sms());
+  const size_t smem = pages_smem_bytes(d->batch);
   if (smem > 48 * 1024)
-    MOE_CUDA_TRY(cudaFuncSetAttribute(kv_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (6 * kPagesMaxBatch + 3)));
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kv_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(pages_smem_bytes(kPagesMaxBatch))));
   return launch_pdl(kv_pages_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPagesThreads), smem, as_stream(stream), a);
 }

@@ -163,6 +163,8 @@ def test_everything_at_once(lib):
     """No sequences, no rows, empty sequences, a cache that fills and empties whole."""
     State([], [], [], 16, spare=5, max_pages=4, rows=0).check(lib)
     State([], [], [], 16, spare=5, max_pages=4, rows=7).check(lib)
+    State([], [], [], 16, spare=5, max_pages=4, rows=5000).check(lib)
+    State([3], [3], [1], 16, spare=5, max_pages=4, rows=200001).check(lib)
     State([0, 0, 0], [0, 0, 0], [0, 0, 0], 16, spare=0, max_pages=4).check(lib)
     State([64] * 50, [0] * 50, [0] * 50, 16, spare=0, max_pages=4).check(lib)             # all end
     State([0] * 50, [0] * 50, [64] * 50, 16, spare=200, max_pages=4).check(lib)           # all begin, to the last page
