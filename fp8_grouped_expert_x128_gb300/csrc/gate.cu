@@ -85,11 +85,11 @@ __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uin
 }
 
 // A copy into this CTA whose barrier may be the even CTA's of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t bar, int32_t x, int32_t y) {
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t bar, int32_t x, int32_t y, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
       : "memory");
 }
 
@@ -181,6 +181,8 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t n = 2 / G::kSub * (kb1 - kb0), full_even = kPair ? cluster_map_shared(full0, rank - side) : full0;
+      // tokens that only this tile reads leave the L2 first, the gate stays
+      const uint64_t px = p.n_tiles == 1 ? l2_policy_evict_first() : l2_policy_evict_normal(), pw = l2_policy_evict_last();
       uint32_t it = 0, s = 0, ph = 1;
       for (; it < n; ++it) {
         if (!wait(empty0 + 8 * s, ph)) break;
@@ -190,8 +192,8 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
           const int32_t col = (2 * kb0 + static_cast<int32_t>(it) * G::kSub + i) * kCols;
           const uint32_t to = tiles + s * stage_bytes + i * box_bytes;
           if constexpr (kPair) {
-            tma_load_2d_pair(to, &tmX, full_even + 8 * s, col, static_cast<int32_t>(t0));
-            tma_load_2d_pair(to + x_bytes, &tmW, full_even + 8 * s, col, e0 + side * G::kWRows);
+            tma_load_2d_pair(to, &tmX, full_even + 8 * s, col, static_cast<int32_t>(t0), px);
+            tma_load_2d_pair(to + x_bytes, &tmW, full_even + 8 * s, col, e0 + side * G::kWRows, pw);
           } else {
             tma_load_2d(to, &tmX, full0 + 8 * s, col, static_cast<int32_t>(t0));
             tma_load_2d(to + x_bytes, &tmW, full0 + 8 * s, col, e0);

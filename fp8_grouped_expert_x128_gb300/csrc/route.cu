@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
 #pragma unroll
     for (int i = 1; i < VPL; ++i) most = max(most, key[i]);
     if constexpr (VPL > 1) {
-#pragma unroll 1
+#pragma unroll 4
       for (int j = 0; j <= d.k; ++j) {
         least = __reduce_max_sync(kAll, most);
         most = most == least ? 0u : most;
