@@ -345,10 +345,10 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
   }
 }
 
-// Up to 8 tokens: a tile would be idle, and what counts is how soon the gate's rows are
+// Up to 16 tokens: a tile would be idle, and what counts is how soon the gate's rows are
 // here.  A CTA takes EB experts whole, its threads 8 columns at a time.
 constexpr int kFewThreads = 256;
-constexpr int kFewTokens = 8;
+constexpr int kFewTokens = 16;
 
 template <int TT, int EB, bool F16>
 __global__ void __launch_bounds__(kFewThreads) gate_few_kernel(const __grid_constant__ moe_gate_desc d) {
@@ -407,11 +407,12 @@ __global__ void __launch_bounds__(kFewThreads) gate_few_kernel(const __grid_cons
 
 template <int TT, bool F16>
 int launch_few(const moe_gate_desc& d, cudaStream_t st) {
-  // a CTA for every SM, and no more than two of them
+  // a CTA for every SM, and no more than two of them while the sums fit a thread's registers
   const int sms = num_sms();
   if (d.E <= sms) return launch_pdl(gate_few_kernel<TT, 1, F16>, dim3(d.E), dim3(kFewThreads), 0, st, d);
-  if (d.E <= 2 * sms) return launch_pdl(gate_few_kernel<TT, 2, F16>, dim3((d.E + 1) / 2), dim3(kFewThreads), 0, st, d);
-  return launch_pdl(gate_few_kernel<TT, 4, F16>, dim3((d.E + 3) / 4), dim3(kFewThreads), 0, st, d);
+  if (d.E <= 2 * sms || TT > 8) return launch_pdl(gate_few_kernel<TT, 2, F16>, dim3((d.E + 1) / 2), dim3(kFewThreads), 0, st, d);
+  if constexpr (TT <= 8) return launch_pdl(gate_few_kernel<TT, 4, F16>, dim3((d.E + 3) / 4), dim3(kFewThreads), 0, st, d);
+  return MOE_ERR_UNSUPPORTED;
 }
 
 // A choice of tile and split, and what it takes.
@@ -430,8 +431,11 @@ size_t gate_smem(int bn, bool pair, int box_rows, int stages) {
   return 1024 + std::max(ring, static_cast<size_t>(box_rows) * (bn + 4) * 4);
 }
 
-// Estimated clock cycles of the choices, the least of them: a CTA takes in some 56 bytes a
-// cycle and multiplies 128 x bn x 64 in 2 bn, and costs a few thousand to start and end.
+// Estimated clock cycles of the choices, the least of them: a CTA takes in some 45 bytes a
+// cycle, 1500 cycles after it asked, multiplies 128 x bn x 64 in 2 bn, and costs a few
+// thousand to start and end.  Swept against every choice (17 to 6000 tokens; 8, 64, 160, 256
+// and 512 experts, 70 sizes): the one taken is within 5% of the fastest at 59 of them, 26%
+// slower at worst (700 tokens by 512 experts, 11.5 us for 9.1).
 GatePlan plan_gate(int64_t T, int E, int H, int box_rows, int sms) {
   GatePlan best{};
   double least = 1e300;
@@ -446,21 +450,23 @@ GatePlan plan_gate(int64_t T, int E, int H, int box_rows, int sms) {
         const int sub = bn <= 128 ? 2 : 1;
         const double stage = sub * (box_rows + (pair ? bn / 2 : bn)) * 128.0;
         const int n = 2 / sub * ((blocks + splits - 1) / splits);
-        int stages = std::min(kMaxStages, static_cast<int>((bn >= 128 ? 196608.0 : 98304.0) / stage));
-        stages = std::max(1, std::min(stages, n));
-        const size_t smem = gate_smem(bn, pair, box_rows, stages);
-        const int on_sm = smem <= 110 * 1024 ? 2 : 1;
-        // clusters that an even share of a GPC's SMs does not hold leave SMs idle
-        const int64_t room = cluster <= 2 ? sms : cluster == 4 ? sms - sms / 19 : sms - sms / 19 * 4;
-        const int64_t waves = (ctas + room * on_sm - 1) / (room * on_sm);
-        const double shared = ctas > room && on_sm == 2 ? 2.0 : 1.0;
-        const double step = std::max({shared * stage / 56.0, shared * 2.0 * bn * sub, 300.0 * sub});
-        const double rows = std::min<int64_t>(kTile, T);
-        const double end = 3000.0 + (cluster > 1 ? 1000.0 : 0.0) + rows * bn * 4.0 / (splits > 1 ? 20.0 : 40.0);
-        const double cycles = waves * (end + n * step);
-        if (cycles < least) {
-          least = cycles;
-          best = GatePlan{bn, splits, stages, pair != 0, smem, ctas};
+        for (const double room_for : {98304.0, 196608.0}) {       // two CTAs on an SM, or one
+          const int stages = std::max(1, std::min({kMaxStages, static_cast<int>(room_for / stage), n}));
+          const size_t smem = gate_smem(bn, pair, box_rows, stages);
+          if (smem > kMaxSmemPerBlock) continue;
+          const int on_sm = smem <= 110 * 1024 ? 2 : 1;
+          // clusters that an even share of a GPC's SMs does not hold leave SMs idle
+          const int64_t room = cluster <= 2 ? sms : cluster == 4 ? sms - sms / 19 : sms - sms / 19 * 4;
+          const int64_t waves = (ctas + room * on_sm - 1) / (room * on_sm);
+          const double shared = ctas > room && on_sm == 2 ? 2.0 : 1.0, feed = shared * stage / 45.0;
+          const double step = std::max({feed, shared * 2.0 * bn * sub, 300.0 * sub, (1500.0 + feed) / stages});
+          const double rows = std::min<int64_t>(kTile, T);
+          const double end = 3000.0 + (cluster > 1 ? 1000.0 : 0.0) + rows * bn * 4.0 / (splits > 1 ? 32.0 : 40.0);
+          const double cycles = waves * (end + n * step);
+          if (cycles < least) {
+            least = cycles;
+            best = GatePlan{bn, splits, stages, pair != 0, smem, ctas};
+          }
         }
       }
   return best;
@@ -491,7 +497,8 @@ int run_gate(const moe_gate_desc& d, cudaStream_t st) {
   if (d.T == 1) return launch_few<1, F16>(d, st);
   if (d.T == 2) return launch_few<2, F16>(d, st);
   if (d.T <= 4) return launch_few<4, F16>(d, st);
-  if (d.T <= kFewTokens) return launch_few<8, F16>(d, st);
+  if (d.T <= 8) return launch_few<8, F16>(d, st);
+  if (d.T <= kFewTokens) return launch_few<16, F16>(d, st);
   const int box_rows = static_cast<int>(std::min<int64_t>(kTile, (d.T + 7) / 8 * 8));
   const GatePlan plan = plan_gate(d.T, d.E, d.H, box_rows, num_sms());
   if (plan.ctas > INT32_MAX) return MOE_ERR_UNSUPPORTED;
