@@ -530,6 +530,9 @@ extern "C" int moe_gate(const moe_gate_desc* d, void* stream) {
     return MOE_ERR_UNSUPPORTED;
   if (d->T == 0) return MOE_OK;
   MOE_CHECK_ARG(d->x && d->w && d->logits && aligned16(d->x) && aligned16(d->w) && (reinterpret_cast<uintptr_t>(d->logits) & 3) == 0);
+  const int64_t out = 4 * ((d->T - 1) * d->logits_ld + d->E);
+  MOE_CHECK_ARG(!memory_overlaps(d->logits, out, d->x, 2 * ((d->T - 1) * d->x_ld + d->H)) &&
+                !memory_overlaps(d->logits, out, d->w, 2 * ((d->E - 1ll) * d->w_ld + d->H)));
   if (int rc = check_device()) return rc;
   return d->dtype == MOE_DTYPE_F16 ? run_gate<true>(*d, as_stream(stream)) : run_gate<false>(*d, as_stream(stream));
 }

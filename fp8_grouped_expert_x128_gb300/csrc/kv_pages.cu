@@ -297,10 +297,7 @@ struct Range {
   const void* p;
   int64_t bytes;
 };
-inline bool overlap(const Range& a, const Range& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
-}
+inline bool overlap(const Range& a, const Range& b) { return memory_overlaps(a.p, a.bytes, b.p, b.bytes); }
 
 }  // namespace
 }  // namespace moe

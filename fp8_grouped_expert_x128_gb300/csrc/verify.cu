@@ -13,6 +13,7 @@
 // and a warp's holds up the SM's other warps), so sums are pairs of fp32 (D. E. Knuth's
 // two-sum, TAOCP vol. 2, 4.2.2: sum and rounding error of two numbers as two numbers).
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 
@@ -392,6 +393,15 @@ int launch_verify(const VerifyArgs& a, cudaStream_t st) {
   const int64_t vectors = a.d.vocab / Weights<DT>::kVec + 2, B = a.d.batch;
   int ctas = 16 * B <= 112 ? 16 : 8;
   while (ctas > 1 && (B * ctas > 8 * num_sms() || (ctas / 2) * kVerifyWarps * 32 >= vectors)) ctas /= 2;
+  if (ctas > 8) {
+    static std::atomic<uint64_t> allowed{0};      // a bit for each GPU that has been told
+    int dev = 0;
+    MOE_CUDA_TRY(cudaGetDevice(&dev));
+    if (!((allowed.load() >> (dev & 63)) & 1)) {
+      MOE_CUDA_TRY(cudaFuncSetAttribute(verify_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+      allowed.fetch_or(1ull << (dev & 63));
+    }
+  }
   for (int32_t b0 = 0; b0 < a.d.batch; b0 += 65535) {      // a grid's second dimension
     VerifyArgs part = a;
     part.d.batch = std::min(a.d.batch - b0, 65535);
@@ -414,7 +424,6 @@ int launch_verify(const VerifyArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (ctas > 8) MOE_CUDA_TRY(cudaFuncSetAttribute(verify_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     if (cudaLaunchKernelEx(&cfg, verify_kernel<DT>, part) != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;

@@ -603,10 +603,12 @@ int moe_kv_attention(const moe_kv_attention_desc *desc, void *workspace, size_t 
  *   logits[t, e] = sum_h x[t, h] * w[e, h]          (fp32)
  * x: device [T, H], w: device [E, H], both of one type (MOE_DTYPE_BF16 or
  * MOE_DTYPE_F16); row strides in elements, multiples of 8, at least H, below 2^31;
- * logits: device fp32 [T, E], row stride at least E.  Products are exact; they are summed on the tensor cores over 128 columns at
- * a time, and these sums in fp32, rounded to nearest.  Results repeat bit for bit.
+ * logits: device fp32 [T, E], row stride at least E.  Products are exact.  Up to 16
+ * tokens they are summed in fp32, rounded to nearest; above that on the tensor cores over
+ * 512 columns at a time (which cuts what it adds, towards zero: some 2^-21 of a logit's
+ * size in all), and these sums in fp32.  Results repeat bit for bit.
  * Limits: H a multiple of 8, up to 2^20; E up to 1024; T up to 2^24.  T may be 0
- * (nothing is launched).  logits must not overlap x or w.
+ * (nothing is launched).  logits that overlap x or w are refused.
  */
 #define MOE_DTYPE_F32 2
 

@@ -28,7 +28,8 @@ def bound(x, w):
 @pytest.mark.parametrize("T,E,H", [(1, 1, 8), (1, 256, 7168), (2, 16, 64), (3, 17, 72), (31, 60, 2040), (64, 256, 512), (128, 128, 128),
                                    (129, 257, 136), (130, 1024, 264), (200, 300, 1000), (257, 8, 4096), (333, 60, 2040), (1000, 512, 192),
                                    (5000, 64, 256), (4097, 255, 520), (7, 31, 8200), (20000, 33, 128), (16461, 256, 264),
-                                   (3000, 512, 7168), (8193, 200, 2048), (900, 129, 1032)])
+                                   (3000, 512, 7168), (8193, 200, 2048), (900, 129, 1032), (9, 300, 72), (16, 1024, 7168),
+                                   (13, 5, 8), (12, 200, 2056), (16, 153, 4104), (8, 305, 520), (17, 256, 7168), (700, 512, 4096)])
 def test_logits(lib, T, E, H, dtype):
     x, w = made(T, E, H, dtype, seed=T + E)
     out = Guarded((T, E), torch.float32, f32_bits(SENTINEL_F32))

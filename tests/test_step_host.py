@@ -50,7 +50,8 @@ def verify(moe, **kw):
     (dict(logits=(1 << 24) + 2), -1), (dict(T=-1), -1), (dict(E=0), -1), (dict(H=0), -1), (dict(H=60), -1), (dict(x_ld=56), -1),
     (dict(x_ld=68), -1), (dict(w_ld=60), -1), (dict(logits_ld=9), -1), (dict(dtype=2), -1), (dict(dtype=-1), -1), (dict(flags=1), -1),
     (dict(E=1025, logits_ld=2000), -2), (dict(H=1 << 21, x_ld=1 << 21, w_ld=1 << 21), -2), (dict(T=(1 << 24) + 1), -2),
-    (dict(x_ld=1 << 31), -2), (dict(logits_ld=1 << 31), -2)])
+    (dict(x_ld=1 << 31), -2), (dict(logits_ld=1 << 31), -2),
+    (dict(logits=256 + 512), -1), (dict(logits=(1 << 20) - 4 * 49), -1)])      # on x, into w
 def test_gate_refusals(moe, bad, rc):
     assert gate(moe, **bad) == rc
 
