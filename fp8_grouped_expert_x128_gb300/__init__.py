@@ -669,6 +669,15 @@ _verify_pack = struct.Struct("@12Q5q4i").pack
 
 _current_device = torch._C._cuda_getDevice
 
+# The quick way (csrc/binding.cpp): 0 or the library's status, or 1 where a call is to be
+# looked at here.  It knows the current stream only.
+try:
+    from . import _binding as _native
+    _native.connect(*(ctypes.cast(getattr(_lib, _name), ctypes.c_void_p).value
+                      for _name in ("moe_gate", "moe_route", "moe_kv_pages", "moe_verify_drafts")))
+except ImportError:
+    _native = None
+
 
 # The checks of these calls pass quickly and leave the telling of what is wrong to
 # functions that run only then.
@@ -721,6 +730,12 @@ def _step_err(err, device):
 def moe_gate(x, w, logits, err=None, stream=None):
     """Router logits: x [T, H] and w [E, H] (both bf16 or both f16, contiguous rows) ->
     logits fp32 [T, E], summed in fp32.  See moe_fp8.h for the limits."""
+    if stream is None and _native is not None:
+        rc = _native.gate(x, w, logits, err)
+        if rc == MOE_OK:
+            return logits
+        if rc < 0:
+            raise MoeError(rc, "moe_gate")
     T, H = x.shape
     E = w.shape[0]
     dtype, device = x.dtype, x.get_device()
@@ -749,6 +764,12 @@ def moe_route(logits, topk_ids, topk_w, bias=None, n_group=1, topk_group=1, scal
     bias: fp32 [E] added to the scores for the ranking alone; n_tokens: int32 [1], rows at
     and past it get id -1; flags: MOE_ROUTE_SOFTMAX (else sigmoid scores),
     MOE_ROUTE_RENORM, MOE_ROUTE_GROUP_PAIR."""
+    if stream is None and _native is not None:
+        rc = _native.route(logits, topk_ids, topk_w, bias, n_tokens, n_group, topk_group, scale, flags)
+        if rc == MOE_OK:
+            return topk_ids, topk_w
+        if rc < 0:
+            raise MoeError(rc, "moe_route")
     T, E = logits.shape
     k = topk_ids.shape[1]
     dtype, device = logits.dtype, logits.get_device()
@@ -784,6 +805,13 @@ def moe_kv_pages(kv_old, n_new, page_table, free_list, free_count, page_size, kv
     stack of free_count[0] pages, of free_count_out[0] afterwards) and, where given, each
     new row's sequence, position (int32 [rows]) and slot page * page_size + offset (int64
     [rows]).  kv_len and kv_old, and the two counts, are different tensors."""
+    if stream is None and _native is not None:
+        rc = _native.kv_pages(kv_old, n_new, page_table, free_list, free_count, page_size, kv_len, cu_new, free_count_out, kv_keep, seqs,
+                              positions, slots, err)
+        if rc == MOE_OK:
+            return None
+        if rc < 0:
+            raise MoeError(rc, "moe_kv_pages")
     batch, max_pages = page_table.shape
     device = kv_old.get_device()
     i32 = torch.int32
@@ -828,6 +856,12 @@ def moe_verify_drafts(probs, tokens, cu_new, u_accept, u_sample, accepted, out_t
     (the taken drafts, the token behind them, -1) and kv_keep int32 [batch] =
     kv_len - rejected drafts.  n_draft int32 [batch]: drafts among a sequence's rows
     (None: all but the first)."""
+    if stream is None and _native is not None:
+        rc = _native.verify(probs, tokens, cu_new, u_accept, u_sample, accepted, out_tokens, draft_probs, n_draft, kv_len, kv_keep, err)
+        if rc == MOE_OK:
+            return accepted, out_tokens
+        if rc < 0:
+            raise MoeError(rc, "moe_verify_drafts")
     T, vocab = probs.shape
     batch, max_out = out_tokens.shape
     dtype, device = probs.dtype, probs.get_device()

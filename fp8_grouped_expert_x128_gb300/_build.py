@@ -1,6 +1,8 @@
 """Builds libmoe_fp8.so in-tree for sm_103a with nvcc (no cmake, no torch
 extension machinery): every .cu under csrc/ is compiled in parallel, then
-linked into one shared library next to this file.
+linked into one shared library next to this file.  Beside it, with g++ and the
+headers of Python and torch, _binding.so: the quick way from Python to some of the
+calls (csrc/binding.cpp).  Where that does not build, the calls go the longer way.
 
     python fp8_grouped_expert_x128_gb300/_build.py [--force] [--verbose] [--ptxas-info]
 """
@@ -10,8 +12,10 @@ import argparse
 import concurrent.futures as cf
 import os
 import shutil
+import importlib.util
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_fp8.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -51,6 +56,29 @@ def _stale(out: str, ins: list[str]) -> bool:
     return any(os.path.getmtime(i) > t for i in ins)
 
 
+def _build_binding(cuda: str, force: bool) -> None:
+    """_binding.so, if its headers are there."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and not _stale(BINDING, [src, os.path.join(INCLUDE, "moe_fp8.h"), os.path.abspath(__file__)]):
+        return
+    spec = importlib.util.find_spec("torch")
+    gxx = os.environ.get("CXX") or shutil.which("g++")
+    if spec is None or gxx is None:
+        print("_binding.so is not built: it takes torch and g++", file=sys.stderr)
+        return
+    torch_dir = list(spec.submodule_search_locations)[0]
+    tmp = BINDING + ".tmp"
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", tmp, "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(cuda, "include"), "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath," + os.path.join(torch_dir, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        print(f"_binding.so is not built:\n{' '.join(cmd)}\n{r.stderr[-2000:]}", file=sys.stderr)
+        return
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     """Compile (if stale) and return the path of libmoe_fp8.so."""
     nvcc = _nvcc()
@@ -73,8 +101,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_build_binding, os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), force)
         list(ex.map(run, jobs))
+        binding.result()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in sources()]
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp"

@@ -133,3 +133,17 @@ def test_packed_descriptors_have_the_structures_layout(moe):
                       (moe._kv_pages_pack, moe.moe_kv_pages_desc), (moe._verify_pack, moe.moe_verify_desc)):
         values = tuple(range(1, 1 + len(cls._fields_)))
         assert pack(*values) == bytes(cls(*values)), cls
+
+
+def test_quick_way_is_there_and_leaves_the_telling_to_python(moe):
+    """_binding.so is built beside the library; it answers 1 for whatever it would not take as it is."""
+    assert moe._native is not None
+    x, f, i = torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros((2, 8)), torch.zeros((2, 2), dtype=torch.int32)
+    n = torch.zeros(2, dtype=torch.int32)
+    assert moe._native.gate(x, x, f, None) == 1                                # tensors of the CPU
+    assert moe._native.gate(None, 3, "x", ()) == 1
+    assert moe._native.gate() == 1
+    assert moe._native.route(f, i, f, None, None, 1, 1, 1.0, 0) == 1
+    assert moe._native.route(f, i, f, None, None, "1", 1 << 40, None, 0) == 1
+    assert moe._native.kv_pages(n, n, i, n, n, 16, n, n, n, None, None, None, None, None) == 1
+    assert moe._native.verify(f, n, n, f, f, n, i, None, None, None, None, None) == 1
