@@ -23,9 +23,13 @@ struct PagesArgs {
   int32_t shift;   // log2 page_size
 };
 
-struct Sums {      // over sequences: new tokens, pages taken, pages given back
-  int64_t n, take, back;
-  __device__ __forceinline__ Sums operator+(const Sums& o) const { return {n + o.n, take + o.take, back + o.back}; }
+// Sums over sequences that stop at 2^31 - 1, which is past all that may be asked for: below
+// it they are exact, and so are the sums in front of them.
+constexpr uint32_t kMost = INT32_MAX;
+__device__ __forceinline__ uint32_t add(uint32_t x, uint32_t y) { return min(x + y, kMost); }
+struct Sums {      // new tokens, pages taken, pages given back
+  uint32_t n, take, back;
+  __device__ __forceinline__ Sums operator+(const Sums& o) const { return {add(n, o.n), add(take, o.take), add(back, o.back)}; }
 };
 
 __device__ __forceinline__ Sums shfl_up(const Sums& v, int o) {
@@ -35,8 +39,8 @@ __device__ __forceinline__ Sums shfl(const Sums& v, int lane) {
   return {__shfl_sync(0xffffffffu, v.n, lane), __shfl_sync(0xffffffffu, v.take, lane), __shfl_sync(0xffffffffu, v.back, lane)};
 }
 
-// Exclusive sums over the block's threads; `total` gets the sum of all.
-__device__ Sums block_scan(Sums v, Sums* part, Sums& total) {
+// The sums over the block's threads before this one; `total` gets the sum of all.
+__device__ Sums block_scan(const Sums& v, Sums* part, Sums& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Sums x = v;
 #pragma unroll
@@ -54,8 +58,9 @@ __device__ Sums block_scan(Sums v, Sums* part, Sums& total) {
     if (lane >= o) w = w + y;
   }
   total = shfl(w, kPagesThreads / 32 - 1);
-  const Sums before = warp ? shfl(w, warp - 1) : Sums{0, 0, 0};
-  return {before.n + x.n - v.n, before.take + x.take - v.take, before.back + x.back - v.back};
+  Sums before = shfl_up(x, 1);
+  if (lane == 0) before = Sums{0, 0, 0};
+  return warp ? shfl(w, warp - 1) + before : before;
 }
 
 // The last b in [0, n) with first[b] <= x (first is not decreasing, first[0] <= x).
@@ -91,106 +96,78 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const __grid_co
   const bool list_ok = f >= 0 && f <= d.free_capacity;
   auto pages = [&](int64_t tokens) { return static_cast<int32_t>((tokens + d.page_size - 1) >> a.shift); };
 
-  struct Seq {
-    int32_t old, keep, n, held;
-    int64_t want;
-    bool bad, wide;
-  };
-  auto load = [&](int b) {
-    Seq s;
-    s.old = __ldg(d.kv_old + b);
-    s.n = __ldg(d.n_new + b);
-    s.keep = d.kv_keep ? __ldg(d.kv_keep + b) : s.old;
-    s.bad = !list_ok || s.old < 0 || s.n < 0 || s.old > most || s.keep < 0 || s.keep > s.old;
-    s.held = s.bad ? 0 : pages(s.old);
-    s.want = static_cast<int64_t>(s.keep) + s.n;
-    s.wide = !s.bad && s.want > most;
-    return s;
-  };
-  // what a sequence asks for
-  auto asked = [&](const Seq& s) {
-    Sums v{0, 0, 0};
-    if (s.bad || s.wide) return v;
-    const int32_t need = pages(s.want);
-    v.n = s.n;
-    v.take = max(0, need - s.held);
-    v.back = max(0, s.held - need);
-    return v;
-  };
+  // What a sequence asks for, kept in its places of the arrays until it is known what it gets:
+  // tokens to keep, pages held and needed, new tokens (row0) and whether it is left alone (2) or
+  // needs more pages than a row of the table has (1) (take0).
   int32_t bits = 0;
   Sums mine{0, 0, 0}, total;
-  bool refused = false;
   for (int b = b0; b < b1; ++b) {
-    const Seq s = load(b);
-    mine = mine + asked(s);
-    refused |= s.wide;
-    if (s.bad) bits |= MOE_DEV_BAD_INDEX;
-    if (s.wide) bits |= MOE_DEV_OVERFLOW;
+    const int32_t old = __ldg(d.kv_old + b), n = __ldg(d.n_new + b), keep = d.kv_keep ? __ldg(d.kv_keep + b) : old;
+    const bool bad = !list_ok || old < 0 || n < 0 || old > most || keep < 0 || keep > old;
+    const int64_t want = static_cast<int64_t>(keep) + n;
+    const bool wide = !bad && want > most;
+    const int32_t held = bad ? 0 : pages(old), need = bad || wide ? held : pages(want);
+    keep_of[b] = keep;
+    held_of[b] = held;
+    need_of[b] = need;
+    row0[b] = n;
+    take0[b] = bad ? 2 : wide ? 1 : 0;
+    if (bad) bits |= MOE_DEV_BAD_INDEX;
+    if (wide) bits |= MOE_DEV_OVERFLOW;
+    // (too wide: more than there is, so that the sums tell)
+    mine = mine + Sums{bad ? 0u : wide ? kMost : static_cast<uint32_t>(n), static_cast<uint32_t>(max(0, need - held)),
+                       static_cast<uint32_t>(max(0, held - need))};
   }
   Sums before = block_scan(mine, part, total);
-  const int64_t room = f + total.back;
-  const bool all = !__syncthreads_or(refused) && total.n <= d.rows && total.take <= room;
-  // which sequences get what they ask for (bit i: the thread's i-th; at most 16 of them)
-  uint32_t grants = 0xffffffffu;
-  if (!all) {
-    // by rows first, then by pages among those that pass
-    int64_t n = before.n;
-    uint32_t fits = 0;
-    Sums asks{0, 0, 0};
-    for (int b = b0; b < b1; ++b) {
-      const Seq s = load(b);
-      const Sums v = asked(s);
-      n += v.n;
-      if (s.bad || s.wide || (v.n > 0 && n > d.rows)) continue;
-      fits |= 1u << (b - b0);
-      asks.take += v.take;
-    }
-    Sums sum;
-    int64_t take = block_scan(asks, part, sum).take;
-    grants = 0;
+  const uint32_t room = add(f, total.back), all_rows_u = static_cast<uint32_t>(d.rows);
+  if (list_ok && (total.n > all_rows_u || total.take > room)) {
+    // not all get what they ask for: by rows first, then by pages among those that pass
+    Sums asks{0, 0, 0}, sum;
+    for (int b = b0; b < b1; ++b) asks.n = add(asks.n, take0[b] ? 0 : row0[b]);
+    uint32_t n = block_scan(asks, part, sum).n;
+    asks = Sums{0, 0, 0};
+    for (int b = b0; b < b1; ++b)
+      if (take0[b] == 0) {
+        n = add(n, row0[b]);
+        if (row0[b] > 0 && n > all_rows_u) take0[b] = 1;
+        else asks.take = add(asks.take, max(0, need_of[b] - held_of[b]));
+      }
+    uint32_t take = block_scan(asks, part, sum).take;
     mine = Sums{0, 0, 0};
     for (int b = b0; b < b1; ++b) {
-      const Seq s = load(b);
-      Sums v = asked(s);
-      bool ok = (fits >> (b - b0)) & 1;
-      if (ok) {
-        take += v.take;
-        ok = v.take == 0 || take <= room;
+      if (take0[b] == 0 && need_of[b] > held_of[b]) {
+        take = add(take, need_of[b] - held_of[b]);
+        if (take > room) take0[b] = 1;
       }
-      if (ok) {
-        grants |= 1u << (b - b0);
-      } else if (!s.bad) {
+      if (take0[b] == 1) {             // keeps what it keeps
         bits |= MOE_DEV_OVERFLOW;
-        v = Sums{0, 0, s.held - pages(s.keep)};
+        row0[b] = 0;
+        need_of[b] = pages(keep_of[b]);
       }
-      mine = mine + v;
+      if (take0[b] != 2)
+        mine = mine + Sums{static_cast<uint32_t>(row0[b]), static_cast<uint32_t>(max(0, need_of[b] - held_of[b])),
+                           static_cast<uint32_t>(max(0, held_of[b] - need_of[b]))};
     }
     before = block_scan(mine, part, total);
   }
   // a list that would not hold what comes back: nothing moves
-  const bool whole = list_ok && f + total.back <= d.free_capacity;
+  const bool whole = list_ok && add(f, total.back) <= d.free_capacity;
   if (!whole) {
     bits |= MOE_DEV_BAD_INDEX;
     before = total = Sums{0, 0, 0};
   }
   for (int b = b0; b < b1; ++b) {
-    const Seq s = load(b);
-    const bool stays = s.bad || !whole, ok = !stays && ((grants >> (b - b0)) & 1);
-    const int32_t len = stays ? s.old : ok ? static_cast<int32_t>(s.want) : s.keep;
-    const int32_t held = stays ? 0 : s.held, need = stays ? 0 : pages(len);
+    const bool stays = !whole || take0[b] == 2;
+    const int32_t n = stays ? 0 : row0[b], held = held_of[b], need = stays ? held : need_of[b];
+    if (blockIdx.x == 0) {
+      d.cu_new[b] = static_cast<int32_t>(before.n);
+      d.kv_len[b] = stays ? __ldg(d.kv_old + b) : keep_of[b] + n;
+    }
     row0[b] = static_cast<int32_t>(before.n);
     take0[b] = static_cast<int32_t>(before.take);
     back0[b] = static_cast<int32_t>(before.back);
-    keep_of[b] = s.keep;
-    held_of[b] = held;
     need_of[b] = need;
-    if (blockIdx.x == 0) {
-      d.cu_new[b] = row0[b];
-      d.kv_len[b] = len;
-    }
-    before.n += ok ? s.n : 0;
-    before.take += max(0, need - held);
-    before.back += max(0, held - need);
+    before = before + Sums{static_cast<uint32_t>(n), static_cast<uint32_t>(max(0, need - held)), static_cast<uint32_t>(max(0, held - need))};
   }
   const int32_t rows = static_cast<int32_t>(total.n), taken = static_cast<int32_t>(total.take), back = static_cast<int32_t>(total.back);
   const int32_t left = f + back - taken;
@@ -330,7 +307,7 @@ extern "C" int moe_kv_pages(const moe_kv_pages_desc* d, void* stream) {
   // a CTA for every 512 rows, and for 16 sequences, whose pages may all go back
   const int64_t told = d->seqs || d->positions || d->slots ? d->rows : 0;
   const int64_t ctas = std::min<int64_t>(std::max<int64_t>({(told + kPagesThreads - 1) / kPagesThreads, (d->batch + 15) / 16, 1}),
-                                         (d->batch <= kPagesMaxBatch / 2 ? 2 : 1) * num_sms());
+                                         num_sms());
   const size_t smem = pages_smem_bytes(d->batch);
   if (smem > 48 * 1024)
     MOE_CUDA_TRY(cudaFuncSetAttribute(kv_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
