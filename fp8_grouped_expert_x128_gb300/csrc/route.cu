@@ -1,16 +1,13 @@
 // Routing to experts: softmax or sigmoid scores, a bias for balance, groups,
 // top-k, renormalised weights (moe_route).
 #include <algorithm>
-#include <cfloat>
-#include <cmath>
 
-#include "kv_common.cuh"
+#include "route_common.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kRouteWarps = 4;      // tokens of a CTA, a warp each
-constexpr uint32_t kAll = 0xffffffffu;
 
 struct RouteArgs {
   moe_route_desc d;
@@ -19,151 +16,6 @@ struct RouteArgs {
   int32_t slot;          // shared memory of a warp, 8-byte units
   int32_t group_lanes;
 };
-
-// A logit as fp32: NaN and -inf (an expert that is not open) become -inf, +inf the
-// largest fp32.
-__device__ __forceinline__ float as_logit(float z) { return z > -INFINITY ? fminf(z, FLT_MAX) : -INFINITY; }
-
-template <int DT>
-__device__ __forceinline__ float raw_logit(const void* row, int e) {
-  if constexpr (DT == MOE_DTYPE_F32) return __ldg(static_cast<const float*>(row) + e);
-  const uint16_t b = __ldg(static_cast<const uint16_t*>(row) + e);
-  return DT == MOE_DTYPE_F16 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_float(b);
-}
-template <int DT>
-__device__ __forceinline__ float load_logit(const void* row, int e) {
-  return as_logit(raw_logit<DT>(row, e));
-}
-
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
-
-// Numbers whose order as unsigned integers is that of the doubles (and -0 as 0); 0 is none.
-// GB300 has few 64-bit floating-point units: values are compared as integers.
-__device__ __forceinline__ uint64_t key_of(double v) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
-  return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
-}
-__device__ __forceinline__ double value_of(uint64_t k) {
-  return __longlong_as_double(static_cast<int64_t>(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
-}
-
-// One token in 64-bit arithmetic by one warp.  value: E words of shared memory.
-// Lane j < k gets the number of the j-th expert, -1 where there is none.
-template <int DT>
-__device__ __noinline__ int route_exact(const moe_route_desc& d, const void* row, uint64_t* value, int group_lanes) {
-  const int lane = threadIdx.x & 31;
-  const bool softmax = d.flags & MOE_ROUTE_SOFTMAX, pair = d.flags & MOE_ROUTE_GROUP_PAIR;
-  float top = -INFINITY;
-  double sum = 1.0;
-  if (softmax) {
-    for (int e = lane; e < d.E; e += 32) top = fmaxf(top, load_logit<DT>(row, e));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    sum = 0.0;
-    for (int e = lane; e < d.E; e += 32) {
-      const float z = load_logit<DT>(row, e);
-      if (z > -INFINITY) sum += exp(static_cast<double>(z) - top);
-    }
-    sum = warp_sum(sum);
-  }
-  auto score = [&](double z) { return softmax ? exp(z - top) / sum : 1.0 / (1.0 + exp(-z)); };
-  auto fill = [&](bool scores) {
-    for (int e = lane; e < d.E; e += 32) {
-      const float z = load_logit<DT>(row, e);
-      const float b = d.bias ? __ldg(d.bias + e) : 0.0f;
-      uint64_t k = 0;
-      if (z > -INFINITY && b > -INFINITY) k = key_of(scores ? score(z) + b : static_cast<double>(z));
-      value[e] = k;
-    }
-    __syncwarp();
-  };
-  const int size = d.E / d.n_group;
-  uint32_t kept = kAll;
-  if (d.n_group > 1) {
-    fill(d.bias != nullptr || pair);
-    const int g = lane / group_lanes;
-    uint64_t a = 0, b = 0;
-    if (g < d.n_group)
-      for (int i = lane % group_lanes; i < size; i += group_lanes) {
-        const uint64_t v = value[g * size + i];
-        b = max(b, min(a, v));
-        a = max(a, v);
-      }
-    for (int o = group_lanes / 2; o > 0; o >>= 1) {
-      const uint64_t oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
-      b = max(min(a, oa), max(b, ob));
-      a = max(a, oa);
-    }
-    if (pair && b != 0) a = key_of(value_of(a) + value_of(b));
-    int rank = 0;
-    for (int i = 0; i < d.n_group; ++i) {
-      const uint64_t other = __shfl_sync(kAll, a, i * group_lanes);
-      rank += other > a || (other == a && i < g);
-    }
-    kept = __ballot_sync(kAll, g < d.n_group && rank < d.topk_group);
-    __syncwarp();
-  }
-  if (d.n_group == 1 || (d.bias == nullptr && pair)) fill(d.bias != nullptr);
-  int found = -1;
-  for (int j = 0; j < d.k; ++j) {
-    uint64_t v = 0;
-    int n = INT32_MAX;
-    for (int e = lane; e < d.E; e += 32) {
-      const uint64_t x = value[e];
-      if (x > v && (d.n_group == 1 || ((kept >> (e / size * group_lanes)) & 1))) {
-        v = x;
-        n = e;
-      }
-    }
-    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32));
-    const uint32_t lo = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
-    const uint64_t best = static_cast<uint64_t>(hi) << 32 | lo;
-    if (best == 0) break;
-    n = __reduce_min_sync(kAll, v == best ? n : INT32_MAX);
-    if (lane == j) found = n;
-    if (lane == (n & 31)) value[n] = 0;
-    __syncwarp();
-  }
-  __syncwarp();
-  return found;
-}
-
-// Numbers whose order as unsigned integers is that of the floats (and -0 as 0); 0 is none.
-__device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t b = __float_as_uint(v + 0.0f);
-  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-}
-// of a sum, which is never -0
-__device__ __forceinline__ uint32_t key_of_sum(float v) {
-  const uint32_t b = __float_as_uint(v);
-  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-}
-
-// Values this near may be in another order than they appear in.  A sigmoid: its exponential
-// is off by at most 2^-22 + |z| 2^-24 relatively, its slope is at most 1/4 and |z| times its slope 0.23, its
-// quotient is off by 2^-23: less than 2^-22 in all, 2^-21 between two of them.  A softmax's share:
-// its sum is off by less than 2^-19 of it, by which two of them shift together.  Adding a bias
-// rounds either to 2^-24.
-__device__ __forceinline__ float near_of(float v, bool softmax) { return (softmax ? 0x1p-18f : 0x1p-20f) + 0x1p-22f * fabsf(v); }
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-constexpr float kLog2e = 1.44269504088896340736f;
 
 // VPL consecutive values of a lane, from e0 = lane * VPL on; `rest` past the last.
 template <int DT, int VPL>
@@ -242,38 +94,6 @@ __device__ __noinline__ int select_slowly(uint32_t* key, int E, int most, uint2*
   return count;
 }
 
-// The rank of lane l < count's expert e (numbers rising with the lanes) by its sigmoid and
-// bias in 64 bits.
-template <int DT>
-__device__ __noinline__ int rank_exactly(const void* row, const float* bias, int e, int count) {
-  const int lane = threadIdx.x & 31;
-  uint64_t key = 0;
-  if (lane < count) key = key_of(1.0 / (1.0 + exp(-static_cast<double>(load_logit<DT>(row, e)))) + __ldg(bias + e));
-  int rank = 0;
-  for (int j = 0; j < count; ++j) rank += __shfl_sync(kAll, key, j) + (j < lane) > key;
-  return rank;
-}
-
-// Which groups stay, as a mask, by their sigmoids and biases in 64 bits.  Lane l < count has
-// expert e; among these are the experts that any group counts.
-template <int DT>
-__device__ __noinline__ uint32_t groups_exactly(const moe_route_desc& d, const void* row, int e, int count) {
-  const int lane = threadIdx.x & 31, size = d.E / d.n_group;
-  uint64_t key = 0, a = 0, b = 0;
-  if (lane < count) key = key_of(1.0 / (1.0 + exp(-static_cast<double>(load_logit<DT>(row, e)))) + __ldg(d.bias + e));
-  const int g = lane < count ? e / size : -1;
-  for (int j = 0; j < count; ++j) {
-    const uint64_t k = __shfl_sync(kAll, key, j);
-    if (__shfl_sync(kAll, g, j) == lane) {
-      b = max(b, min(a, k));
-      a = max(a, k);
-    }
-  }
-  if ((d.flags & MOE_ROUTE_GROUP_PAIR) && b != 0) a = key_of(value_of(a) + value_of(b));
-  int rank = 0;
-  for (int i = 0; i < d.n_group; ++i) rank += __shfl_sync(kAll, a, i) + (i < lane) > a;
-  return __ballot_sync(kAll, lane < d.n_group && rank < d.topk_group);
-}
 
 // How many of the earlier lanes' things there are, and of all.
 __device__ __forceinline__ int lanes_before(int have, int& all) {
@@ -288,9 +108,10 @@ __device__ __forceinline__ int lanes_before(int have, int& all) {
   return upto - have;
 }
 
-// A warp routes one token after another, in fp32 as far as that decides.  What bounds it is
-// the number of instructions (256 experts: 40 instructions' time of loads, some 450 of
-// arithmetic and exchange a token), so values become sortable keys once, and selection works
+// A warp routes one token after another, in fp32 as far as that decides: 3 us for a token, 5.3
+// for 2048 of 256 experts, where a token's chain of exchanges is what takes time.  More tokens
+// than there are warps at once are bound by the instructions (some 850 a token), and most of
+// these calls are for route_many.  Values become sortable keys once, and selection works
 // on few of them: the k + 1 largest of the lanes' maxima leave a threshold that at least k + 1
 // experts reach and seldom many more.  These (32 at most) go to a lane each, in the order of
 // their numbers, which counts those in front of it.  Where two neighbours of that order, or
@@ -570,8 +391,6 @@ int launch_route(RouteArgs& a, cudaStream_t st) {
   a.wide = reinterpret_cast<uintptr_t>(a.d.logits) % unit == 0 && a.d.logits_ld * kSize % unit == 0;
   a.wide_bias = reinterpret_cast<uintptr_t>(a.d.bias) % std::min(16, VPL * 4) == 0;
   a.slot = 54 + a.d.E;                            // the lists and all keys, or 64-bit values
-  a.group_lanes = 1;
-  while (2 * a.group_lanes * a.d.n_group <= 32) a.group_lanes *= 2;
   // a few tokens a warp, so that a row is on its way while another is routed
   const int64_t ctas = std::min<int64_t>((a.d.T + kRouteWarps - 1) / kRouteWarps, 32ll * num_sms());
   return launch_pdl(route_kernel<DT, VPL>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kRouteWarps),
@@ -610,7 +429,10 @@ extern "C" int moe_route(const moe_route_desc* d, void* stream) {
                 (reinterpret_cast<uintptr_t>(d->topk_w) & 3) == 0 && (reinterpret_cast<uintptr_t>(d->bias) & 3) == 0 &&
                 (reinterpret_cast<uintptr_t>(d->n_tokens) & 3) == 0);
   if (int rc = check_device()) return rc;
-  RouteArgs a{*d, 0, 0, 0, 0};
+  int group_lanes = 1;
+  while (2 * group_lanes * d->n_group <= 32) group_lanes *= 2;
+  if (is_for_route_many(*d)) return route_many(*d, group_lanes, as_stream(stream));
+  RouteArgs a{*d, 0, 0, 0, group_lanes};
   if (d->dtype == MOE_DTYPE_F32) return pick_route<MOE_DTYPE_F32>(a, as_stream(stream));
   return d->dtype == MOE_DTYPE_F16 ? pick_route<MOE_DTYPE_F16>(a, as_stream(stream)) : pick_route<MOE_DTYPE_BF16>(a, as_stream(stream));
 }
