@@ -247,10 +247,14 @@ struct Weights {
   }
 };
 
-template <int DT, bool kMarked>
+// How a warp's lanes share its run of vectors: each a 32nd of it, whose sum the search then has;
+// every 32nd vector each; these, with marks.
+enum class Way { kParted, kStrided, kMarked };
+
+template <int DT, Way kWay>
 __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ Pair sums[2][kVerifyWarps * kVerifyMaxCluster];      // of all warps of the cluster
-  __shared__ Pair marks[kMarked ? kVerifyWarps : 1][kMarks][32];
+  __shared__ Pair marks[kWay == Way::kMarked ? kVerifyWarps : 1][kMarks][32];
   const moe_verify_desc& d = a.d;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y, ctas = gridDim.x, rank = blockIdx.x;
@@ -314,11 +318,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
   const int every = (run + kRound * kMarks - 1) / (kRound * kMarks);
   const float u = u_sample > 0.0f ? u_sample : 0.0f;
   const int per = (warps + 31) / 32;            // warps' sums of a lane, at most 4
-  Pair before, target;
+  constexpr bool kMarked = kWay == Way::kMarked, kParted = kWay == Way::kParted;
+  const int f0 = kParted ? min(k0 + lane * (run / 32), k1) : k0 + lane, t0 = kParted ? min(f0 + run / 32, k1) : k1;
+  Pair before, target, own;
   int owner = -1;
   bool any = false, beyond = false;
   for (int pass = 0; pass < 4; ++pass) {
-    Pair sum = w.template sum<kMarked>(k0 + lane, k1, 32, &marks[kMarked ? warp : 0][0][lane], every);
+    own = w.template sum<kMarked>(f0, t0, kParted ? 1 : 32, &marks[kMarked ? warp : 0][0][lane], every);
+    Pair sum = own;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum.add(Pair{__shfl_xor_sync(kAll, sum.hi, o), __shfl_xor_sync(kAll, sum.lo, o)});
     // to every CTA of the cluster
@@ -403,9 +410,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       k1 = min(k0 + every * kRound, k1);
     }
     // the entry in it, a 32nd at a time and then an entry a lane
-    while ((k1 - k0) * W::kVec > 32) {
-      const int piece = (k1 - k0 + 31) / 32, f = min(k0 + lane * piece, k1), t = min(f + piece, k1);
-      const Pair x = w.template sum<false>(f, t, 1);
+    auto narrow = [&](int f, int t, const Pair& x) {
       Pair ahead;
       const Pair upto = warp_prefix(x, ahead);
       const uint32_t over = __ballot_sync(kAll, !beyond && x.hi > 0.0f && plus(before, upto).above(target));
@@ -416,6 +421,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       before.add(shfl(ahead, at));
       k0 = __shfl_sync(kAll, f, at);
       k1 = __shfl_sync(kAll, t, at);
+    };
+    if (kParted) narrow(f0, t0, own);
+    while ((k1 - k0) * W::kVec > 32) {
+      const int piece = (k1 - k0 + 31) / 32, f = min(k0 + lane * piece, k1), t = min(f + piece, k1);
+      narrow(f, t, w.template sum<false>(f, t, 1));
     }
     const int j = k0 * W::kVec - w.shift + lane;
     Pair x, ahead;
@@ -427,14 +437,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
   }
 }
 
-template <int DT, bool kMarked>
+template <int DT, Way kWay>
 int launch_verify(const VerifyArgs& a, int ctas, cudaStream_t st) {
   if (ctas > 8) {
     static std::atomic<uint64_t> allowed{0};      // a bit for each GPU that has been told
     int dev = 0;
     MOE_CUDA_TRY(cudaGetDevice(&dev));
     if (!((allowed.load() >> (dev & 63)) & 1)) {
-      MOE_CUDA_TRY(cudaFuncSetAttribute(verify_kernel<DT, kMarked>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+      MOE_CUDA_TRY(cudaFuncSetAttribute(verify_kernel<DT, kWay>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
       allowed.fetch_or(1ull << (dev & 63));
     }
   }
@@ -460,7 +470,7 @@ int launch_verify(const VerifyArgs& a, int ctas, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, verify_kernel<DT, kMarked>, part) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, verify_kernel<DT, kWay>, part) != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }
@@ -473,8 +483,12 @@ int pick_verify(const VerifyArgs& a, cudaStream_t st) {
   const int64_t vectors = a.d.vocab / Weights<DT>::kVec + 2, B = a.d.batch;
   int ctas = 16 * B <= 112 ? 16 : 8;
   while (ctas > 1 && (B * ctas > 4 * num_sms() || (ctas / 2) * kVerifyWarps * 32 >= vectors)) ctas /= 2;
-  // Marks from three rounds of loads on: the border is found in 1.4 us less (16 sequences 11.1 -> 9.2 us).
-  return vectors > 2ll * kRound * kVerifyWarps * ctas ? launch_verify<DT, true>(a, ctas, st) : launch_verify<DT, false>(a, ctas, st);
+  // Parts where a round of loads takes them whole (37 sequences of 50021 bf16 entries 7.2 -> 6.1 us;
+  // of two rounds, one sequence of 128000 in fp32, they take 6.2 and strides 6.05), marks from three
+  // rounds on (16 sequences of these 11.1 -> 9.4 us).
+  const int64_t rounds = (vectors - 1) / (kRound * kVerifyWarps * ctas);
+  if (rounds == 0) return launch_verify<DT, Way::kParted>(a, ctas, st);
+  return rounds < 2 ? launch_verify<DT, Way::kStrided>(a, ctas, st) : launch_verify<DT, Way::kMarked>(a, ctas, st);
 }
 
 }  // namespace
