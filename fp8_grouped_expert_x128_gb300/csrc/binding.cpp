@@ -1,7 +1,7 @@
 // The quick way from a Python call to the library for the calls that a serving step
 // makes between its products (moe_gate, moe_route, moe_kv_pages, moe_verify_drafts).
-// In Python the checks of a call's tensors take longer than its launch and its kernel
-// together (12 tensors: 3.6 of 7.8 us); here they take some 0.3.  A call that is not as
+// In Python the checks of a call's tensors can take longer than its launch or its kernel (12
+// tensors: a call among others took 7.8 us, here 3.8).  A call that is not as
 // it should be is not refused here but left to the Python binding, which makes the
 // same checks and says what is wrong.
 #include <Python.h>

@@ -8,6 +8,11 @@
 // below its old length, or straight from the table of a sequence that shrinks;
 // what is written are table entries of sequences that grow and list entries past
 // the old length.
+//
+// What bounds it is a thread's chain of loads, scans and searches, not bytes: 256
+// sequences with a token each take 3.4 us, 61 with 5 drafts 4.2, 1024 prompts of up to
+// 2048 tokens 9.5 (16 bytes a row, 1.8 TB/s).  512 threads: 768 and 1024 took 3.6 and
+// 3.8 us for the first; a second CTA an SM made all of them slower.
 #include <algorithm>
 
 #include "common.cuh"
