@@ -10,8 +10,8 @@
 // the old length.
 //
 // What bounds it is a thread's chain of loads, scans and searches, not bytes: 256
-// sequences with a token each take 3.4 us, 61 with 5 drafts 4.2, 1024 prompts of up to
-// 2048 tokens 9.5 (16 bytes a row, 1.8 TB/s).  512 threads: 768 and 1024 took 3.6 and
+// sequences with a token each take 3.4 us, 61 with 5 drafts 4.3, 1024 prompts of up to
+// 2048 tokens 10 (16 bytes a row, 1.8 TB/s).  512 threads: 768 and 1024 took 3.6 and
 // 3.8 us for the first; a second CTA an SM made all of them slower.
 #include <algorithm>
 
@@ -191,17 +191,19 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const __grid_co
   const int32_t step = static_cast<int32_t>(gridDim.x) * kPagesThreads;
   const int32_t first = static_cast<int32_t>(blockIdx.x) * kPagesThreads + threadIdx.x;
   auto entry = [&](int b, int32_t j) { return d.page_table + b * d.table_ld + j; };
-  // the i-th page given back, and the i-th page taken
+  // The i-th page given back, and the i-th page taken.  Read from the L2: other CTAs write other
+  // words of these lines, and what is launched behind this may be on an SM before they have, where
+  // it should not find the lines as they were (1024 prompts 9.4 -> 10 us).
   auto given = [&](int32_t i) {
     const int b = find_last(back0, B, i);
-    return __ldg(entry(b, need_of[b] + i - back0[b]));
+    return __ldcg(entry(b, need_of[b] + i - back0[b]));
   };
   auto source = [&](int32_t i) {
     const int32_t at = f + back - 1 - i;
-    return at < f ? __ldg(d.free_list + at) : given(at - f);
+    return at < f ? __ldcg(d.free_list + at) : given(at - f);
   };
   // page j of sequence b
-  auto lookup = [&](int b, int32_t j) { return j < held_of[b] ? __ldg(entry(b, j)) : source(take0[b] + j - held_of[b]); };
+  auto lookup = [&](int b, int32_t j) { return j < held_of[b] ? __ldcg(entry(b, j)) : source(take0[b] + j - held_of[b]); };
   for (int64_t i = first; i < taken; i += step) {
     const int b = find_last(take0, B, static_cast<int32_t>(i));
     *entry(b, held_of[b] + static_cast<int32_t>(i) - take0[b]) = source(static_cast<int32_t>(i));
