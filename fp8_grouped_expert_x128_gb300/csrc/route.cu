@@ -1,6 +1,7 @@
 // Routing to experts: softmax or sigmoid scores, a bias for balance, groups,
 // top-k, renormalised weights (moe_route).
 #include <algorithm>
+#include <utility>
 
 #include "route_common.cuh"
 
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
       if (unsure && whole && biased && !softmax) {
         // the experts that a group may count, up to a lane each, settle it in 64 bits
         const float v = value_of(pair && second ? second : best);
-        const uint32_t from = best ? key_of(v - 4.0f * near_of(v, false)) : 0xffffffffu;
+        const uint32_t from = best ? key_of(v <= FLT_MAX ? v - 4.0f * near_of(v, false) : v) : 0xffffffffu;
         int have = 0, count;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) have += key[i] >= from;
@@ -428,6 +429,12 @@ extern "C" int moe_route(const moe_route_desc* d, void* stream) {
   MOE_CHECK_ARG((reinterpret_cast<uintptr_t>(d->logits) & unit) == 0 && (reinterpret_cast<uintptr_t>(d->topk_ids) & 3) == 0 &&
                 (reinterpret_cast<uintptr_t>(d->topk_w) & 3) == 0 && (reinterpret_cast<uintptr_t>(d->bias) & 3) == 0 &&
                 (reinterpret_cast<uintptr_t>(d->n_tokens) & 3) == 0);
+  const int64_t ids = 4 * ((d->T - 1) * d->ids_ld + d->k), w = 4 * ((d->T - 1) * d->w_ld + d->k);
+  const int64_t logits = static_cast<int64_t>(unit + 1) * ((d->T - 1) * d->logits_ld + d->E);
+  MOE_CHECK_ARG(!memory_overlaps(d->topk_ids, ids, d->topk_w, w));
+  for (const auto& [out, bytes] : {std::pair<const void*, int64_t>(d->topk_ids, ids), std::pair<const void*, int64_t>(d->topk_w, w)})
+    MOE_CHECK_ARG(!memory_overlaps(out, bytes, d->logits, logits) && !memory_overlaps(out, bytes, d->bias, 4ll * d->E) &&
+                  !memory_overlaps(out, bytes, d->n_tokens, 4));
   if (int rc = check_device()) return rc;
   int group_lanes = 1;
   while (2 * group_lanes * d->n_group <= 32) group_lanes *= 2;

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
         if (again) {
           // the experts that a group may count, up to 32, settle it in 64 bits (but for a softmax,
           // whose sum would take all of them)
-          const float v = pair && second > -INFINITY ? second : best, from = v - 4.0f * near_of(v, false);
+          const float v = pair && second > -INFINITY ? second : best, from = v <= FLT_MAX ? v - 4.0f * near_of(v, false) : v;
           uint32_t reach = 0;
 #pragma unroll
           for (int i = 0; i < V; ++i) reach |= value[i] > -INFINITY && value[i] >= from ? 1u << i : 0u;

@@ -20,6 +20,7 @@
 #include <atomic>
 #include <cfloat>
 #include <cmath>
+#include <utility>
 
 #include "kv_common.cuh"
 
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
 
   const int64_t r0 = d.cu_new[b], r1 = d.cu_new[b + 1];
   const int64_t n = d.n_draft ? d.n_draft[b] : r1 - r0 - 1;
-  const int32_t len = d.kv_len ? d.kv_len[b] : 0;
+  const int32_t len = d.kv_len ? __ldcg(d.kv_len + b) : 0;      // may be kv_keep, whose line others write to
   const float u_sample = d.u_sample[b];
   const bool none = r1 == r0 && r0 >= 0 && r1 <= d.T;
   const bool bad = !none && (r0 < 0 || r1 < r0 || r1 > d.T || n < 0 || n >= r1 - r0), wide = !none && !bad && n >= d.max_out;
@@ -512,6 +513,17 @@ extern "C" int moe_verify_drafts(const moe_verify_desc* d, void* stream) {
   MOE_CHECK_ARG((reinterpret_cast<uintptr_t>(d->probs) & unit) == 0 && (reinterpret_cast<uintptr_t>(d->draft_probs) & unit) == 0);
   const void* words[9] = {d->tokens, d->cu_new, d->n_draft, d->u_accept, d->u_sample, d->kv_len, d->accepted, d->out_tokens, d->kv_keep};
   for (const void* p : words) MOE_CHECK_ARG((reinterpret_cast<uintptr_t>(p) & 3) == 0);
+  const int64_t t4 = 4 * d->T, b4 = 4ll * d->batch, size = static_cast<int64_t>(unit) + 1;
+  const std::pair<const void*, int64_t> in[8] = {{d->probs, d->T ? size * ((d->T - 1) * d->p_ld + d->vocab) : 0},
+                                                 {d->draft_probs, d->T ? size * ((d->T - 1) * d->q_ld + d->vocab) : 0},
+                                                 {d->tokens, t4}, {d->cu_new, b4 + 4}, {d->n_draft, b4}, {d->u_accept, t4}, {d->u_sample, b4},
+                                                 {d->kv_len, b4}};
+  const std::pair<const void*, int64_t> out[3] = {{d->accepted, b4}, {d->out_tokens, 4 * ((d->batch - 1) * d->out_ld + d->max_out)}, {d->kv_keep, b4}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& [p, bytes] : in)
+      MOE_CHECK_ARG(!memory_overlaps(out[i].first, out[i].second, p, bytes) || (i == 2 && p == d->kv_len && d->kv_keep == d->kv_len));
+    for (int j = 0; j < i; ++j) MOE_CHECK_ARG(!memory_overlaps(out[i].first, out[i].second, out[j].first, out[j].second));
+  }
   if (int rc = check_device()) return rc;
   const VerifyArgs a{*d};
   if (d->dtype == MOE_DTYPE_F32) return pick_verify<MOE_DTYPE_F32>(a, as_stream(stream));

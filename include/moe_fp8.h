@@ -651,7 +651,8 @@ int moe_gate(const moe_gate_desc *desc, void *stream);
  * elements, at least E and k.  scale finite.
  * Limits: E and k as moe_permute (1024 and 32; k up to topk_group * E / n_group),
  * n_group up to 32, a divisor of E; T up to 2^24, 0 launches nothing.  logits aligned
- * to its elements.
+ * to its elements.  topk_ids and topk_w that overlap each other or an input, from their
+ * first row to the end of their last, are refused.
  */
 #define MOE_ROUTE_SOFTMAX 0x1
 #define MOE_ROUTE_RENORM 0x2
@@ -769,7 +770,8 @@ int moe_kv_pages(const moe_kv_pages_desc *desc, void *stream);
  * row strides in elements, at least vocab, aligned to their elements; tokens, cu_new
  * [batch + 1], n_draft, accepted, kv_len, kv_keep [batch], out_tokens [batch, max_out]
  * (row stride out_ld): device int32; u_accept [T], u_sample [batch]: device fp32.
- * kv_keep may be kv_len.  Limits: vocab 1 .. 2^24, batch up to 2^20, T up to 2^24,
+ * kv_keep may be kv_len; outputs that overlap an input or each other otherwise, from
+ * their first entry to their last, are refused.  Limits: vocab 1 .. 2^24, batch up to 2^20, T up to 2^24,
  * max_out 1 .. 1024.  batch = 0 launches nothing.
  */
 typedef struct moe_verify_desc {

@@ -106,6 +106,18 @@ def test_values_that_fp32_cannot_tell_apart(lib):
     check(lib, wide, 8, soft, n_group=8, topk_group=4, flags=lib.MOE_ROUTE_SOFTMAX | lib.MOE_ROUTE_GROUP_PAIR)
 
 
+def test_infinite_biases(lib):
+    """Groups whose experts are +inf rank before all others, in the order of their numbers."""
+    z, inf = logits_of(20, 256, seed=6), float("inf")
+    for at in ([70, 75, 170, 180], [70, 75, 170, 180, 230, 231], [3, 70, 170], list(range(256)), [255]):
+        b = bias_of(256)
+        b[at] = inf
+        for topk_group in (1, 2, 3):
+            for flags in (0, lib.MOE_ROUTE_GROUP_PAIR):
+                for T in (8195, 20):
+                    check(lib, z, 2, b, n_group=8, topk_group=topk_group, flags=flags, T=T)
+
+
 def test_ties_go_to_the_lowest_number(lib):
     z = logits_of(100, 256, seed=2).mul(2).round().div(2).to(torch.bfloat16)      # many equal logits
     for bias in (None, torch.zeros(256, device="cuda"), torch.full((256,), 0.25, device="cuda")):

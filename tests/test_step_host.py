@@ -147,3 +147,18 @@ def test_quick_way_is_there_and_leaves_the_telling_to_python(moe):
     assert moe._native.route(f, i, f, None, None, "1", 1 << 40, None, 0) == 1
     assert moe._native.kv_pages(n, n, i, n, n, 16, n, n, n, None, None, None, None, None) == 1
     assert moe._native.verify(f, n, n, f, f, n, i, None, None, None, None, None) == 1
+
+
+@pytest.mark.parametrize("bad", [
+    dict(topk_ids=256), dict(topk_ids=256 + 4 * 79), dict(topk_w=256 + 64), dict(topk_w=(1 << 20) + 76), dict(topk_ids=(1 << 24) - 76),
+    dict(bias=(1 << 20) - 60), dict(n_tokens=1 << 24), dict(topk_w=(1 << 20) + 4, ids_ld=8, w_ld=8)])
+def test_route_outputs_on_inputs_and_each_other(moe, bad):
+    assert route(moe, **bad) == -1
+
+
+@pytest.mark.parametrize("bad", [
+    dict(accepted=3 << 20), dict(out_tokens=1 << 20), dict(out_tokens=(2 << 20) + 4 * 899), dict(kv_keep=9 << 20), dict(accepted=(4 << 20) + 12),
+    dict(kv_keep=(8 << 20) + 4), dict(accepted=8 << 20), dict(out_tokens=(11 << 20) - 44), dict(accepted=(10 << 20) + 44),
+    dict(kv_keep=(6 << 20) + 32), dict(accepted=(7 << 20) - 8)])
+def test_verify_outputs_on_inputs_and_each_other(moe, bad):
+    assert verify(moe, **bad) == -1
