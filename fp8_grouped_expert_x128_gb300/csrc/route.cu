@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
     // keys of the values.  Equal logits and biases give equal bits.
     uint32_t key[VPL];
     const float per = rcp_fast(sum);
+    const float unit = unit_of(softmax, per);
     if (biased) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
@@ -249,15 +250,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
         if (biased || pair) {
           low = __reduce_min_sync(kAll, kept && mark ? mark : 0xffffffffu);
           const uint32_t next_one = __reduce_max_sync(kAll, real && !kept ? mark : 0u);
-          unsure = next_one && !(value_of(low) - value_of(next_one) > 4.0f * near_of(value_of(low), softmax));
+          unsure = next_one && !(value_of(low) - value_of(next_one) > 4.0f * near_of(value_of(low), unit));
         }
       } else if (biased || pair) {
-        unsure = out && !(value_of(low) - value_of(out) > 4.0f * near_of(value_of(low), softmax));
+        unsure = out && !(value_of(low) - value_of(out) > 4.0f * near_of(value_of(low), unit));
       }
       if (unsure && whole && biased && !softmax) {
         // the experts that a group may count, up to a lane each, settle it in 64 bits
         const float v = value_of(pair && second ? second : best);
-        const uint32_t from = best ? key_of(v <= FLT_MAX ? v - 4.0f * near_of(v, false) : v) : 0xffffffffu;
+        const uint32_t from = best ? key_of(v <= FLT_MAX ? v - 4.0f * near_of(v, unit) : v) : 0xffffffffu;
         int have = 0, count;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) have += key[i] >= from;
@@ -339,11 +340,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
       __syncwarp();
       const bool judged = lane < count && rank < d.k && rank + 1 < count;
       const float v = value_of(me.x);
-      if (__any_sync(kAll, judged && !(v - value_of(sorted[rank + 1]) > near_of(v, softmax)))) {
+      if (__any_sync(kAll, judged && !(v - value_of(sorted[rank + 1]) > near_of(v, unit)))) {
         // where the k-th is clear of what stayed below the threshold, the listed experts settle
         // it among themselves (but for a softmax, whose sum would take all of them)
         const float kth = value_of(sorted[min(d.k, count) - 1]);
-        if (!softmax && few && (least == 1u || kth - value_of(least) > near_of(kth, false)))
+        if (!softmax && few && (least == 1u || kth - value_of(least) > near_of(kth, unit)))
           rank = rank_exactly<DT>(row, d.bias, me.y, count);
         else
           unsure = true;

@@ -146,9 +146,11 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // Values this near may be in another order than they appear in.  A sigmoid: its exponential
 // is off by at most 2^-22 + |z| 2^-24 relatively, its slope is at most 1/4 and |z| times its slope 0.23, its
 // quotient is off by 2^-23: less than 2^-22 in all, 2^-21 between two of them.  A softmax's share:
-// its sum is off by less than 2^-19 of it, by which two of them shift together.  Adding a bias
-// rounds either to 2^-24.
-__device__ __forceinline__ float near_of(float v, bool softmax) { return (softmax ? 0x1p-18f : 0x1p-20f) + 0x1p-22f * fabsf(v); }
+// its sum is off by less than 2^-18.5 of it (32 additions one after another and 5 more), by which the
+// difference of two shares shifts, at most the largest share; the exponentials, as shares of it, by
+// less than 2^-21.  Adding a bias rounds either to 2^-24.
+__device__ __forceinline__ float unit_of(bool softmax, float largest_share) { return softmax ? 0x1p-18f * largest_share : 0x1p-20f; }
+__device__ __forceinline__ float near_of(float v, float unit) { return unit + 0x1p-22f * fabsf(v); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
     }
     // The values, -inf where there is none.  Equal logits and biases give equal bits, here and
     // where a value is made again.
-    const float per = rcp_fast(sum);
+    const float per = rcp_fast(sum), unit = unit_of(softmax, per);
     auto remake = [&](float x, int e, float top, float per) {
       if (!biased) return x;
       const float v = softmax ? __fmaf_rn(exp2_fast(__fmul_rn(__fsub_rn(x, top), kLog2e)), per, bias_at(e))
@@ -287,12 +287,12 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
       kept = real && rank < d.topk_group;
       if (biased) {
         const bool near = live && real && rank == d.topk_group - 1 && next > -INFINITY &&
-                          !(mark - next > 4.0f * near_of(mark, softmax));
+                          !(mark - next > 4.0f * near_of(mark, unit));
         uint32_t again = __ballot_sync(kAll, near);
         if (again) {
           // the experts that a group may count, up to 32, settle it in 64 bits (but for a softmax,
           // whose sum would take all of them)
-          const float v = pair && second > -INFINITY ? second : best, from = v <= FLT_MAX ? v - 4.0f * near_of(v, false) : v;
+          const float v = pair && second > -INFINITY ? second : best, from = v <= FLT_MAX ? v - 4.0f * near_of(v, unit) : v;
           uint32_t reach = 0;
 #pragma unroll
           for (int i = 0; i < V; ++i) reach |= value[i] > -INFINITY && value[i] >= from ? 1u << i : 0u;
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
     if (biased) {
       const uint2 next = l < d.k ? sorted[l + 1] : make_uint2(0u, kAll);
       const float v = __uint_as_float(it.x);
-      const bool near = next.y != kAll && !(v - __uint_as_float(next.x) > near_of(v, softmax));
+      const bool near = next.y != kAll && !(v - __uint_as_float(next.x) > near_of(v, unit));
       uint32_t again = __ballot_sync(kAll, near) & ~doubt;
       if (again | doubt) {
         while (again) {
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
           doubt |= its;
           if (softmax) continue;
           // the experts that may be among the k, up to 32
-          const float kth = __uint_as_float(sorted_all[which * M::kSortedLd + min(d.k, n) - 1].x), at_least = kth - near_of(kth, false);
+          const float kth = __uint_as_float(sorted_all[which * M::kSortedLd + min(d.k, n) - 1].x), at_least = kth - near_of(kth, unit);
           uint32_t may = 0;
           for (int i = 0; i < kPer; ++i) {
             const float x = value_of_expert(first, lane * kPer + i, 0.0f, 1.0f);
