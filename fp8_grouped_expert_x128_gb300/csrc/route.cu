@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
       } else if (biased || pair) {
         unsure = out && !(value_of(low) - value_of(out) > 4.0f * near_of(value_of(low), unit));
       }
-      if (unsure && whole && biased && !softmax) {
+      if (unsure && whole && biased) {
         // the experts that a group may count, up to a lane each, settle it in 64 bits
         const float v = value_of(pair && second ? second : best);
         const uint32_t from = best ? key_of(v <= FLT_MAX ? v - 4.0f * near_of(v, unit) : v) : 0xffffffffu;
@@ -268,7 +268,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
           for (int i = 0; i < VPL; ++i)
             if (key[i] >= from) sorted[at++] = e0 + i;
           __syncwarp();
-          kept = real && ((groups_exactly<DT>(d, row, lane < count ? sorted[lane] : 0, count) >> mine) & 1);
+          const int e = lane < count ? sorted[lane] : 0;
+          const uint32_t groups = softmax ? groups_exactly<DT, true>(d, row, e, count) : groups_exactly<DT, false>(d, row, e, count);
+          kept = real && ((groups >> mine) & 1);
           unsure = false;
           __syncwarp();
         }
@@ -342,10 +344,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
       const float v = value_of(me.x);
       if (__any_sync(kAll, judged && !(v - value_of(sorted[rank + 1]) > near_of(v, unit)))) {
         // where the k-th is clear of what stayed below the threshold, the listed experts settle
-        // it among themselves (but for a softmax, whose sum would take all of them)
+        // it among themselves
         const float kth = value_of(sorted[min(d.k, count) - 1]);
-        if (!softmax && few && (least == 1u || kth - value_of(least) > near_of(kth, unit)))
-          rank = rank_exactly<DT>(row, d.bias, me.y, count);
+        if (few && (least == 1u || kth - value_of(least) > near_of(kth, unit)))
+          rank = softmax ? rank_exactly<DT, true>(d, row, me.y, count) : rank_exactly<DT, false>(d, row, me.y, count);
         else
           unsure = true;
       }

@@ -164,25 +164,53 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// The rank of lane l < count's expert e (numbers rising with the lanes) by its sigmoid and
+// A logit's score in 64 bits, for a warp that has the token's row.  What a softmax needs is looked
+// for here and not handed over: few tokens come here, and all would keep it in registers.
+template <int DT, bool kSoftmax>
+struct ExactScore {
+  float top = -INFINITY;
+  double sum = 0.0;
+  __device__ __forceinline__ ExactScore(const void* row, int E) {
+    if constexpr (kSoftmax) {
+      const int lane = threadIdx.x & 31;
+      for (int e = lane; e < E; e += 32) top = fmaxf(top, load_logit<DT>(row, e));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+#pragma unroll 4
+      for (int e = lane; e < E; e += 32) {
+        const float z = load_logit<DT>(row, e);
+        sum += z > -INFINITY ? exp(static_cast<double>(z) - top) : 0.0;
+      }
+      sum = warp_sum(sum);
+    }
+  }
+  __device__ __forceinline__ double operator()(float z) const {
+    if constexpr (kSoftmax) return exp(static_cast<double>(z) - top) / sum;
+    return 1.0 / (1.0 + exp(-static_cast<double>(z)));
+  }
+};
+
+// The rank of lane l < count's expert e (numbers rising with the lanes) by its score and
 // bias in 64 bits.
-template <int DT>
-__device__ __noinline__ int rank_exactly(const void* row, const float* bias, int e, int count) {
+template <int DT, bool kSoftmax>
+__device__ __noinline__ int rank_exactly(const moe_route_desc& d, const void* row, int e, int count) {
   const int lane = threadIdx.x & 31;
+  const ExactScore<DT, kSoftmax> score(row, d.E);
   uint64_t key = 0;
-  if (lane < count) key = key_of(1.0 / (1.0 + exp(-static_cast<double>(load_logit<DT>(row, e)))) + __ldg(bias + e));
+  if (lane < count) key = key_of(score(load_logit<DT>(row, e)) + __ldg(d.bias + e));
   int rank = 0;
   for (int j = 0; j < count; ++j) rank += __shfl_sync(kAll, key, j) + (j < lane) > key;
   return rank;
 }
 
-// Which groups stay, as a mask, by their sigmoids and biases in 64 bits.  Lane l < count has
+// Which groups stay, as a mask, by their scores and biases in 64 bits.  Lane l < count has
 // expert e; among these are the experts that any group counts.
-template <int DT>
+template <int DT, bool kSoftmax>
 __device__ __noinline__ uint32_t groups_exactly(const moe_route_desc& d, const void* row, int e, int count) {
+  const ExactScore<DT, kSoftmax> score(row, d.E);
   const int lane = threadIdx.x & 31, size = d.E / d.n_group;
   uint64_t key = 0, a = 0, b = 0;
-  if (lane < count) key = key_of(1.0 / (1.0 + exp(-static_cast<double>(load_logit<DT>(row, e)))) + __ldg(d.bias + e));
+  if (lane < count) key = key_of(score(load_logit<DT>(row, e)) + __ldg(d.bias + e));
   const int g = lane < count ? e / size : -1;
   for (int j = 0; j < count; ++j) {
     const uint64_t k = __shfl_sync(kAll, key, j);

@@ -112,7 +112,7 @@ struct Many {
 // What bounds it is that pipe and the issue of instructions: 65536 tokens of 256 experts in 8
 // groups, fp32, take 33 us (2.2 TB/s), 12 with the rows' way through shared memory alone, 57 by a
 // warp a token.  Five CTAs an SM: four take 36 us, and six, with the fewer registers, 36.
-template <int DT, int V, int L>
+template <int DT, int V, int L, bool kSoftmax>
 __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __grid_constant__ ManyArgs a) {
   using M = Many<DT, V, L>;
   constexpr int kRun = M::kRun, kPer = V * L / 32;
@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
   uint16_t* number = reinterpret_cast<uint16_t*>(numbers + tok * M::kNumberLd);
   uint2* sorted = sorted_all + tok * M::kSortedLd;
   float* bias = reinterpret_cast<float*>(many_smem + kManyWarps * M::kWarpBytes);
-  const bool softmax = d.flags & MOE_ROUTE_SOFTMAX, pair = (d.flags & MOE_ROUTE_GROUP_PAIR) && d.n_group > 1;
+  constexpr bool softmax = kSoftmax;
+  const bool pair = (d.flags & MOE_ROUTE_GROUP_PAIR) && d.n_group > 1;
   const bool renorm = d.flags & MOE_ROUTE_RENORM, biased = d.bias != nullptr;
   const int stride = d.n_group > 1 ? d.E / d.n_group / V : 1;      // lanes of a group
   const int group = l / stride;
@@ -290,8 +291,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
                           !(mark - next > 4.0f * near_of(mark, unit));
         uint32_t again = __ballot_sync(kAll, near);
         if (again) {
-          // the experts that a group may count, up to 32, settle it in 64 bits (but for a softmax,
-          // whose sum would take all of them)
+          // the experts that a group may count, up to 32, settle it in 64 bits
           const float v = pair && second > -INFINITY ? second : best, from = v <= FLT_MAX ? v - 4.0f * near_of(v, unit) : v;
           uint32_t reach = 0;
 #pragma unroll
@@ -301,14 +301,16 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
             const int which = (__ffs(again) - 1) / L, n = __shfl_sync(kAll, all, which * L);
             const uint32_t its = ((1u << L) - 1) << which * L;
             again &= ~its;
-            if (softmax || n > 32) {
+            if (n > 32) {
               doubt |= its;
               continue;
             }
             if (tok == which)
               for (; reach; reach &= reach - 1) among[at++] = e0 + __ffs(reach) - 1;
             __syncwarp();
-            const uint32_t groups = groups_exactly<DT>(d, row_of(t0 + which), lane < n ? among[lane] : 0, n);
+            const char* row = row_of(t0 + which);
+            const int e = lane < n ? among[lane] : 0;
+            const uint32_t groups = groups_exactly<DT, kSoftmax>(d, row, e, n);
             if (tok == which) kept = real && ((groups >> group) & 1);
             __syncwarp();
           }
@@ -430,19 +432,20 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
           const uint32_t its = ((1u << L) - 1) << first;
           again &= ~its;
           doubt |= its;
-          if (softmax) continue;
           // the experts that may be among the k, up to 32
-          const float kth = __uint_as_float(sorted_all[which * M::kSortedLd + min(d.k, n) - 1].x), at_least = kth - near_of(kth, unit);
+          const float kth = __uint_as_float(sorted_all[which * M::kSortedLd + min(d.k, n) - 1].x), at_least = kth - near_of(kth, __shfl_sync(kAll, unit, first));
+          const float its_top = __shfl_sync(kAll, top, first), its_per = __shfl_sync(kAll, per, first);
           uint32_t may = 0;
           for (int i = 0; i < kPer; ++i) {
-            const float x = value_of_expert(first, lane * kPer + i, 0.0f, 1.0f);
+            const float x = value_of_expert(first, lane * kPer + i, its_top, its_per);
             may |= x > -INFINITY && !(x < at_least) ? 1u << i : 0u;
           }
           int all, at = lanes_before<32>(__popc(may), all), *among = reinterpret_cast<int*>(lists);
           if (all > 32) continue;
           for (; may; may &= may - 1) among[at++] = lane * kPer + __ffs(may) - 1;
           __syncwarp();
-          const int e = lane < all ? among[lane] : 0, rank = rank_exactly<DT>(row_of(t0 + which), d.bias, e, all);
+          const char* row = row_of(t0 + which);
+          const int e = lane < all ? among[lane] : 0, rank = rank_exactly<DT, kSoftmax>(d, row, e, all);
           if (lane < all && rank < d.k) sorted_all[which * M::kSortedLd + rank] = make_uint2(0u, e);
           __syncwarp();
           doubt &= ~its;
@@ -505,20 +508,25 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
 // Lanes of a token and experts of a lane, for E experts.
 int experts_of_lane(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : 32; }
 
-template <int DT, int V, int L>
+template <int DT, int V, int L, bool kSoftmax>
 int launch_many(const ManyArgs& a, cudaStream_t st) {
   using M = Many<DT, V, L>;
   const int64_t batch = kManyWarps * M::kTokens;
   const int64_t ctas = std::min<int64_t>((a.d.T + batch - 1) / batch, 5ll * num_sms());
-  return launch_pdl(route_many_kernel<DT, V, L>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kManyWarps), M::kSmem, st, a);
+  return launch_pdl(route_many_kernel<DT, V, L, kSoftmax>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kManyWarps), M::kSmem, st, a);
+}
+
+template <int DT, bool kSoftmax>
+int pick_many(const ManyArgs& a, cudaStream_t st) {
+  if (a.d.E <= 64) return launch_many<DT, 8, 8, kSoftmax>(a, st);
+  if (a.d.E <= 128) return launch_many<DT, 16, 8, kSoftmax>(a, st);
+  if (a.d.E <= 256) return launch_many<DT, 32, 8, kSoftmax>(a, st);
+  return launch_many<DT, 32, 16, kSoftmax>(a, st);
 }
 
 template <int DT>
 int pick_many(const ManyArgs& a, cudaStream_t st) {
-  if (a.d.E <= 64) return launch_many<DT, 8, 8>(a, st);
-  if (a.d.E <= 128) return launch_many<DT, 16, 8>(a, st);
-  if (a.d.E <= 256) return launch_many<DT, 32, 8>(a, st);
-  return launch_many<DT, 32, 16>(a, st);
+  return a.d.flags & MOE_ROUTE_SOFTMAX ? pick_many<DT, true>(a, st) : pick_many<DT, false>(a, st);
 }
 
 }  // namespace
@@ -527,7 +535,7 @@ bool is_for_route_many(const moe_route_desc& d) {
   const int64_t bytes = d.dtype == MOE_DTYPE_F32 ? 4 : 2;
   const int V = experts_of_lane(d.E), size = d.E / d.n_group;
   // Enough tokens for all warps, at this many a warp: 8192 tokens of 256 experts in groups take
-  // 9.9 us here and 10.2 by a warp a token, 4096 take 7.5 and 6.8; 4096 of 512 take 10.9 and 23.8.
+  // 9.3 us here and 10.2 by a warp a token, 4096 take 7.5 and 6.8; 4096 of 512 take 10.9 and 23.8.
   if (d.T < (d.E <= 256 ? 8192 : 4096) || d.E > 512 || d.k > kManyK) return false;
   // rows in pieces of 16 bytes
   if (reinterpret_cast<uintptr_t>(d.logits) % 16 || d.logits_ld * bytes % 16 || d.E * bytes % 16) return false;
