@@ -106,6 +106,21 @@ def test_values_that_fp32_cannot_tell_apart(lib):
     check(lib, wide, 8, soft, n_group=8, topk_group=4, flags=lib.MOE_ROUTE_SOFTMAX | lib.MOE_ROUTE_GROUP_PAIR)
 
 
+def test_near_values_of_a_softmax(lib):
+    """Shares and biases that come to nearly the same for a few experts, or two of each group: few and many tokens."""
+    T, E = 32, 256
+    wide = logits_of(T, E, seed=9)
+    wide[:] = wide[:1] + 1e-6 * logits_of(T, E, seed=10)
+    level = (0.5 - torch.softmax(wide[0].double(), 0)).float()
+    e = torch.arange(E, device="cuda")
+    for at in (e % 19 == 3, e % 32 < 2, e % 32 < 5, e < 20):
+        bias = torch.where(at, level, level - 0.25)
+        for flags in (lib.MOE_ROUTE_SOFTMAX, lib.MOE_ROUTE_SOFTMAX | lib.MOE_ROUTE_GROUP_PAIR | lib.MOE_ROUTE_RENORM):
+            for n in (T, MANY):
+                check(lib, wide, 8, bias, flags=flags, T=n)
+                check(lib, wide, 5, bias, n_group=8, topk_group=4, flags=flags, T=n)
+
+
 def test_infinite_biases(lib):
     """Groups whose experts are +inf rank before all others, in the order of their numbers."""
     z, inf = logits_of(20, 256, seed=6), float("inf")
