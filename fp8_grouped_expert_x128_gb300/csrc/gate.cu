@@ -29,7 +29,6 @@
 #include "gemm_common.cuh"
 #include "kv_common.cuh"
 
-
 namespace moe {
 namespace {
 

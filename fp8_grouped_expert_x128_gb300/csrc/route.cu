@@ -95,7 +95,6 @@ __device__ __noinline__ int select_slowly(uint32_t* key, int E, int most, uint2*
   return count;
 }
 
-
 // How many of the earlier lanes' things there are, and of all.
 __device__ __forceinline__ int lanes_before(int have, int& all) {
   const int lane = threadIdx.x & 31;
@@ -109,15 +108,15 @@ __device__ __forceinline__ int lanes_before(int have, int& all) {
   return upto - have;
 }
 
-// A warp routes one token after another, in fp32 as far as that decides: 3 us for a token, 5.3
-// for 2048 of 256 experts, where a token's chain of exchanges is what takes time.  More tokens
-// than there are warps at once are bound by the instructions (some 850 a token), and most of
-// these calls are for route_many.  Values become sortable keys once, and selection works
-// on few of them: the k + 1 largest of the lanes' maxima leave a threshold that at least k + 1
+// A warp routes one token after another, in fp32 as far as that decides: 3.1 us for a token,
+// 5.4 for 2048 of 256 experts, where a token's chain of exchanges is what takes time.  More
+// tokens than there are warps at once are bound by the instructions (some 850 a token), and most
+// of these calls are for route_many.  Values become sortable keys once, and selection works on
+// few of them: the k + 1 largest of the lanes' maxima leave a threshold that at least k + 1
 // experts reach and seldom many more.  These (32 at most) go to a lane each, in the order of
-// their numbers, which counts those in front of it.  Where two neighbours of that order, or
-// the last group that stays and the first that does not, lie too near, the token is decided
-// in 64 bits.
+// their numbers, which counts those in front of it.  Where two neighbours of that order, or the
+// last group that stays and the first that does not, lie too near, the token is decided in 64
+// bits.
 template <int DT, int VPL>
 __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ uint64_t route_smem[];

@@ -109,9 +109,10 @@ struct Many {
 // or three of them.  Neighbours of that order, or the last group that stays and the first that
 // does not, that lie too near each other are put in order in 64 bits, by the whole warp.
 //
-// What bounds it is that pipe and the issue of instructions: 65536 tokens of 256 experts in 8
-// groups, fp32, take 33 us (2.2 TB/s), 12 with the rows' way through shared memory alone, 57 by a
-// warp a token.  Five CTAs an SM: four take 36 us, and six, with the fewer registers, 36.
+// What bounds it is the pipe of comparisons and the issue of instructions: 65536 tokens of 256
+// experts in 8 groups, fp32, take 33 us (2.2 TB/s), 12 with the rows' way through shared memory
+// alone, 57 by a warp a token.  Five CTAs an SM: four take 36 us, and six, with the fewer
+// registers, 36.
 template <int DT, int V, int L, bool kSoftmax>
 __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __grid_constant__ ManyArgs a) {
   using M = Many<DT, V, L>;
