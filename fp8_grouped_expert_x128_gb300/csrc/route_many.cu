@@ -54,7 +54,7 @@ __device__ __forceinline__ void exchange4(float* v, int mask, float sign) {
     v[i + 1] = r.y;
   }
 }
-// The sign of a - b behind the bits of m: 1 where a < b.
+// The sign of a - b behind the bits of m: 1 where a < b (neither of them -0).
 __device__ __forceinline__ uint32_t below(uint32_t m, float a, float b) { return __funnelshift_l(__float_as_uint(__fsub_rn(a, b)), m, 1); }
 
 // How many of the earlier lanes' things of L there are, and of all L.
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
     // where a value is made again.
     const float per = rcp_fast(sum), unit = unit_of(softmax, per);
     auto remake = [&](float x, int e, float top, float per) {
-      if (!biased) return x;
+      if (!biased) return __fadd_rn(x, 0.0f);
       const float v = softmax ? __fmaf_rn(exp2_fast(__fmul_rn(__fsub_rn(x, top), kLog2e)), per, bias_at(e))
                               : __fadd_rn(rcp_fast(__fadd_rn(exp2_fast(__fmul_rn(x, -kLog2e)), 1.0f)), bias_at(e));
       return x > -INFINITY ? v : -INFINITY;
@@ -239,8 +239,13 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
         }
       }
     } else {
+      // logits as they are, but -0 as 0: the difference of the two has a sign
 #pragma unroll
-      for (int i = 0; i < V; ++i) value[i] = as_logit(z[i]);
+      for (int i = 0; i < V; i += 2) {
+        const float2 v = __fadd2_rn(make_float2(as_logit(z[i]), as_logit(z[i + 1])), make_float2(0.0f, 0.0f));
+        value[i] = v.x;
+        value[i + 1] = v.y;
+      }
     }
     // the maxima of the lane's runs
     float run[M::kRuns], best = -INFINITY, second = -INFINITY;
