@@ -355,16 +355,18 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       w.set(p_row(row), nullptr, static_cast<int>(d.vocab), -1);    // nothing is left of the target's distribution: all of it
       continue;
     }
-    target.hi = __fmul_rn(u, total.hi);
+    // (no sum passes what a u of 1 or more asks for, whatever rounding makes of sums added up in
+    // another order)
+    target.hi = u < 1.0f ? __fmul_rn(u, total.hi) : INFINITY;
     target.lo = __fmaf_rn(u, total.lo, __fmaf_rn(u, total.hi, -target.hi));
-    // the first warp whose sums pass the target, or the last that has some
+    // the first warp with weight whose sums pass the target, or the last that has some
     int first = -1, last = -1;
     Pair from;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < per) {
         const Pair next = i + 1 == per ? upto : plus(at, x[i]);
-        if (first < 0 && next.above(target)) {
+        if (first < 0 && x[i].hi > 0.0f && next.above(target)) {
           first = lane * per + i;
           from = at;
         }
@@ -392,8 +394,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
     }
   }
   if (any && owner == me) {
-    if (kMarked && !w.careful) {
-      // the part of the run between two marks, four lanes a mark
+    if (kMarked && !w.careful && !beyond) {
+      // the part of the run between two marks, four lanes a mark.  (Not for its last entry with
+      // weight: a weight that is small beside the run's does not show in the sums up to the marks.)
       __syncwarp();
       const int i = lane / 4;
       Pair upto;
@@ -403,9 +406,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       for (int o = 1; o < 4; o <<= 1) upto.add(Pair{__shfl_xor_sync(kAll, upto.hi, o), __shfl_xor_sync(kAll, upto.lo, o)});
       Pair ahead{__shfl_up_sync(kAll, upto.hi, 4), __shfl_up_sync(kAll, upto.lo, 4)};
       if (i == 0) ahead = Pair{};
-      const uint32_t over = __ballot_sync(kAll, !beyond && plus(before, upto).above(target)), some = __ballot_sync(kAll, upto.above(ahead));
+      const uint32_t over = __ballot_sync(kAll, plus(before, upto).above(target)), some = __ballot_sync(kAll, upto.above(ahead));
       const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
-      beyond |= over == 0;
+      beyond = over == 0;
       before.add(shfl(ahead, at));
       k0 = min(k0 + at / 4 * every * kRound, k1);
       k1 = min(k0 + every * kRound, k1);
