@@ -119,7 +119,8 @@ struct Weights {
   int shift;          // entries of vector 0 in front of the row
   int whole0, whole1; // vectors that lie in the row whole
   bool q_wide;        // q's vectors lie like p's
-  bool careful;       // entries that are not finite are looked for (else they show as a sum that is not)
+  float careful;      // 0: as they come.  Else entries that are not finite are looked for (they show as a
+                      // sum that is not), and the others count this many times
 
   __device__ __forceinline__ void set(const char* p_row, const char* q_row, int v, int wo) {
     p = p_row;
@@ -130,7 +131,7 @@ struct Weights {
     whole0 = shift > 0;
     whole1 = (shift + vocab) / kVec;
     q_wide = ((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15) == 0;
-    careful = false;
+    careful = 0.0f;
   }
   __device__ __forceinline__ int vectors() const { return (shift + vocab + kVec - 1) / kVec; }
   static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kVec]) {
@@ -167,14 +168,16 @@ struct Weights {
   }
   __device__ __forceinline__ Pair entry(int j) const {
     if (j < 0 || j >= vocab || j == without) return Pair{};
-    return weight(prob_at<DT>(p, j), q ? prob_at<DT>(q, j) : 0.0f);
+    const Pair v = weight(prob_at<DT>(p, j), q ? prob_at<DT>(q, j) : 0.0f);
+    const float times = careful > 0.0f ? careful : 1.0f;      // a power of two
+    return {v.hi * times, v.lo * times};
   }
   // The sum of vectors from, from + by, .. below to.  q counts as min(q, p): no comparison is
   // left, and what is not finite shows in the sum.  marks: the sums after `every`, 2 every,
   // .. rounds of loads, 32 places apart.
   template <bool kMarked>
   __device__ __forceinline__ Pair sum(int from, int to, int by, Pair* marks = nullptr, int every = 0) const {
-    if (careful) return sum_carefully(from, to, by);
+    if (careful > 0.0f) return sum_carefully(from, to, by);
     Pairs acc[2];
     auto round = [&](int k) {
       uint4 a[kAhead], b[kAhead];
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
   Pair before, target, own;
   int owner = -1;
   bool any = false, beyond = false;
-  for (int pass = 0; pass < 4; ++pass) {
+  for (int pass = 0; pass < 6; ++pass) {      // at most: the residual careful and empty, p careful and too large
     own = w.template sum<kMarked>(f0, t0, kParted ? 1 : 32, &marks[kMarked ? warp : 0][0][lane], every);
     Pair sum = own;
 #pragma unroll
@@ -346,8 +349,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       if (i < per) mine.add(x[i]);
     Pair at, upto = warp_prefix(mine, at);
     const Pair total = shfl(upto, 31);
-    if (!(fabsf(total.hi) <= FLT_MAX) && !w.careful) {       // infinities among the entries: without them
-      w.careful = true;
+    // Infinities among the entries: without them.  Sums of finite ones that are past fp32, or so small
+    // that a random number's part of them has bits below fp32's last: of their multiples.
+    if (!(total.hi >= 0x1p-90f && total.hi <= FLT_MAX) && total.hi != 0.0f && (w.careful == 0.0f || w.careful == 1.0f)) {
+      const bool small = total.hi > 0.0f && total.hi < 1.0f;
+      w.careful = small ? 0x1p64f : w.careful == 0.0f ? 1.0f : 0x1p-30f;      // (2^24 entries below 2^128)
       continue;
     }
     any = total.hi > 0.0f;
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
     }
   }
   if (any && owner == me) {
-    if (kMarked && !w.careful && !beyond) {
+    if (kMarked && w.careful == 0.0f && !beyond) {
       // the part of the run between two marks, four lanes a mark.  (Not for its last entry with
       // weight: a weight that is small beside the run's does not show in the sums up to the marks.)
       __syncwarp();
