@@ -95,6 +95,13 @@ __device__ __noinline__ int select_slowly(uint32_t* key, int E, int most, uint2*
   return count;
 }
 
+// A lane's share of the chosen scores, where fp32 has few bits of these or none.
+template <int DT>
+__device__ __noinline__ float small_share(const void* row, int e, bool chosen) {
+  const float x = chosen ? load_logit<DT>(row, e) : -INFINITY, s = small_score(x, warp_max(x)), all = warp_sum(s);
+  return all > 0.0f ? __fdividef(s, all) : 0.0f;
+}
+
 // How many of the earlier lanes' things there are, and of all.
 __device__ __forceinline__ int lanes_before(int have, int& all) {
   const int lane = threadIdx.x & 31;
@@ -371,8 +378,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
       s = __fdividef(x < 0.0f ? u : 1.0f, 1.0f + u);
     }
     if (renorm) {
-      const float all = warp_sum(s), up = all < 0x1p-60f ? 0x1p100f : 1.0f;
-      s = all > 0.0f ? __fdividef(s * up, all * up) : 0.0f;
+      const float all = warp_sum(s);
+      s = softmax || all >= 0x1p-60f ? __fdividef(s, all) : small_share<DT>(row, me.y, chosen);
     }
     int32_t* ids = d.topk_ids + t * d.ids_ld;
     float* weights = d.topk_w + t * d.w_ld;

@@ -164,6 +164,10 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// A sigmoid far below 1 is its exponential: such a score, as a part of that of the largest of them.
+// Past exp(709.78), which is past 64 bits, it is 0.
+__device__ __forceinline__ float small_score(float x, float largest) { return x >= -709.78f ? expf(x - largest) : 0.0f; }
+
 // A logit's score in 64 bits, for a warp that has the token's row.  What a softmax needs is looked
 // for here and not handed over: few tokens come here, and all would keep it in registers.
 template <int DT, bool kSoftmax>

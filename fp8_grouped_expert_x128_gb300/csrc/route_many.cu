@@ -491,8 +491,22 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
       float all = s;
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
-      const float up = all < 0x1p-60f ? 0x1p100f : 1.0f;
-      s = all > 0.0f ? __fdividef(s * up, all * up) : 0.0f;
+      if constexpr (!softmax) {
+        const bool small = all < 0x1p-60f;     // of which fp32 may have few bits, or none
+        if (__any_sync(kAll, small && chosen)) {
+          float base = x, sum_of = 0.0f;
+#pragma unroll
+          for (int o = L / 2; o > 0; o >>= 1) base = fmaxf(base, __shfl_xor_sync(kAll, base, o));
+          const float share = sum_of = small_score(x, base);
+#pragma unroll
+          for (int o = L / 2; o > 0; o >>= 1) sum_of += __shfl_xor_sync(kAll, sum_of, o);
+          if (small) {
+            s = share;
+            all = fmaxf(sum_of, FLT_MIN);
+          }
+        }
+      }
+      s = __fdividef(s, all);
     }
     if (l < d.k && t < T) {
       d.topk_ids[t * d.ids_ld + l] = expert;

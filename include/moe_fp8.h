@@ -639,7 +639,8 @@ int moe_gate(const moe_gate_desc *desc, void *stream);
  *            stay open; one without open experts comes last.
  *   topk_ids[t, 0..k)  the open experts of largest value, falling
  *   topk_w[t, j]       scale * score of topk_ids[t, j], with MOE_ROUTE_RENORM divided
- *                      by the sum of the k scores first
+ *                      by the sum of the k scores first (0 where the scores are 0 in 64
+ *                      bits: sigmoids of logits below -709.78)
  * Among equal values (and groups) the lowest number comes first.  Values are compared
  * as 64-bit arithmetic has them: what fp32 cannot tell apart is computed again.
  * Where fewer than k experts are open, the remaining entries get id -1 and weight 0
