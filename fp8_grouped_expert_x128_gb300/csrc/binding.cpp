@@ -91,6 +91,16 @@ PyObject* quick(Py_ssize_t n, Py_ssize_t wanted, F call) {
   return PyLong_FromLong(rc);
 }
 
+// The call itself, in which other Python threads run: a launch waits where the stream's queue is full,
+// maybe behind a function of the host that needs the interpreter.
+template <class Desc>
+int launch(int (*f)(const Desc*, void*), const Desc& d, void* stream) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int rc = f(&d, stream);
+  PyEval_RestoreThread(state);
+  return rc;
+}
+
 // gate(x, w, logits, err)
 PyObject* gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return quick(n, 4, [&] {
@@ -108,7 +118,7 @@ PyObject* gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.T = T;
     d.E = static_cast<int32_t>(E);
     d.H = static_cast<int32_t>(H);
-    return g_gate(&d, c.stream());
+    return launch(g_gate, d, c.stream());
   });
 }
 
@@ -136,7 +146,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) throw NotQuick{};
     d.scale = static_cast<float>(scale);
     d.flags = number(a[8]);
-    return g_route(&d, c.stream());
+    return launch(g_route, d, c.stream());
   });
 }
 
@@ -170,7 +180,7 @@ PyObject* kv_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.err = c.flat<int32_t>(a[13], 1, at::kInt);
     d.batch = static_cast<int32_t>(batch);
     d.max_pages = static_cast<int32_t>(max_pages);
-    return g_pages(&d, c.stream());
+    return launch(g_pages, d, c.stream());
   });
 }
 
@@ -200,7 +210,7 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.err = c.flat<int32_t>(a[11], 1, at::kInt);
     d.batch = static_cast<int32_t>(batch);
     d.max_out = static_cast<int32_t>(max_out);
-    return g_verify(&d, c.stream());
+    return launch(g_verify, d, c.stream());
   });
 }
 
