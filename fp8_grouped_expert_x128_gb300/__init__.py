@@ -13,7 +13,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+import re
 import struct
+import sys
 
 import torch
 
@@ -671,10 +673,20 @@ _current_device = torch._C._cuda_getDevice
 
 # The quick way (csrc/binding.cpp): 0 or the library's status, or 1 where a call is to be
 # looked at here.  It knows the current stream only.
+def _is_ours(native):
+    """Whether it was built for this torch, this Python and these descriptors."""
+    release = [int(n) for n in re.findall(r"\d+", torch.__version__)[:3]]
+    here = (*release, *sys.version_info[:2], *(ctypes.sizeof(d) for d in (moe_gate_desc, moe_route_desc, moe_kv_pages_desc, moe_verify_desc)))
+    return hasattr(native, "made_for") and native.made_for() == here
+
+
 try:
     from . import _binding as _native
-    _native.connect(*(ctypes.cast(getattr(_lib, _name), ctypes.c_void_p).value
-                      for _name in ("moe_gate", "moe_route", "moe_kv_pages", "moe_verify_drafts")))
+    if _is_ours(_native):
+        _native.connect(*(ctypes.cast(getattr(_lib, _name), ctypes.c_void_p).value
+                          for _name in ("moe_gate", "moe_route", "moe_kv_pages", "moe_verify_drafts")))
+    else:
+        _native = None
 except ImportError:
     _native = None
 

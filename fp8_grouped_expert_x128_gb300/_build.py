@@ -12,6 +12,7 @@ import argparse
 import concurrent.futures as cf
 import os
 import shutil
+import importlib.metadata
 import importlib.util
 import subprocess
 import sys
@@ -56,27 +57,45 @@ def _stale(out: str, ins: list[str]) -> bool:
     return any(os.path.getmtime(i) > t for i in ins)
 
 
+def _installed(name: str) -> str:
+    try:
+        return importlib.metadata.version(name)
+    except importlib.metadata.PackageNotFoundError:
+        return ""
+
+
 def _build_binding(cuda: str, force: bool) -> None:
-    """_binding.so, if its headers are there."""
-    src = os.path.join(CSRC, "binding.cpp")
-    if not force and not _stale(BINDING, [src, os.path.join(INCLUDE, "moe_fp8.h"), os.path.abspath(__file__)]):
-        return
+    """_binding.so, if its headers are there.  It holds torch's and Python's layouts beside the library's, so one of
+    other versions, or of an older source, is taken away before it is built again."""
+    src, stamp = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.txt")
     spec = importlib.util.find_spec("torch")
     gxx = os.environ.get("CXX") or shutil.which("g++")
-    if spec is None or gxx is None:
+    cmd, tmp = [], BINDING + ".tmp"
+    if spec is not None and gxx is not None:
+        torch_dir = list(spec.submodule_search_locations)[0]
+        cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", tmp, "-I", os.path.join(torch_dir, "include"),
+               "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+               "-I", os.path.join(cuda, "include"), "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+               "-Wl,-rpath," + os.path.join(torch_dir, "lib")]
+    made_with = "\n".join([" ".join(cmd), "torch " + _installed("torch"), "python " + sys.version, ""])
+    was = ""
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            was = f.read()
+    if not force and was == made_with and not _stale(BINDING, [src, os.path.join(INCLUDE, "moe_fp8.h"), os.path.abspath(__file__)]):
+        return
+    if os.path.exists(BINDING):
+        os.remove(BINDING)
+    if not cmd:
         print("_binding.so is not built: it takes torch and g++", file=sys.stderr)
         return
-    torch_dir = list(spec.submodule_search_locations)[0]
-    tmp = BINDING + ".tmp"
-    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", tmp, "-I", os.path.join(torch_dir, "include"),
-           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
-           "-I", os.path.join(cuda, "include"), "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
-           "-Wl,-rpath," + os.path.join(torch_dir, "lib")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         print(f"_binding.so is not built:\n{' '.join(cmd)}\n{r.stderr[-2000:]}", file=sys.stderr)
         return
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(made_with)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:

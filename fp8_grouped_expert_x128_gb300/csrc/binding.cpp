@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "../../include/moe_fp8.h"
 
@@ -235,9 +236,16 @@ PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// made_for(): the releases of torch and Python whose layouts this holds, and the descriptors' sizes
+PyObject* made_for(PyObject*, PyObject* const*, Py_ssize_t) {
+  return Py_BuildValue("(iiiiinnnn)", TORCH_VERSION_MAJOR, TORCH_VERSION_MINOR, TORCH_VERSION_PATCH, PY_MAJOR_VERSION, PY_MINOR_VERSION,
+                       static_cast<Py_ssize_t>(sizeof(moe_gate_desc)), static_cast<Py_ssize_t>(sizeof(moe_route_desc)),
+                       static_cast<Py_ssize_t>(sizeof(moe_kv_pages_desc)), static_cast<Py_ssize_t>(sizeof(moe_verify_desc)));
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr
 PyMethodDef methods[] = {{"connect", FAST(connect)}, {"gate", FAST(gate)},     {"route", FAST(route)},
-                         {"kv_pages", FAST(kv_pages)}, {"verify", FAST(verify)}, {nullptr, nullptr, 0, nullptr}};
+                         {"kv_pages", FAST(kv_pages)}, {"verify", FAST(verify)}, {"made_for", FAST(made_for)}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
