@@ -191,9 +191,10 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const __grid_co
   const int32_t step = static_cast<int32_t>(gridDim.x) * kPagesThreads;
   const int32_t first = static_cast<int32_t>(blockIdx.x) * kPagesThreads + threadIdx.x;
   auto entry = [&](int b, int32_t j) { return d.page_table + b * d.table_ld + j; };
-  // The i-th page given back, and the i-th page taken.  Read from the L2: other CTAs write other
-  // words of these lines, and what is launched behind this may be on an SM before they have, where
-  // it should not find the lines as they were (1024 prompts 9.4 -> 10 us).
+  // The i-th page given back, and the i-th page taken.  Read from the L2, as a precaution: other CTAs
+  // write other words of these lines, while the next launch may be on an SM already (1024 prompts 9.4
+  // -> 10 us).  The wait in front makes what was written before visible, and lengths and counts, which
+  // share lines in the same way and are read through the L1, were never found as they had been.
   auto given = [&](int32_t i) {
     const int b = find_last(back0, B, i);
     return __ldcg(entry(b, need_of[b] + i - back0[b]));
