@@ -102,6 +102,11 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// A barrier of the warps that know tensor memory (0 is all threads').
+constexpr int kTmemBarrier = 1;
+__device__ __forceinline__ void named_sync(int id, int threads) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void named_arrive(int id, int threads) { asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
 // A CTA's place: `rank` in its cluster of splits (x 2 in pairs) CTAs; in a pair the even
 // CTA issues the MMAs of both (M = 256: its own 128 tokens and the odd one's), with half of
 // the gate's rows in each one's shared memory.  The copies of both complete on the even
@@ -251,6 +256,14 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
         mbar_wait_bounded(empty0 + 8 * j, s == 0 ? ph ^ 1 : ph, &dummy, nullptr, p.wait_limit_ns / 10);
       }
     }
+    __syncwarp();
+    if constexpr (!kPair) {
+      // Given back before the cluster is waited for: a small CTA finds room beside a GEMM's, which may
+      // want all of the SM's tensor memory while the cluster's other CTAs want some of another SM's.
+      named_sync(kTmemBarrier, 32 + 32 * G::kEpi);
+      tc_fence_after();
+      tmem_dealloc(tmem, G::kTmem);
+    }
   } else {
     const int q = warp & 3, g = (warp - 2) >> 2;
     float2 acc[G::kPer / 2];
@@ -287,6 +300,10 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
       if (lane == 0) {
         if constexpr (kPair) mbar_arrive_cluster(tempty + 8 * b); else mbar_arrive(tempty + 8 * b);
       }
+    }
+    if constexpr (!kPair) {
+      tc_fence_before();
+      named_arrive(kTmemBarrier, 32 + 32 * G::kEpi);
     }
     // The part goes to shared memory, over the ring: with the last accumulator full every
     // copy has landed and every MMA has read its stage.
@@ -341,10 +358,12 @@ __global__ void __launch_bounds__(Gate<BN, kPair>::kThreadCount, 1)
   // done with it.  What they read has been stored by now, so no order of memory is asked for,
   // which would have each CTA wait for its stores.
   if (kPair || p.splits > 1) cluster_sync_relaxed();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    if constexpr (kPair) tmem_dealloc_pair(tmem, G::kTmem); else tmem_dealloc(tmem, G::kTmem);
+  if constexpr (kPair) {
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after();
+      tmem_dealloc_pair(tmem, G::kTmem);
+    }
   }
 }
 
