@@ -5,16 +5,19 @@
 // A skinny product: with few tokens it reads the gate (3.7 MB for 256 experts of
 // hidden 7168) and should take as long as launching it; with many it reads the
 // tokens, 256 multiply-adds a value, which is where GB300's tensor cores and its
-// memory take equally long.  So one kernel on the tensor cores (tcgen05, 128 tokens
-// by BN experts a CTA) whose tile and split follow the number of tokens:
+// memory take equally long.  Up to 16 tokens are multiplied without the tensor cores, a
+// CTA for one, two or four experts (gate_few_kernel).  More go through one kernel on the tensor cores
+// (gate_kernel: tcgen05, 128 tokens by BN experts a CTA) whose tile and split follow
+// their number:
 //
-//  * many tokens: BN = 256, so that a token's row is read once for 256 experts;
-//  * few: the hidden dimension is split over a cluster of up to 8 CTAs, and then the
+//  * many tokens: BN = 256 in pairs of CTAs, so that a token's row is read once for 256
+//    experts and a gate's row once for 256 tokens;
+//  * fewer: the hidden dimension is split over a cluster of up to 8 CTAs, and then the
 //    experts over narrower tiles, until there is a CTA for every SM.  The cluster
 //    adds its parts through distributed shared memory, in the order of the ranks.
 //
-// Warp roles: one TMA producer (ring of stages of 64 columns, 128-byte swizzle), one
-// MMA issuer, and epilogue warps, four for every 64 experts.  Precision: the tensor
+// Warp roles: one TMA producer (ring of stages of 64 columns, of 128 where BN is up to 128;
+// 128-byte swizzle), one MMA issuer, and epilogue warps, four for every 64 experts.  Precision: the tensor
 // cores cut what they add to a running sum, some 2^-24 of it a step, always towards
 // zero; over 448 steps (hidden 7168) that is more than the logits of a router may be
 // off.  So a sum runs over 512 columns only (32 steps; kRun), into one of two
@@ -22,8 +25,10 @@
 // registers while the next 512 run.
 //
 // 16384 tokens of hidden 7168 by 256 experts take 50 us (5.1 TB/s, 1.2 PFLOP/s): bound by
-// the copies into the SMs.  333 tokens of hidden 2040 by 60 take 4.1, one token by 256 2.0:
-// launch, a round of loads, a cluster barrier.
+// the copies into the SMs, and so are 256 (7.1 us), 512 (8.5), 1024 (10.8) and 2048 tokens (13.4)
+// of it, whose narrower tiles bring each gate row into an SM once for every 128 tokens.  333 tokens
+// of hidden 2040 by 60 take 4.1: launch, copies, a cluster barrier; one token by 256 2.0: launch and
+// a round of loads.
 #include <algorithm>
 
 #include "gemm_common.cuh"
@@ -455,7 +460,8 @@ size_t gate_smem(int bn, bool pair, int box_rows, int stages) {
 
 // Estimated clock cycles of the choices, the least of them: a CTA takes in some 45 bytes a
 // cycle, 1500 cycles after it asked, multiplies 128 x bn x 64 in 2 bn, and costs a few
-// thousand to start and end.  Swept against every choice (17 to 6000 tokens; 8, 64, 160, 256
+// thousand to start and end.  Two CTAs share an SM where their shared memory lets them: so it
+// counts for every tile, although from BN = 128 on their registers (146 x 320, 96 x 576) never do.  Swept against every choice (17 to 6000 tokens; 8, 64, 160, 256
 // and 512 experts, 70 sizes): the one taken is within 5% of the fastest at 59 of them, 26%
 // slower at worst (700 tokens by 512 experts, 11.5 us for 9.1).
 GatePlan plan_gate(int64_t T, int E, int H, int box_rows, int sms) {
@@ -472,7 +478,7 @@ GatePlan plan_gate(int64_t T, int E, int H, int box_rows, int sms) {
         const int sub = bn <= 128 ? 2 : 1;
         const double stage = sub * (box_rows + (pair ? bn / 2 : bn)) * 128.0;
         const int n = 2 / sub * ((blocks + splits - 1) / splits);
-        for (const double room_for : {98304.0, 196608.0}) {       // two CTAs on an SM, or one
+        for (const double room_for : {98304.0, 196608.0}) {       // rings of which two fit an SM, or one
           const int stages = std::max(1, std::min({kMaxStages, static_cast<int>(room_for / stage), n}));
           const size_t smem = gate_smem(bn, pair, box_rows, stages);
           if (smem > kMaxSmemPerBlock) continue;
@@ -495,7 +501,7 @@ GatePlan plan_gate(int64_t T, int E, int H, int box_rows, int sms) {
 }
 
 template <int BN, bool kPair, bool F16>
-int launch_gate(const moe_gate_desc& d, const GatePlan& plan, const CUtensorMap& x, const CUtensorMap& w, const GateArgs& p, cudaStream_t st) {
+int launch_gate(const GatePlan& plan, const CUtensorMap& x, const CUtensorMap& w, const GateArgs& p, cudaStream_t st) {
   using G = Gate<BN, kPair>;
   if (int rc = prepare_kernel(gate_kernel<BN, kPair, F16>, plan.smem, false)) return rc;
   cudaLaunchConfig_t cfg = {};
@@ -528,13 +534,13 @@ int run_gate(const moe_gate_desc& d, cudaStream_t st) {
   CUtensorMap x, w;
   if (int rc = make_tmap_b16_sw128(&x, d.x, d.T, d.H, 2 * d.x_ld, box_rows)) return rc;
   if (int rc = make_tmap_b16_sw128(&w, d.w, d.E, d.H, 2 * d.w_ld, plan.pair ? plan.bn / 2 : plan.bn)) return rc;
-  if (plan.pair) return launch_gate<256, true, F16>(d, plan, x, w, p, st);
+  if (plan.pair) return launch_gate<256, true, F16>(plan, x, w, p, st);
   switch (plan.bn) {
-    case 256: return launch_gate<256, false, F16>(d, plan, x, w, p, st);
-    case 128: return launch_gate<128, false, F16>(d, plan, x, w, p, st);
-    case 64: return launch_gate<64, false, F16>(d, plan, x, w, p, st);
-    case 32: return launch_gate<32, false, F16>(d, plan, x, w, p, st);
-    default: return launch_gate<16, false, F16>(d, plan, x, w, p, st);
+    case 256: return launch_gate<256, false, F16>(plan, x, w, p, st);
+    case 128: return launch_gate<128, false, F16>(plan, x, w, p, st);
+    case 64: return launch_gate<64, false, F16>(plan, x, w, p, st);
+    case 32: return launch_gate<32, false, F16>(plan, x, w, p, st);
+    default: return launch_gate<16, false, F16>(plan, x, w, p, st);
   }
 }
 

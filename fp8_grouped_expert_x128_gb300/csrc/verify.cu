@@ -10,7 +10,8 @@
 //
 // 256 sequences of 128000 fp32 entries: 39 us, of which the rows take 32 (6.4 TB/s); the
 // exchange (some 5) and the search (2 to 3) come after the rows, as all CTAs go through
-// their phases in step.  One sequence: 6 us, a chain of loads that wait on one another.
+// their phases in step.  16 sequences 9.4, 64 15.2, 128 22.4: tests, rows, exchange and search add up.
+// One sequence: 6 us, a chain of loads that wait on one another.
 //
 // Exactness: a token's borders may lie 1e-9 of the total apart, so sums are those of
 // 64-bit arithmetic.  GB300 has few 64-bit units (a dependent addition takes 61 cycles,
