@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? 8 : 2) route_kern
     }
     if (renorm) {
       const float all = warp_sum(s);
-      s = softmax || all >= 0x1p-60f ? __fdividef(s, all) : small_share<DT>(row, me.y, chosen);
+      s = softmax || all >= 0x1p-30f ? __fdividef(s, all) : small_share<DT>(row, me.y, chosen);
     }
     int32_t* ids = d.topk_ids + t * d.ids_ld;
     float* weights = d.topk_w + t * d.w_ld;

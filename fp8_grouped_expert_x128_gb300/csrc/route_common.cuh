@@ -164,7 +164,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// A sigmoid far below 1 is its exponential: such a score, as a part of that of the largest of them.
+// A sigmoid below 2^-30 is its exponential in fp32: such a score, as a part of that of the largest of them.
 // Past exp(709.78), which is past 64 bits, it is 0.
 __device__ __forceinline__ float small_score(float x, float largest) { return x >= -709.78f ? expf(x - largest) : 0.0f; }
 

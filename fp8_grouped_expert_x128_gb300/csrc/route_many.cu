@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 5) route_many_kernel(const __
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
       if constexpr (!softmax) {
-        const bool small = all < 0x1p-60f;     // of which fp32 may have few bits, or none
+        const bool small = all < 0x1p-30f;     // of which fp32 may have few bits, or none
         if (__any_sync(kAll, small && chosen)) {
           float base = x, sum_of = 0.0f;
 #pragma unroll
